@@ -26,7 +26,8 @@ CONFIG_FIELDS = ("path", "block_size", "outputs_per_block", "k_unroll", "vector_
 EXPORTED = ("skinny_addmm_bf16", "skinny_select_config", "skinny_addmm_bf16_with_config",
             "skinny_addmm_bf16_acc_f32", "skinny_addmm_bf16_shard", "skinny_addmm_bf16_shard_acc_f32",
             "skinny_kbit_gemv_bf16", "skinny_kbit_gemv_bf16_acc_f32", "skinny_kda_verify_bf16",
-            "skinny_num_configs", "skinny_get_config",
+            "skinny_latent_append_bf16", "skinny_latent_decode_bf16", "skinny_latent_prefill_bf16",
+            "skinny_latent_decode_workspace", "skinny_latent_prefill_workspace", "skinny_num_configs", "skinny_get_config",
             "skinny_config_resources", "skinny_status_string", "skinny_last_hip_error",
             "skinny_version", "skinny_probe_null", "skinny_probe_read", "skinny_probe_copy",
             "skinny_probe_read_rows", "skinny_probe_spin", "skinny_config_kernel_name")
@@ -51,6 +52,34 @@ class SkinnyKdaArgs(ctypes.Structure):
                                                 "ring_k", "ring_g", "ring_beta", "out")]
                 + [(f, ctypes.c_int64) for f in ("B", "T", "H", "HV", "K", "V", "lines", "slots", "ring_len")]
                 + [("scale", ctypes.c_float)])
+
+
+def _args(pointers, sizes, tail):
+    return ([(f, ctypes.c_void_p) for f in pointers.split()] + [(f, ctypes.c_int64) for f in sizes.split()] + tail)
+
+
+class SkinnyLatentAppendArgs(ctypes.Structure):
+    """skinny_latent_append_args of include/skinny.h."""
+    _fields_ = _args("kv cache slots positions inv_freq norm_weight q q_out",
+                     "kv_stride cache_page_stride cache_row_stride q_row_stride q_head_stride q_out_row_stride "
+                     "q_out_head_stride n heads pages page latent rope",
+                     [("eps", ctypes.c_float), ("interleaved", ctypes.c_int32)])
+
+
+class SkinnyLatentDecodeArgs(ctypes.Structure):
+    """skinny_latent_decode_args of include/skinny.h."""
+    _fields_ = _args("q cache table lens out lse workspace",
+                     "workspace_bytes q_row_stride q_head_stride cache_page_stride cache_row_stride table_stride "
+                     "out_row_stride out_head_stride batch tokens heads pages page max_pages latent rope",
+                     [("scale", ctypes.c_float)])
+
+
+class SkinnyLatentPrefillArgs(ctypes.Structure):
+    """skinny_latent_prefill_args of include/skinny.h."""
+    _fields_ = _args("q k v k_rot cu_q cu_k out lse workspace",
+                     "workspace_bytes q_row_stride q_head_stride k_row_stride k_head_stride v_row_stride "
+                     "v_head_stride k_rot_stride out_row_stride out_head_stride nq nk batch heads head_dim rope",
+                     [("scale", ctypes.c_float), ("causal", ctypes.c_int32)])
 
 
 class SkinnyError(RuntimeError):
@@ -92,6 +121,11 @@ def lib() -> ctypes.CDLL:
     L.skinny_kbit_gemv_bf16.argtypes = [vp, vp, vp, vp, ctypes.c_int32, vp, vp, i64, i64, i64, vp]
     L.skinny_kbit_gemv_bf16_acc_f32.argtypes = [vp, vp, vp, vp, ctypes.c_int32, vp, vp, i64, i64, i64, vp]
     L.skinny_kda_verify_bf16.argtypes = [ctypes.POINTER(SkinnyKdaArgs), vp]
+    L.skinny_latent_append_bf16.argtypes = [ctypes.POINTER(SkinnyLatentAppendArgs), vp]
+    L.skinny_latent_decode_bf16.argtypes = [ctypes.POINTER(SkinnyLatentDecodeArgs), vp]
+    L.skinny_latent_prefill_bf16.argtypes = [ctypes.POINTER(SkinnyLatentPrefillArgs), vp]
+    L.skinny_latent_decode_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    L.skinny_latent_prefill_workspace.argtypes = [i64, i64, i64, i64, ctypes.POINTER(i64)]
     L.skinny_select_config.argtypes = [i64, i64, i64, cfgp]
     L.skinny_get_config.argtypes = [ctypes.c_int32, cfgp]
     L.skinny_config_resources.argtypes = [cfgp, ctypes.POINTER(SkinnyResources)]
@@ -111,7 +145,8 @@ def lib() -> ctypes.CDLL:
     for f in ("skinny_addmm_bf16", "skinny_addmm_bf16_with_config", "skinny_addmm_bf16_acc_f32",
               "skinny_addmm_bf16_shard", "skinny_addmm_bf16_shard_acc_f32",
               "skinny_kbit_gemv_bf16", "skinny_kbit_gemv_bf16_acc_f32", "skinny_kda_verify_bf16",
-              "skinny_select_config", "skinny_get_config", "skinny_config_resources",
+              "skinny_latent_append_bf16", "skinny_latent_decode_bf16", "skinny_latent_prefill_bf16",
+              "skinny_latent_decode_workspace", "skinny_latent_prefill_workspace", "skinny_select_config", "skinny_get_config", "skinny_config_resources",
               "skinny_num_configs", "skinny_last_hip_error"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L

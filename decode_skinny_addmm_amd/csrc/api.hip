@@ -4,7 +4,10 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <atomic>
 #include <climits>
+#include <cmath>
+#include <initializer_list>
 #include <vector>
 
 #include "common.hpp"
@@ -262,10 +265,170 @@ skinny_status run_kda(const skinny_kda_args *a, void *stream) {
     return SKINNY_OK;
 }
 
+// ---- latent attention --------------------------------------------------------------------
+
+constexpr int64_t kMaxStride = (int64_t)1 << 40;         // keeps every offset inside 64 bits
+
+// A row stride of an extent: unused if the extent is at most 1, else positive and whole vectors.
+skinny_status check_stride(int64_t stride, int64_t extent, int64_t least) {
+    if (extent <= 1) return SKINNY_OK;
+    if (stride < least || stride > kMaxStride) return SKINNY_EINVAL;
+    return stride % 8 ? SKINNY_EALIGN : SKINNY_OK;
+}
+
+skinny_status first_bad(std::initializer_list<skinny_status> all) {
+    for (const skinny_status s : all)
+        if (s != SKINNY_OK) return s;
+    return SKINNY_OK;
+}
+
+// Compute units of the current device, 0 on an error (left in g_last_hip_error). Read once a
+// device: the workspace size and the launch of a call have to agree on it.
+int device_cus() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err == hipSuccess && dev >= 0 && dev < 64) {
+        n = known[dev].load(std::memory_order_relaxed);
+        if (n) return n;
+        err = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+        if (err == hipSuccess && n > 0) {
+            known[dev].store(n, std::memory_order_relaxed);
+            return n;
+        }
+    }
+    g_last_hip_error = (int32_t)(err == hipSuccess ? hipErrorInvalidDevice : err);
+    return 0;
+}
+
+skinny_status hip_status(hipError_t err) {
+    if (err == hipSuccess) return SKINNY_OK;
+    g_last_hip_error = (int32_t)err;
+    return SKINNY_EHIP;
+}
+
+skinny_status run_latent_append(const skinny_latent_append_args *a, void *stream) {
+    if (!a || a->n < 0 || a->heads < 0 || a->pages < 0 || a->page < 1 || !(a->eps >= 0.0f)) return SKINNY_EINVAL;
+    if (a->latent != 512 || a->rope != 64) return SKINNY_ENOTSUP;
+    const int64_t dim = a->latent + a->rope;
+    const bool with_q = a->q && a->heads > 0;
+    const skinny_status st = first_bad({check_stride(a->kv_stride, a->n, dim),
+                                        check_stride(a->cache_page_stride, a->pages, dim),
+                                        check_stride(a->cache_row_stride, a->page, dim),
+                                        with_q ? first_bad({check_stride(a->q_row_stride, a->n, a->rope),
+                                                            check_stride(a->q_head_stride, a->heads, a->rope),
+                                                            check_stride(a->q_out_row_stride, a->n, a->rope),
+                                                            check_stride(a->q_out_head_stride, a->heads, a->rope)})
+                                               : SKINNY_OK});
+    if (st != SKINNY_OK) return st;
+    if (a->heads > 65536 || a->n > ((int64_t)1 << 31) / 4 || a->page > INT_MAX || a->pages > INT_MAX) return SKINNY_ENOTSUP;
+    if (a->n * ((a->heads + 7) / 8 + 1) > INT_MAX) return SKINNY_ENOTSUP;
+    if (a->n == 0) return SKINNY_OK;
+    if (!a->kv || (!a->cache && a->pages > 0) || !a->slots || !a->positions || !a->inv_freq || (with_q && !a->q_out))
+        return SKINNY_EINVAL;
+    const void *wide[] = {a->kv, a->cache, a->norm_weight, with_q ? a->q : nullptr, with_q ? a->q_out : nullptr};
+    for (const void *p : wide)
+        if (p && !aligned(p, 16)) return SKINNY_EALIGN;
+    if (!aligned(a->slots, 8) || !aligned(a->positions, 8) || !aligned(a->inv_freq, 8)) return SKINNY_EALIGN;
+    return hip_status(launch_latent_append(*a, static_cast<hipStream_t>(stream)));
+}
+
+skinny_status run_latent_decode(const skinny_latent_decode_args *a, void *stream) {
+    if (!a || a->batch < 0 || a->tokens < 1 || a->heads < 0 || a->pages < 0 || a->page < 1 || a->max_pages < 0 ||
+        a->workspace_bytes < 0 || !(a->scale > 0.0f) || !(a->scale < INFINITY))
+        return SKINNY_EINVAL;
+    if (a->latent != 512 || a->rope != 64) return SKINNY_ENOTSUP;
+    const int64_t dim = a->latent + a->rope;
+    // counts first, so that the products below stay inside 64 bits
+    if (a->batch > 1 << 20 || a->tokens > 1 << 20 || a->heads > 1 << 16 || a->tokens * a->heads > 1 << 20 ||
+        a->batch * a->tokens * a->heads > 1 << 28 || a->pages > INT_MAX || a->page > 1 << 28 || a->max_pages > 1 << 28 || a->max_pages * a->page > 1 << 30)
+        return SKINNY_ENOTSUP;
+    const int64_t rows = a->batch * a->tokens;
+    if (rows == 0 || a->heads == 0) return SKINNY_OK;
+    if (a->pages < 1 || a->max_pages < 1) return SKINNY_EINVAL;  // a request's first page is always looked up
+    const skinny_status st = first_bad({check_stride(a->q_row_stride, rows, dim), check_stride(a->q_head_stride, a->heads, dim),
+                                        check_stride(a->cache_page_stride, a->pages, dim),
+                                        check_stride(a->cache_row_stride, a->page, dim),
+                                        check_stride(a->out_row_stride, rows, a->latent),
+                                        check_stride(a->out_head_stride, a->heads, a->latent)});
+    if (st != SKINNY_OK) return st;
+    if (a->batch > 1 && (a->table_stride < a->max_pages || a->table_stride > kMaxStride)) return SKINNY_EINVAL;
+    if (!a->q || !a->cache || !a->table || !a->lens || !a->out) return SKINNY_EINVAL;
+    const void *wide[] = {a->q, a->cache, a->out, a->workspace};
+    for (const void *p : wide)
+        if (p && !aligned(p, 16)) return SKINNY_EALIGN;
+    if (!aligned(a->table, 4) || !aligned(a->lens, 4) || (a->lse && !aligned(a->lse, 4))) return SKINNY_EALIGN;
+    const int cus = device_cus();
+    if (!cus) return SKINNY_EHIP;
+    if (a->workspace_bytes < latent_decode_workspace_bytes(a->batch, a->tokens, a->heads, cus) || !a->workspace)
+        return SKINNY_EINVAL;
+    return hip_status(launch_latent_decode(*a, cus, static_cast<hipStream_t>(stream)));
+}
+
+skinny_status run_latent_prefill(const skinny_latent_prefill_args *a, void *stream) {
+    if (!a || a->nq < 0 || a->nk < 0 || a->batch < 0 || a->heads < 0 || a->workspace_bytes < 0 || !(a->scale > 0.0f) ||
+        !(a->scale < INFINITY))
+        return SKINNY_EINVAL;
+    if (a->head_dim != 128 || a->rope != 64) return SKINNY_ENOTSUP;
+    if (a->nq > 1 << 30 || a->nk > 1 << 30 || a->batch > 1 << 20 || a->heads > 1 << 16) return SKINNY_ENOTSUP;
+    if ((a->nq / 64 + a->batch) * a->heads > 1 << 24) return SKINNY_ENOTSUP;     // workgroups of one launch
+    if (a->nq == 0 || a->heads == 0 || a->batch == 0) return SKINNY_OK;
+    const int64_t dq = a->head_dim + a->rope;
+    const skinny_status st = first_bad({check_stride(a->q_row_stride, a->nq, dq), check_stride(a->q_head_stride, a->heads, dq),
+                                        check_stride(a->k_row_stride, a->nk, a->head_dim),
+                                        check_stride(a->k_head_stride, a->heads, a->head_dim),
+                                        check_stride(a->v_row_stride, a->nk, a->head_dim),
+                                        check_stride(a->v_head_stride, a->heads, a->head_dim),
+                                        check_stride(a->k_rot_stride, a->nk, a->rope),
+                                        check_stride(a->out_row_stride, a->nq, a->head_dim),
+                                        check_stride(a->out_head_stride, a->heads, a->head_dim)});
+    if (st != SKINNY_OK) return st;
+    if (!a->q || !a->out || !a->cu_q || !a->cu_k || (a->nk > 0 && (!a->k || !a->v || !a->k_rot))) return SKINNY_EINVAL;
+    const void *wide[] = {a->q, a->k, a->v, a->k_rot, a->out, a->workspace};
+    for (const void *p : wide)
+        if (p && !aligned(p, 16)) return SKINNY_EALIGN;
+    if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || (a->lse && !aligned(a->lse, 4))) return SKINNY_EALIGN;
+    const int cus = device_cus();
+    if (!cus) return SKINNY_EHIP;
+    const int64_t need = latent_prefill_workspace_bytes(a->nq, a->nk, a->batch, a->heads, cus);
+    if (a->workspace_bytes < need || (need > 0 && !a->workspace)) return SKINNY_EINVAL;
+    return hip_status(launch_latent_prefill(*a, cus, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace skinny
 
 extern "C" {
+
+skinny_status skinny_latent_append_bf16(const skinny_latent_append_args *args, void *stream) {
+    return skinny::run_latent_append(args, stream);
+}
+
+skinny_status skinny_latent_decode_bf16(const skinny_latent_decode_args *args, void *stream) {
+    return skinny::run_latent_decode(args, stream);
+}
+
+skinny_status skinny_latent_prefill_bf16(const skinny_latent_prefill_args *args, void *stream) {
+    return skinny::run_latent_prefill(args, stream);
+}
+
+skinny_status skinny_latent_decode_workspace(int64_t batch, int64_t tokens, int64_t heads, int64_t *bytes) {
+    if (!bytes || batch < 0 || tokens < 0 || heads < 0) return SKINNY_EINVAL;
+    if (batch > 1 << 20 || tokens > 1 << 20 || heads > 1 << 16) return SKINNY_ENOTSUP;
+    const int cus = skinny::device_cus();
+    if (!cus) return SKINNY_EHIP;
+    *bytes = skinny::latent_decode_workspace_bytes(batch, tokens, heads, cus);
+    return SKINNY_OK;
+}
+
+skinny_status skinny_latent_prefill_workspace(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int64_t *bytes) {
+    if (!bytes || nq < 0 || nk < 0 || batch < 0 || heads < 0) return SKINNY_EINVAL;
+    if (nq > 1 << 30 || nk > 1 << 30 || batch > 1 << 20 || heads > 1 << 16) return SKINNY_ENOTSUP;
+    const int cus = skinny::device_cus();
+    if (!cus) return SKINNY_EHIP;
+    *bytes = skinny::latent_prefill_workspace_bytes(nq, nk, batch, heads, cus);
+    return SKINNY_OK;
+}
 
 skinny_status skinny_kda_verify_bf16(const skinny_kda_args *args, void *stream) {
     return skinny::run_kda(args, stream);

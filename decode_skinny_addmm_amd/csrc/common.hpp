@@ -68,6 +68,15 @@ int64_t kbit_max_k();
 // One KDA chain-verify call (kda_verify.hip), validated by the C ABI layer.
 hipError_t launch_kda_verify(const skinny_kda_args &a, hipStream_t stream);
 
+// The latent attention operators (latent_append.hip, latent_decode.hip, latent_prefill.hip),
+// validated by the C ABI layer. cus: compute units of the current device; the launch and the
+// workspace size of one call must be given the same number.
+hipError_t launch_latent_append(const skinny_latent_append_args &a, hipStream_t stream);
+hipError_t launch_latent_decode(const skinny_latent_decode_args &a, int cus, hipStream_t stream);
+int64_t latent_decode_workspace_bytes(int64_t batch, int64_t tokens, int64_t heads, int cus);
+hipError_t launch_latent_prefill(const skinny_latent_prefill_args &a, int cus, hipStream_t stream);
+int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus);
+
 // Registries filled by each kernel family's translation unit.
 const KernelEntry *gemv_entries(int *count);
 const KernelEntry *mfma_entries(int *count);

@@ -1,0 +1,393 @@
+// latent_prefill.hip -- expanded latent attention of prompts: each head's own keys and values
+// (128 numbers each) next to the 64 rotated numbers of a key that all heads share.
+//
+// Sequence i has queries cu_q[i] .. cu_q[i + 1] and keys cu_k[i] .. cu_k[i + 1]; per head
+//     s = scale * (q[:128] . k + q[128:] . k_rot),   out = softmax(s) v,   lse = log sum exp(s);
+// causal: the last query sees the last key, the one before it one key fewer, and so on.
+//
+// What bounds it: the matrix cores (2 * 320 operations a query-key pair and head) and beside
+// them the exponentials. A workgroup of 4 waves holds 128 query rows of one head, 32 a wave, in
+// registers, and reads keys and values in tiles of 64 through two LDS stages of 40 KB; two
+// workgroups share a CU, so that one's softmax runs beside the other's matrix instructions.
+// Where the queries are too few to fill the chip, a row's keys are split over several
+// workgroups and their partial sums joined by a second kernel.
+#include <algorithm>
+
+#include "latent.hpp"
+
+namespace skinny {
+namespace {
+
+using namespace latent;
+typedef Tile32 T;
+
+constexpr int HD = 128, ROT = 64, DQ = HD + ROT;
+constexpr int WAVES = 4, THREADS = WAVES * 64;
+constexpr int BM = WAVES * T::ROWS;          // query rows a workgroup
+constexpr int KT = 64;                       // keys a tile
+constexpr int KSEG = DQ * 2 / 128, VSEG = HD * 2 / 128;
+constexpr int K_BYTES = KT * DQ * 2, STAGE_BYTES = K_BYTES + KT * HD * 2;
+constexpr int STAGES = 2;
+constexpr int KS = DQ / T::KSTEP;            // K steps of the score product
+constexpr int ND = HD / T::DIMS;             // dim tiles of the output
+constexpr int NT = KT / T::ROWS;             // key subtiles
+constexpr int NP = NT * T::NS;               // weights a lane holds
+
+struct PrefillArgs {
+    const uint16_t *q, *k, *v, *kr;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head, kr_row;
+    const int32_t *cu_q, *cu_k;
+    uint16_t *out;
+    int64_t o_row, o_head;
+    float *lse;
+    float *work;                             // split: per split, row and head: 128 sums, then maximum, total
+    int64_t nq, nk;
+    int batch, heads, tiles, splits;         // tiles: most query tiles that nq rows in batch sequences can need
+    float c;
+    bool causal;
+};
+
+// One row's partial: 128 sums; maxima and totals follow all rows' sums.
+__host__ __device__ inline int64_t split_floats(int64_t nq, int64_t heads) { return nq * heads * (HD + 2); }
+
+// cu[i], never outside 0 .. n
+__device__ __forceinline__ int start(const int32_t *cu, int i, int64_t n) { return (int)min((int64_t)max(cu[i], 0), n); }
+
+// The sequence whose query tiles hold tile `at`, counted over all sequences; -1: none.
+__device__ __forceinline__ int find_tile(const PrefillArgs &a, int at, int &tile) {
+    const int lane = threadIdx.x & 63;
+    int carry = 0;
+    for (int i0 = 0; i0 < a.batch; i0 += 64) {
+        const int i = i0 + lane;
+        const int n = i < a.batch ? (max(0, start(a.cu_q, i + 1, a.nq) - start(a.cu_q, i, a.nq)) + BM - 1) / BM : 0;
+        int s = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(s, d);
+            if (lane >= d) s += o;
+        }
+        const uint64_t past = __ballot(carry + s > at);
+        if (past) {
+            const int w = __builtin_ctzll(past);
+            tile = at - carry - (__shfl(s, w) - __shfl(n, w));
+            return i0 + w;
+        }
+        carry += __shfl(s, 63);
+    }
+    return -1;
+}
+
+// One pass over key tiles [t0, t1). limit: keys that the lane's row sees; first: the fewest that
+// any row of the workgroup sees. safe: non-finite values in tiles that some row sees in part
+// reach only the rows that see them (see split_value).
+__device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, const u32x4_t (&qf)[KS], int head,
+                                          int64_t k0row, int lk, int t0, int t1, int limit, int first, bool safe,
+                                          f32x16_t (&o)[ND], float &m, float &l) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row = T::row(lane), grp = T::grp(lane);
+    lds_u8 *ring = (lds_u8 *)lds;
+
+    // staging: wave w takes the 8-row groups 2w and 2w + 1 of a tile. Rows past the last key
+    // repeat it (their scores are masked)
+    auto issue = [&](int t) {
+        lds_u8 *st = ring + (t & 1) * STAGE_BYTES;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int rg = 2 * wave + u, r = 8 * rg + (lane >> 3);
+            const int chunk = ((lane & 7) ^ swz(r)) * 8;
+            const int64_t key = k0row + min(t * KT + r, lk - 1);
+            const uint16_t *kp = a.k + key * a.k_row + head * a.k_head + chunk;
+            const uint16_t *rp = a.kr + key * a.kr_row + chunk;
+            const uint16_t *vp = a.v + key * a.v_row + head * a.v_head + chunk;
+            lds_u8 *kd = st + rg * (KSEG * 1024), *vd = st + K_BYTES + rg * (VSEG * 1024);
+            __builtin_amdgcn_global_load_lds((const void *)kp, (lds_void *)kd, 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const void *)(kp + 64), (lds_void *)(kd + 1024), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const void *)rp, (lds_void *)(kd + 2048), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const void *)vp, (lds_void *)vd, 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const void *)(vp + 64), (lds_void *)(vd + 1024), 16, 0, 0);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int j = 0; j < T::NO; ++j) o[i][j] = 0.0f;
+    m = -INFINITY;
+    l = 0.0f;
+    // fragment places within a stage, with the swizzle worked out once: see latent_decode.hip
+    int koff[4], voff[2][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        koff[j] = (row >> 3) * (KSEG * 1024) + (row & 7) * 128 + (((2 * j + grp) ^ swz(row)) << 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int r = 8 * hh + 4 * grp + ((lane & 15) >> 2);
+            const int ch = 4 * j + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+            voff[j][hh] = K_BYTES + hh * (VSEG * 1024) + (r & 7) * 128 + ((ch ^ swz(r)) << 4) + (lane & 1) * 8;
+        }
+    if (t0 < t1) issue(t0);
+    for (int t = t0; t < t1; ++t) {
+        wait_vmcnt<0>();
+        lds_barrier();                       // tile t is staged, the other stage is free
+        if (t + 1 < t1) issue(t + 1);
+        lds_u8 *st = ring + (t & 1) * STAGE_BYTES;
+        f32x16_t s[NT];
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int j = 0; j < T::NO; ++j) s[u][j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const u32x4_t kf = *(const lds_u32x4 *)(st + koff[k % 4] + u * (T::ROWS / 8) * (KSEG * 1024) +
+                                                        (k / 4) * 1024);
+                s[u] = T::mfma(kf, qf[k], s[u]);
+            }
+        }
+        float p[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) p[i] = s[i / T::NS][i % T::NS];
+        const int k0 = t * KT;
+        const bool mixed = k0 + KT > first;
+        if (mixed) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                p[i] = k0 + (i / T::NS) * T::ROWS + T::place(i % T::NS, grp) < limit ? p[i] : -INFINITY;
+        }
+        float top = p[0];
+#pragma unroll
+        for (int i = 1; i < NP; ++i) top = fmaxf(top, p[i]);
+        top = row_max<T>(top) * a.c;
+        if (__any(top > m + kSlack)) {
+            const float n = fmaxf(m, top);
+            const float alpha = n == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - n);
+            m = n;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+                for (int j = 0; j < T::NO; ++j) o[i][j] *= alpha;
+        }
+        const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], a.c, -mu));
+            l += p[i];
+        }
+        // weights are rounded to bf16 for the matrix product (relative 2^-9 each, as the values
+        // are); their sum l is of the unrounded ones
+        u32x4_t pf[NP / 8];
+#pragma unroll
+        for (int i = 0; i < NP / 2; ++i) pf[i / 4][i % 4] = pack_bf16(p[2 * i], p[2 * i + 1]);
+        auto value = [&](int i, int x) {     // dim tile i, 16 keys x
+            u32x4_t f;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                lds_u8 *at = st + voff[i % 2][hh] + (i / 2) * 1024 + 2 * x * (VSEG * 1024);
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
+                f[2 * hh] = v[0];
+                f[2 * hh + 1] = v[1];
+            }
+            return f;
+        };
+        if (!(mixed && safe)) {
+#pragma unroll
+            for (int x = 0; x < NP / 8; ++x)
+#pragma unroll
+                for (int i = 0; i < ND; ++i) o[i] = T::mfma(value(i, x), pf[x], o[i]);
+        } else {
+            u32x4_t see[NP / 8];
+#pragma unroll
+            for (int j = 0; j < NP; j += 2) {
+                const int key = k0 + (j / T::NS) * T::ROWS + T::place(j % T::NS, grp);
+                see[j / 8][j % 8 / 2] = seen_pair(key < limit, key + 1 < limit);
+            }
+#pragma unroll
+            for (int x = 0; x < NP / 8; ++x)
+#pragma unroll
+                for (int i = 0; i < ND; ++i) {
+                    u32x4_t g, a1, a2;
+                    split_value(value(i, x), g, a1, a2);
+                    o[i] = T::mfma(g, pf[x], o[i]);
+                    o[i] = T::mfma(a1, see[x], o[i]);
+                    o[i] = T::mfma(a2, see[x], o[i]);
+                }
+        }
+    }
+    l = row_sum<T>(l);
+    lds_barrier();
+}
+
+// Whether the flag is set in any lane of the workgroup (in the ring's memory: two workgroups'
+// rings are all of a CU's LDS). The ring is free before and after.
+__device__ __forceinline__ bool any_wave(bool flag, uint8_t *lds) {
+    volatile int *w = reinterpret_cast<volatile int *>(lds);
+    const bool mine = __any(flag);
+    if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = mine;
+    __syncthreads();
+    const bool any = w[0] | w[1] | w[2] | w[3];
+    __syncthreads();
+    return any;
+}
+
+__global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int row = T::row(lane), grp = T::grp(lane);
+    // Block order. Workgroups go to the XCDs in turn; where the heads divide evenly over them an
+    // XCD takes whole heads, one after the other, so that its L2 holds the keys and values its
+    // workgroups share. A head's last query tiles, which see the most keys, come first.
+    int b = blockIdx.x;
+    const int split = b % a.splits;
+    b /= a.splits;
+    int head, at;
+    if (a.heads % 8 == 0 && a.splits == 1) {
+        const int j = b >> 3;
+        head = (b & 7) + 8 * (j / a.tiles);
+        at = j % a.tiles;
+    } else {
+        head = b % a.heads;
+        at = b / a.heads;
+    }
+    int tile = 0;
+    const int seq = find_tile(a, a.tiles - 1 - at, tile);
+    if (seq < 0) return;
+    const int q0 = start(a.cu_q, seq, a.nq), lq = start(a.cu_q, seq + 1, a.nq) - q0;
+    const int k0 = start(a.cu_k, seq, a.nk), lk = max(0, start(a.cu_k, seq + 1, a.nk) - k0);
+    const int r = tile * BM + wave * T::ROWS + row, rc = min(r, lq - 1);
+    const int64_t qr = (int64_t)q0 + rc;
+
+    u32x4_t qf[KS];
+    const uint16_t *qp = a.q + qr * a.q_row + head * a.q_head + grp * 8;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const u32x4_t *>(qp + k * T::KSTEP);
+
+    // keys that this row, the workgroup's first row and its last row see
+    auto sees = [&](int x) { return a.causal ? max(0, min(lk, lk - lq + 1 + x)) : lk; };
+    const int limit = sees(rc), first = sees(tile * BM), last = sees(min(tile * BM + BM, lq) - 1);
+    const int n = (last + KT - 1) / KT;
+    const int t0 = (int)((int64_t)n * split / a.splits), t1 = (int)((int64_t)n * (split + 1) / a.splits);
+    f32x16_t o[ND];
+    float m, l;
+    bool safe = false;
+    for (;;) {
+        run_tiles(a, lds, qf, head, k0, lk, t0, t1, limit, first, safe, o, m, l);
+        // a non-finite result where some rows see fewer keys than others: once more, key by key
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int j = 0; j < T::NO; ++j) odd |= !finite_f32(o[i][j]);
+        if (safe || !any_wave(odd && t1 * KT > first, lds)) break;
+        safe = true;
+    }
+    if (r >= lq) return;
+    if (a.splits == 1) {
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;          // no key: zeros
+        uint16_t *op = a.out + qr * a.o_row + head * a.o_head;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int x = 0; x < T::NO / 4; ++x) {
+                const u32x2_t v = {pack_bf16(o[i][4 * x] * inv, o[i][4 * x + 1] * inv),
+                                   pack_bf16(o[i][4 * x + 2] * inv, o[i][4 * x + 3] * inv)};
+                *reinterpret_cast<u32x2_t *>(op + i * T::DIMS + T::place(4 * x, grp)) = v;
+            }
+        if (a.lse && grp == 0) a.lse[qr * a.heads + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+    } else {
+        const int64_t at_row = qr * a.heads + head, all = a.nq * a.heads;
+        float *part = a.work + split * split_floats(a.nq, a.heads);
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int x = 0; x < T::NO / 4; ++x)
+                *reinterpret_cast<f32x4_t *>(part + at_row * HD + i * T::DIMS + T::place(4 * x, grp)) =
+                    f32x4_t{o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]};
+        if (grp == 0) {
+            part[all * HD + at_row] = m;
+            part[all * (HD + 1) + at_row] = l;
+        }
+    }
+}
+
+// Joins the splits of a row and head: 32 lanes, 4 numbers each.
+__global__ __launch_bounds__(256) void latent_prefill_join_kernel(PrefillArgs a) {
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), all = a.nq * a.heads;
+    const int x = threadIdx.x & 31;
+    if (at >= all) return;
+    float m = -INFINITY, l = 0.0f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.splits; ++s) {
+        const float *part = a.work + s * split_floats(a.nq, a.heads);
+        const float pm = part[all * HD + at], pl = part[all * (HD + 1) + at];
+        const f32x4_t po = *reinterpret_cast<const f32x4_t *>(part + at * HD + 4 * x);
+        const float n = fmaxf(m, pm);
+        const float ca = m == n ? 1.0f : __builtin_amdgcn_exp2f(m - n);
+        const float cb = pm == n ? 1.0f : __builtin_amdgcn_exp2f(pm - n);
+        m = n;
+        l = l * ca + pl * cb;
+        o = o * ca + po * cb;
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    const int64_t qr = at / a.heads, head = at % a.heads;
+    *reinterpret_cast<u32x2_t *>(a.out + qr * a.o_row + head * a.o_head + 4 * x) =
+        u32x2_t{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+    if (a.lse && x == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+int64_t query_tiles(int64_t nq, int64_t batch) { return std::min(nq, nq / BM + batch); }
+
+// Splits of the keys: as many as fill two workgroups a CU, while each keeps 8 key tiles of the
+// average sequence.
+int pick_splits(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus) {
+    const int64_t blocks = query_tiles(nq, batch) * heads;
+    const int64_t most = std::max<int64_t>(1, nk / batch / (8 * KT));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * (int64_t)cus / std::max<int64_t>(1, blocks), most, 32}));
+}
+
+}  // namespace
+
+int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus) {
+    if (nq == 0 || batch == 0 || heads == 0) return 0;
+    const int s = pick_splits(nq, nk, batch, heads, cus);
+    return s == 1 ? 0 : s * split_floats(nq, heads) * (int64_t)sizeof(float);
+}
+
+hipError_t launch_latent_prefill(const skinny_latent_prefill_args &p, int cus, hipStream_t stream) {
+    PrefillArgs a;
+    a.q = static_cast<const uint16_t *>(p.q);
+    a.k = static_cast<const uint16_t *>(p.k);
+    a.v = static_cast<const uint16_t *>(p.v);
+    a.kr = static_cast<const uint16_t *>(p.k_rot);
+    a.q_row = p.q_row_stride;
+    a.q_head = p.q_head_stride;
+    a.k_row = p.k_row_stride;
+    a.k_head = p.k_head_stride;
+    a.v_row = p.v_row_stride;
+    a.v_head = p.v_head_stride;
+    a.kr_row = p.k_rot_stride;
+    a.cu_q = p.cu_q;
+    a.cu_k = p.cu_k;
+    a.out = static_cast<uint16_t *>(p.out);
+    a.o_row = p.out_row_stride;
+    a.o_head = p.out_head_stride;
+    a.lse = p.lse;
+    a.work = static_cast<float *>(p.workspace);
+    a.nq = p.nq;
+    a.nk = p.nk;
+    a.batch = (int)p.batch;
+    a.heads = (int)p.heads;
+    a.tiles = (int)query_tiles(p.nq, p.batch);
+    a.splits = pick_splits(p.nq, p.nk, p.batch, p.heads, cus);
+    a.c = p.scale * kLog2e;
+    a.causal = p.causal != 0;
+    hipLaunchKernelGGL(latent_prefill_kernel, dim3((unsigned)(a.tiles * a.heads * a.splits)), dim3(THREADS), 0, stream, a);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || a.splits == 1) return err;
+    hipLaunchKernelGGL(latent_prefill_join_kernel, dim3((unsigned)((p.nq * a.heads + 7) / 8)), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace skinny

@@ -307,6 +307,103 @@ typedef struct skinny_kda_args {
 
 SKINNY_API skinny_status skinny_kda_verify_bf16(const skinny_kda_args *args, void *stream);
 
+/*
+ * Latent attention: the cache holds one vector a token, 512 latents (every head's keys and
+ * values follow from them by fixed projections) and the 64 rotated numbers of a key that all
+ * heads share. Three operators: append, decode (absorbed form, over the cache) and prefill
+ * (expanded form, over keys and values of each head). All numbers are bf16 with fp32 sums,
+ * softmax statistics and norms; each output is rounded once, and the softmax weights once, to
+ * bf16, before they meet the values. Strides are in elements, multiples of 8 (rows are read in
+ * 16-byte vectors; a stride whose extent is 1 is not looked at), the innermost is 1, and
+ * q, cache, kv, k, v, k_rot, out, q_out must be 16-byte aligned (else SKINNY_EALIGN). Device
+ * pointers, asynchronous, capturable, no allocation, as everywhere above.
+ *
+ * Append. Per token n: z = x / sqrt(mean(x^2) + eps) * w over kv[n, :512] (norm_weight NULL: x as
+ * it is); r = kv[n, 512:576] turned by the token's position: pairs (i, i + 32), or (2i, 2i + 1)
+ * with interleaved != 0, by positions[n] * inv_freq[i], the angle in 64 bits. [z, r] goes to row
+ * slots[n] % page of cache page slots[n] / page; a slot outside the cache (-1 for padding) writes
+ * nothing. q (may be NULL) is every head's rotated part [n, heads, 64], turned into q_out, which
+ * may be q itself. Two tokens with one slot leave one of the two rows' numbers in each place.
+ */
+typedef struct skinny_latent_append_args {
+    const void *kv;                 /* [n, 576] */
+    void *cache;                    /* [pages, page, 576] */
+    const int64_t *slots, *positions;
+    const double *inv_freq;         /* [32] */
+    const void *norm_weight;        /* [512] contiguous, 16-byte aligned, or NULL */
+    const void *q;                  /* [n, heads, 64] or NULL */
+    void *q_out;
+    int64_t kv_stride, cache_page_stride, cache_row_stride;
+    int64_t q_row_stride, q_head_stride, q_out_row_stride, q_out_head_stride;
+    int64_t n, heads, pages, page, latent, rope;   /* latent 512, rope 64 (else SKINNY_ENOTSUP) */
+    float eps;
+    int32_t interleaved;
+} skinny_latent_append_args;
+
+SKINNY_API skinny_status skinny_latent_append_bf16(const skinny_latent_append_args *args, void *stream);
+
+/*
+ * Decode. Request i has lens[i] cached rows, the last `tokens` of them its new ones; row k lies in
+ * cache page table[i, k / page], place k % page. Query (token j, head h) = q[i * tokens + j, h]
+ * sees keys k < lens[i] - tokens + j + 1:
+ *     s_k = scale * q . cache_k (576 numbers),  out = sum_k softmax(s)_k cache_k[:512],
+ *     lse = log sum_k exp(s_k)  (lse may be NULL).
+ * A row that sees no key gets zeros and -inf; what keys that a row does not see hold (non-finite
+ * numbers too) never reaches it. Lengths outside 0 .. max_pages * page and page ids outside
+ * 0 .. pages - 1 are clamped. scale must be positive and finite. workspace: device memory of
+ * skinny_latent_decode_workspace(), 16-byte aligned, whose contents need not be kept; calls
+ * that may run at the same time need one each.
+ */
+typedef struct skinny_latent_decode_args {
+    const void *q;                  /* [batch * tokens, heads, 576] */
+    const void *cache;              /* [pages, page, 576] */
+    const int32_t *table;           /* [batch, max_pages], rows table_stride apart */
+    const int32_t *lens;            /* [batch] */
+    void *out;                      /* [batch * tokens, heads, 512] */
+    float *lse;                     /* [batch * tokens, heads] or NULL */
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t q_row_stride, q_head_stride, cache_page_stride, cache_row_stride, table_stride;
+    int64_t out_row_stride, out_head_stride;
+    int64_t batch, tokens, heads, pages, page, max_pages, latent, rope;
+    float scale;
+} skinny_latent_decode_args;
+
+SKINNY_API skinny_status skinny_latent_decode_bf16(const skinny_latent_decode_args *args, void *stream);
+
+/* Bytes of workspace that a decode call of these sizes needs on the current device, whatever its
+ * lengths; SKINNY_EINVAL for negative sizes or a NULL `bytes`. */
+SKINNY_API skinny_status skinny_latent_decode_workspace(int64_t batch, int64_t tokens, int64_t heads,
+                                                        int64_t *bytes);
+
+/*
+ * Prefill. Sequence i has queries cu_q[i] .. cu_q[i + 1] - 1 and keys cu_k[i] .. cu_k[i + 1] - 1
+ * (rising, from 0 to nq and nk; values outside are clamped). Per head:
+ *     s = scale * (q[:128] . k + q[128:] . k_rot),  out = softmax(s) v,  lse = log sum exp(s).
+ * causal != 0: of lq queries and lk keys, query x sees the first lk - lq + 1 + x. Rows that see
+ * no key, and keys that a row does not see, as in decode. workspace: of
+ * skinny_latent_prefill_workspace() bytes (may be 0, then NULL is taken).
+ */
+typedef struct skinny_latent_prefill_args {
+    const void *q;                  /* [nq, heads, 192] */
+    const void *k, *v;              /* [nk, heads, 128] each */
+    const void *k_rot;              /* [nk, 64] */
+    const int32_t *cu_q, *cu_k;     /* [batch + 1] */
+    void *out;                      /* [nq, heads, 128] */
+    float *lse;                     /* [nq, heads] or NULL */
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+    int64_t k_rot_stride, out_row_stride, out_head_stride;
+    int64_t nq, nk, batch, heads, head_dim, rope;  /* head_dim 128, rope 64 (else SKINNY_ENOTSUP) */
+    float scale;
+    int32_t causal;
+} skinny_latent_prefill_args;
+
+SKINNY_API skinny_status skinny_latent_prefill_bf16(const skinny_latent_prefill_args *args, void *stream);
+SKINNY_API skinny_status skinny_latent_prefill_workspace(int64_t nq, int64_t nk, int64_t batch, int64_t heads,
+                                                         int64_t *bytes);
+
 /* Number of configurations built into the library, and the i-th of them (0-based). */
 SKINNY_API int32_t skinny_num_configs(void);
 SKINNY_API skinny_status skinny_get_config(int32_t index, skinny_config *out);
