@@ -1,4 +1,5 @@
-"""Ahead-of-time build of libskinny.so for gfx950 with hipcc (no JIT at run time).
+"""Ahead-of-time build of libskinny.so for gfx950 with hipcc and of the _latent binding module with
+g++ (no JIT at run time).
 
     python -m decode_skinny_addmm_amd.build      # or __graft_entry__.build()
 
@@ -6,6 +7,7 @@ Every .hip file in csrc/ is compiled to an object in parallel, then linked into
 decode_skinny_addmm_amd/libskinny.so. Packed-fp32 instructions are disabled for all
 device code (-packed-fp32-ops). kernel_code.json beside the library maps each kernel's
 mangled name to a hash of its gfx950 machine code (the key of measured byte counts).
+csrc/binding.cpp, host code alone, becomes decode_skinny_addmm_amd/_latent.so.
 """
 from __future__ import annotations
 
@@ -47,6 +49,29 @@ def _compile(src: str) -> str:
     if err.strip():
         sys.stderr.write(err + "\n")
     return obj
+
+
+BINDING = os.path.join(PKG, "_latent.so")
+
+
+def _compile_binding() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-Wno-unused-function", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    for inc in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", inc]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp]
+    cmd += ["-L" + p for p in cpp_extension.library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError("g++ failed for binding.cpp:\n%s" % p.stderr)
+    if p.stderr.strip():
+        sys.stderr.write(p.stderr)
+    os.replace(tmp, BINDING)
 
 
 CODE_MAP = os.path.join(PKG, "kernel_code.json")
@@ -131,7 +156,9 @@ def build(jobs: int | None = None, verbose: bool = True) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     jobs = jobs or min(len(srcs), max(1, len(os.sched_getaffinity(0))))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
+        binding.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     subprocess.run(cmd, check=True)

@@ -12,8 +12,7 @@ import ctypes
 import torch
 
 from ._lib import (CONFIG_FIELDS, FLAG_NO_NEG_ZERO, FLAG_ROUND_PRODUCT, SkinnyConfig, SkinnyError, SkinnyKdaArgs,  # noqa: F401
-                   SkinnyLatentAppendArgs, SkinnyLatentDecodeArgs, SkinnyLatentPrefillArgs, SkinnyResources, check,
-                   lib)
+                   SkinnyResources, check, lib)
 
 
 def _as_config(cfg) -> SkinnyConfig | None:
@@ -306,31 +305,26 @@ def kda_verify(inp: dict, T: int, H: int, HV: int, K: int, V: int, scale: float,
     return out
 
 
-def _check_tensors(dev, spec):
-    """spec: name -> (tensor, dtype, shape). Each must be a tensor of that kind on dev."""
-    for name, (t, dt, shape) in spec.items():
-        if not isinstance(t, torch.Tensor):
-            raise ValueError("%s must be a torch.Tensor" % name)
-        if t.dtype != dt or tuple(t.shape) != tuple(shape):
-            raise ValueError("%s must be %s %s, got %s %s" % (name, dt, tuple(shape), t.dtype, tuple(t.shape)))
-        if t.device != dev:
-            raise ValueError("%s is on %s: all tensors must be on %s" % (name, t.device, dev))
+LATENT, ROPE, HEAD = 512, 64, 128  # the sizes that the latent attention kernels are built for
+
+_latent_module = None
 
 
-def _check_rows(spec):
-    """spec: name -> tensor read or written in 16-byte vectors: its last dimension contiguous, its
-    other strides whole vectors, its address aligned."""
-    for name, t in spec.items():
-        if t.numel() == 0:
-            continue
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError("%s must be contiguous in its last dimension" % name)
-        for n, st in zip(t.shape[:-1], t.stride()[:-1]):
-            if n > 1 and (st % 8 or st < t.shape[-1]):
-                raise ValueError("%s has strides %s: rows must not overlap and must start at multiples of 8 "
-                                 "elements" % (name, tuple(t.stride())))
-        if t.data_ptr() % 16:
-            raise ValueError("%s must be 16-byte aligned" % name)
+def _latent():
+    """The native binding of the latent attention operators (csrc/binding.cpp), given the library's
+    entry points: it checks the tensors (ValueError) and calls them."""
+    global _latent_module
+    if _latent_module is None:
+        L = lib()
+        try:
+            from . import _latent as module
+        except ImportError as e:
+            raise RuntimeError("the _latent module is not built; run `python -m decode_skinny_addmm_amd.build` or "
+                               "__graft_entry__.build()") from e
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (L.skinny_latent_append_bf16, L.skinny_latent_decode_bf16, L.skinny_latent_prefill_bf16)))
+        _latent_module = module
+    return _latent_module
 
 
 def _gpu_of(name, t):
@@ -341,24 +335,15 @@ def _gpu_of(name, t):
     return t.device
 
 
-def _no_overlap(outputs, inputs):
-    """outputs, inputs: name -> tensor. Byte spans of outputs may meet none of the others'."""
-    names = list(outputs)
-    for i, a in enumerate(names):
-        for b, t in list(inputs.items()) + [(n, outputs[n]) for n in names[:i]]:
-            if _overlaps(outputs[a], t):
-                raise ValueError("%s must not overlap %s" % (a, b))
-
-
-def _check_scale(scale) -> float:
-    # as the library sees it, in 32 bits
-    s = ctypes.c_float(scale).value
-    if not (s > 0 and s != float("inf")):
-        raise ValueError("scale must be positive and finite, got %r" % (scale,))
-    return s
-
-
-LATENT, ROPE, HEAD = 512, 64, 128  # the sizes that the latent attention kernels are built for
+def _call(fn, what, dev, stream, *args):
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st:
+        check(st, what)
 
 
 def latent_append(kv, cache, slots, positions, inv_freq, norm_weight=None, eps: float = 1e-6, q=None, q_out=None,
@@ -375,54 +360,10 @@ def latent_append(kv, cache, slots, positions, inv_freq, norm_weight=None, eps: 
     into q_out (allocated where None; may be q itself). Returns q_out, or None without q. kv, cache,
     q and q_out may have strides (multiples of 8, contiguous last dimension)."""
     dev = _gpu_of("kv", kv)
-    if kv.dim() != 2:
-        raise ValueError("kv must be 2-D")
-    n = kv.shape[0]
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[1] < 1:
-        raise ValueError("cache must be a tensor [pages, page_size, %d]" % (LATENT + ROPE))
-    pages, page = cache.shape[:2]
-    spec = {"kv": (kv, torch.bfloat16, (n, LATENT + ROPE)), "cache": (cache, torch.bfloat16, (pages, page, LATENT + ROPE)),
-            "slots": (slots, torch.int64, (n,)), "positions": (positions, torch.int64, (n,)),
-            "inv_freq": (inv_freq, torch.float64, (ROPE // 2,))}
-    rows = {"kv": kv, "cache": cache}
-    flat = {"slots": slots, "positions": positions, "inv_freq": inv_freq}
-    if norm_weight is not None:
-        spec["norm_weight"] = (norm_weight, torch.bfloat16, (LATENT,))
-        flat["norm_weight"] = rows["norm_weight"] = norm_weight
-    if not eps >= 0:
-        raise ValueError("eps must not be negative, got %r" % (eps,))
-    heads = 0
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise ValueError("q must be a tensor [n, heads, %d]" % ROPE)
-        heads = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty((n, heads, ROPE), dtype=torch.bfloat16, device=dev)
-        spec["q"] = (q, torch.bfloat16, (n, heads, ROPE))
-        spec["q_out"] = (q_out, torch.bfloat16, (n, heads, ROPE))
-        rows["q"], rows["q_out"] = q, q_out
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    _check_tensors(dev, spec)
-    for name, t in flat.items():
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-    _check_rows(rows)
-    same = q is not None and q.data_ptr() == q_out.data_ptr() and q.stride() == q_out.stride()
-    inputs = {name: t for name, (t, _, _) in spec.items() if name not in ("cache", "q_out") and not (same and name == "q")}
-    _no_overlap({"cache": cache, "q_out": q_out} if q is not None else {"cache": cache}, inputs)
-    p = lambda t: None if t is None else t.data_ptr()
-    a = SkinnyLatentAppendArgs(
-        kv=p(kv), cache=p(cache), slots=p(slots), positions=p(positions), inv_freq=p(inv_freq),
-        norm_weight=p(norm_weight), q=p(q), q_out=p(q_out), kv_stride=kv.stride(0), cache_page_stride=cache.stride(0),
-        cache_row_stride=cache.stride(1), n=n, heads=heads, pages=pages, page=page, latent=LATENT, rope=ROPE,
-        eps=eps, interleaved=int(bool(interleaved)))
-    if q is not None:
-        a.q_row_stride, a.q_head_stride = q.stride()[:2]
-        a.q_out_row_stride, a.q_out_head_stride = q_out.stride()[:2]
-    with torch.cuda.device(dev):
-        st = lib().skinny_latent_append_bf16(ctypes.byref(a), _stream_ptr(stream, dev))
-    check(st, "skinny_latent_append_bf16")
+    if q is not None and q_out is None:
+        q_out = torch.empty(tuple(q.shape) if isinstance(q, torch.Tensor) else 0, dtype=torch.bfloat16, device=dev)
+    _call(_latent().append, "skinny_latent_append_bf16", dev, stream, kv, cache, slots, positions, inv_freq, norm_weight,
+          eps, q, q_out, interleaved)
     return q_out
 
 
@@ -450,15 +391,6 @@ def latent_prefill_workspace(nq: int, nk: int, batch: int, heads: int, device="c
                       heads)
 
 
-def _check_workspace(workspace, dev, others):
-    if (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or workspace.device != dev
-            or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' GPU")
-    for name, t in others.items():
-        if _overlaps(workspace, t):
-            raise ValueError("workspace must not overlap %s" % name)
-
-
 def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim: int = ROPE, out=None, lse=None,
                   workspace=None, stream=None):
     """Absorbed latent attention of each request's newest tokens over a paged latent cache
@@ -474,52 +406,20 @@ def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim
     contiguous last dimension). workspace: latent_decode_workspace(batch, tokens, heads), kept by
     the caller between calls; allocated for this call where None. Returns (out, lse)."""
     dev = _gpu_of("q", q)
-    if rope_dim != ROPE:
-        raise ValueError("rope_dim must be %d" % ROPE)
-    if tokens < 1:
-        raise ValueError("tokens must be at least 1, got %d" % tokens)
-    if q.dim() != 3:
-        raise ValueError("q must be 3-D")
-    rows, heads = q.shape[:2]
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a tensor [batch, max_pages]")
-    batch, max_pages = table.shape
-    if rows != batch * tokens:
-        raise ValueError("q has %d rows: table has %d requests of %d tokens" % (rows, batch, tokens))
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 3 or cache.shape[1] < 1:
-        raise ValueError("cache must be a tensor [pages, page_size, %d]" % (LATENT + ROPE))
-    pages, page = cache.shape[:2]
-    if out is None:
-        out = torch.empty((rows, heads, LATENT), dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = latent_decode_workspace(batch, tokens, heads, LATENT, dev)
-    _check_tensors(dev, {"q": (q, torch.bfloat16, (rows, heads, LATENT + ROPE)),
-                         "cache": (cache, torch.bfloat16, (pages, page, LATENT + ROPE)),
-                         "table": (table, torch.int32, (batch, max_pages)), "lens": (lens, torch.int32, (batch,)),
-                         "out": (out, torch.bfloat16, (rows, heads, LATENT)),
-                         "lse": (lse, torch.float32, (rows, heads))})
-    _check_rows({"q": q, "cache": cache, "out": out})
-    if not lens.is_contiguous() or not lse.is_contiguous():
-        raise ValueError("lens and lse must be contiguous")
-    if (max_pages > 1 and table.stride(1) != 1) or (batch > 1 and table.stride(0) < max_pages):
-        raise ValueError("table must be contiguous in its last dimension, its rows apart")
-    if rows and heads and (pages < 1 or max_pages < 1):
-        raise ValueError("the cache and the table need a page at least")
-    inputs = {"q": q, "cache": cache, "table": table, "lens": lens}
-    _no_overlap({"out": out, "lse": lse}, inputs)
-    _check_workspace(workspace, dev, dict(inputs, out=out, lse=lse))
-    a = SkinnyLatentDecodeArgs(
-        q=q.data_ptr(), cache=cache.data_ptr(), table=table.data_ptr(), lens=lens.data_ptr(), out=out.data_ptr(),
-        lse=lse.data_ptr(), workspace=workspace.data_ptr(), workspace_bytes=workspace.numel(), q_row_stride=q.stride(0),
-        q_head_stride=q.stride(1), cache_page_stride=cache.stride(0), cache_row_stride=cache.stride(1),
-        table_stride=table.stride(0), out_row_stride=out.stride(0), out_head_stride=out.stride(1), batch=batch,
-        tokens=tokens, heads=heads, pages=pages, page=page, max_pages=max_pages, latent=LATENT, rope=rope_dim,
-        scale=_check_scale(scale))
-    with torch.cuda.device(dev):
-        st = lib().skinny_latent_decode_bf16(ctypes.byref(a), _stream_ptr(stream, dev))
-    check(st, "skinny_latent_decode_bf16")
+    if out is None or lse is None or workspace is None:
+        if q.dim() != 3:
+            raise ValueError("q must be 3-D")
+        if tokens < 1:
+            raise ValueError("tokens must be at least 1, got %d" % tokens)
+        rows, heads = q.shape[:2]
+        if out is None:
+            out = torch.empty((rows, heads, LATENT), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = latent_decode_workspace(rows // tokens, tokens, heads, LATENT, dev)
+    _call(_latent().decode, "skinny_latent_decode_bf16", dev, stream, q, cache, table, lens, scale, tokens, rope_dim, out,
+          lse, workspace)
     return out, lse
 
 
@@ -535,39 +435,20 @@ def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True
     strides (multiples of 8, contiguous last dimension). workspace: latent_prefill_workspace(nq,
     nk, batch, heads), allocated for this call where None. Returns (out, lse)."""
     dev = _gpu_of("q", q)
-    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("q and k must be 3-D tensors")
-    nq, heads = q.shape[:2]
-    nk = k.shape[0]
-    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 1:
-        raise ValueError("cu_q must be a tensor [batch + 1]")
-    batch = cu_q.shape[0] - 1
-    if out is None:
-        out = torch.empty((nq, heads, HEAD), dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty((nq, heads), dtype=torch.float32, device=dev)
-    _check_tensors(dev, {"q": (q, torch.bfloat16, (nq, heads, HEAD + ROPE)), "k": (k, torch.bfloat16, (nk, heads, HEAD)),
-                         "v": (v, torch.bfloat16, (nk, heads, HEAD)), "k_rot": (k_rot, torch.bfloat16, (nk, ROPE)),
-                         "cu_q": (cu_q, torch.int32, (batch + 1,)), "cu_k": (cu_k, torch.int32, (batch + 1,)),
-                         "out": (out, torch.bfloat16, (nq, heads, HEAD)), "lse": (lse, torch.float32, (nq, heads))})
-    _check_rows({"q": q, "k": k, "v": v, "k_rot": k_rot, "out": out})
-    if not (cu_q.is_contiguous() and cu_k.is_contiguous() and lse.is_contiguous()):
-        raise ValueError("cu_q, cu_k and lse must be contiguous")
-    if workspace is None:
-        workspace = latent_prefill_workspace(nq, nk, batch, heads, dev)
-    inputs = {"q": q, "k": k, "v": v, "k_rot": k_rot, "cu_q": cu_q, "cu_k": cu_k}
-    _no_overlap({"out": out, "lse": lse}, inputs)
-    _check_workspace(workspace, dev, dict(inputs, out=out, lse=lse))
-    a = SkinnyLatentPrefillArgs(
-        q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), k_rot=k_rot.data_ptr(), cu_q=cu_q.data_ptr(),
-        cu_k=cu_k.data_ptr(), out=out.data_ptr(), lse=lse.data_ptr(), workspace=workspace.data_ptr(),
-        workspace_bytes=workspace.numel(), q_row_stride=q.stride(0), q_head_stride=q.stride(1), k_row_stride=k.stride(0),
-        k_head_stride=k.stride(1), v_row_stride=v.stride(0), v_head_stride=v.stride(1), k_rot_stride=k_rot.stride(0),
-        out_row_stride=out.stride(0), out_head_stride=out.stride(1), nq=nq, nk=nk, batch=batch, heads=heads,
-        head_dim=HEAD, rope=ROPE, scale=_check_scale(scale), causal=int(bool(causal)))
-    with torch.cuda.device(dev):
-        st = lib().skinny_latent_prefill_bf16(ctypes.byref(a), _stream_ptr(stream, dev))
-    check(st, "skinny_latent_prefill_bf16")
+    if out is None or lse is None or workspace is None:
+        if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("q and k must be 3-D tensors")
+        if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 1:
+            raise ValueError("cu_q must be a tensor [batch + 1]")
+        nq, heads = q.shape[:2]
+        if out is None:
+            out = torch.empty((nq, heads, HEAD), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((nq, heads), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = latent_prefill_workspace(nq, k.shape[0], cu_q.shape[0] - 1, heads, dev)
+    _call(_latent().prefill, "skinny_latent_prefill_bf16", dev, stream, q, k, v, k_rot, cu_q, cu_k, scale, causal, out, lse,
+          workspace)
     return out, lse
 
 
