@@ -43,13 +43,53 @@ __device__ __forceinline__ void wait_stages(int later) {
     }
 }
 
-// Barrier ordering the workgroup's LDS accesses without waiting for outstanding
-// direct-to-LDS loads (each wave has already waited for the loads it needs).
+// Barrier ordering the workgroup's LDS accesses: this wave's LDS reads are done, outstanding
+// loads straight into LDS are not waited for (each wave has already waited for those it needs).
 __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);      // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
+}
+
+// ---- loads straight into LDS --------------------------------------------------------------
+// lane l's 16 bytes at src (4 with load_lds_word) go to LDS address lds + 16 l (4 l), and with N
+// pieces those at src + 128 i to lds + 1024 i + 16 l. lds is the same in all lanes. Written out
+// because the compiler does not know which staged bytes a read of LDS needs: behind the builtin it
+// waits for every load in flight before the next read, and the ring would hold one stage. Here
+// the kernel's own counted waits order the two. (No vector register is written; M0, which nothing
+// else in these kernels uses and the compiler never keeps, is given its required
+// wait state, and the instruction's offset counts in both addresses.)
+__device__ __forceinline__ int lds_address(lds_u8 *p) { return uniform((int)(uintptr_t)p); }
+
+__device__ __forceinline__ void load_lds_word(const void *src, int lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :: "s"(lds), "v"(src) : "memory");
+}
+
+#define SKINNY_NEXT_PIECE(o) "\n\ts_add_u32 m0, m0, 896\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:" #o
+template <int N>
+__device__ __forceinline__ void load_lds_pieces(const void *src, int lds) {
+    static_assert(N == 1 || N == 2 || N == 9, "pieces");
+    if constexpr (N == 1)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                     :: "s"(lds), "v"(src) : "memory");
+    else if constexpr (N == 2)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" SKINNY_NEXT_PIECE(128)
+                     :: "s"(lds), "v"(src) : "memory", "scc");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" SKINNY_NEXT_PIECE(128)
+                     SKINNY_NEXT_PIECE(256) SKINNY_NEXT_PIECE(384) SKINNY_NEXT_PIECE(512) SKINNY_NEXT_PIECE(640)
+                     SKINNY_NEXT_PIECE(768) SKINNY_NEXT_PIECE(896) SKINNY_NEXT_PIECE(1024)
+                     :: "s"(lds), "v"(src) : "memory", "scc");
+}
+#undef SKINNY_NEXT_PIECE
 
 // ---- staged key and value rows ----------------------------------------------------------
 // Rows come into LDS in blocks of 8 rows x 128 bytes (one direct-to-LDS instruction: lane l
@@ -158,6 +198,17 @@ __device__ __forceinline__ void split_value(u32x4_t f, u32x4_t &g, u32x4_t &a1, 
     }
 }
 __device__ __forceinline__ uint32_t seen_pair(bool lo, bool hi) { return (lo ? kBig : 0u) | (hi ? kBig << 16 : 0u); }
+
+// f with non-finite values as 0
+__device__ __forceinline__ u32x4_t finite_values(u32x4_t f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = (f[i] & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu;
+        const uint32_t hi = (f[i] & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u;
+        f[i] &= lo | hi;
+    }
+    return f;
+}
 
 // A row's reference maximum follows the scores' only when they pass it by more than this (in
 // powers of two): the sums then stay within 2^kSlack of their usual size, far inside fp32's

@@ -17,6 +17,7 @@
 //     of its rows (repeated by the WD waves: matrix time is spare, and no scores cross waves)
 //     and its dims of the output, so the only barrier is the ring's.
 #include <algorithm>
+#include <type_traits>
 
 #include "latent.hpp"
 
@@ -45,6 +46,7 @@ struct DecodeArgs {
     int64_t o_row, o_head;
     float *lse;
     float *work;                             // partial sums: see part_floats
+    int2 *cuts;                              // a unit (request and row group): its first partial, its last workgroup
     int batch, tokens, heads, pages, page, max_pages;
     int rows, groups, grid;                  // rows a request, row groups a request, workgroups
     float c;                                 // scale * log2(e)
@@ -111,14 +113,15 @@ __device__ void find_request(const DecodeArgs &a, int64_t x, int64_t *sh, int &r
         if (x < carry) break;                // uniform: carry and x are the same in every thread
     }
     __syncthreads();
-    req = (int)sh[4];
-    base = sh[5];
+    req = uniform((int)sh[4]);
+    base = uniform(sh[5]);
     __syncthreads();
 }
 
-// Workgroup b's run of the line: [b * total / grid, (b + 1) * total / grid).
+// Workgroup b's run of the line: [b * total / grid, (b + 1) * total / grid). Runs leave partials
+// 2b (of the run's first unit) and 2b + 1 (of its last, if that is another).
 __device__ __forceinline__ int64_t run_start(int64_t total, int grid, int b) { return total * b / grid; }
-// the workgroup whose run holds place x
+// the workgroup whose run holds place x (no run is empty: grid <= total)
 __device__ __forceinline__ int run_of(int64_t total, int grid, int64_t x) { return (int)(((x + 1) * grid - 1) / total); }
 
 template <typename T, int WR, int WD>
@@ -127,13 +130,15 @@ struct Shape {
     static constexpr int ND = L / T::DIMS / WD;          // dim tiles a wave
     static constexpr int KS = DIM / T::KSTEP;            // K steps of the score product
     static constexpr int NO4 = T::NO / 4;                // 4-register groups of a dim tile
+    // fragments read ahead of the matrix instructions (they need about 130 cycles; a 32 x 32
+    // instruction takes 32 of them): of keys, and of dim tiles of values
+    static constexpr int KG = WR == 4 ? 4 : 6, VG = ND >= 4 ? 2 : 1;
 };
 
 // One run of tiles [t0, t1) of one request and row group: the wave's sums, maximum and total.
 // limit: keys that the lane's row sees; first: the fewest that any row of the request sees.
 template <typename T, int WR, int WD>
-__device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, const u32x4_t (&qf)[Shape<T, WR, WD>::KS],
-                                          int req, int len, int t0, int t1, int limit, int first,
+__device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, const uint16_t *qp, int req, int len, int t0, int t1, int limit, int first,
                                           typename T::acc_t (&o)[Shape<T, WR, WD>::ND], float &m, float &l) {
     typedef Shape<T, WR, WD> S;
     typedef typename T::acc_t acc_t;
@@ -150,17 +155,13 @@ __device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, con
     const int32_t *trow = a.table + (int64_t)req * a.t_row;
     auto key_at = [&](int t) { return max(0, min(t * KT + kl, len - 1)); };
     auto fetch_id = [&](int t) {                         // page id of this lane's key of tile t
-        __builtin_amdgcn_global_load_lds((const void *)(trow + key_at(t) / a.page),
-                                         (lds_void *)(ids + (t % STAGES) * 256), 4, 0, 0);
+        load_lds_word(trow + key_at(t) / a.page, lds_address(ids + (t % STAGES) * 256));
     };
     auto issue = [&](int t, int id) {                    // tile t -> slot t % STAGES
         const int k = key_at(t);
         const int pg = min(max(id, 0), a.pages - 1);     // ids outside the pool are clamped
         const uint16_t *src = a.cache + (int64_t)pg * a.c_page + (int64_t)(k % a.page) * a.c_row + chunk;
-        lds_u8 *dst = ring + (t % STAGES) * STAGE_BYTES + wave * (SEGS * 1024);
-#pragma unroll
-        for (int s = 0; s < SEGS; ++s)
-            __builtin_amdgcn_global_load_lds((const void *)(src + s * 64), (lds_void *)(dst + s * 1024), 16, 0, 0);
+        load_lds_pieces<SEGS>(src, lds_address(ring + (t % STAGES) * STAGE_BYTES + wave * (SEGS * 1024)));
     };
     auto read_id = [&](int t) {
         return *(__attribute__((address_space(3))) const int32_t *)(ids + (t % STAGES) * 256 + lane * 4);
@@ -177,6 +178,10 @@ __device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, con
     int id0[STAGES - 1];
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) id0[s] = trow[key_at(t0 + s) / a.page];
+    asm volatile("" ::: "memory");                       // the queries' loads go out behind the ids'
+    u32x4_t qf[S::KS];
+#pragma unroll
+    for (int k = 0; k < S::KS; ++k) qf[k] = *reinterpret_cast<const u32x4_t *>(qp + k * T::KSTEP + grp * 8);
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {
         if (t0 + s < t1) {
@@ -225,7 +230,8 @@ __device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, con
     // S^T = K Q^T. Fragments are read a group ahead of their matrix instructions; the scheduling
     // barriers keep the compiler from reading whole tiles ahead and spilling
     auto scores = [&]() {
-        constexpr int KG = KA * NT / 2, NG = S::KS * NT / KG;    // fragments a group, groups
+        constexpr int KG = S::KG, NG = S::KS * NT / KG;  // fragments a group, groups
+        static_assert(KG * NG == S::KS * NT, "whole groups");
         auto key_frag = [&](int e) {
             const int k = e / NT, u = e % NT;
             return *(const lds_u32x4 *)(st + koff[k % KA] + (u * T::ROWS / 8) * (SEGS * 1024) + (k / KA) * 1024);
@@ -281,87 +287,77 @@ __device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, con
         }
         return f;
     };
-    // O^T += V^T P^T
-    auto add_values = [&]() {
-        u32x4_t vf[2][XS];
+    // O^T += V^T P^T; with clean, non-finite values count as 0
+    auto add_values = [&](auto clean) {
+        constexpr int VG = S::VG;
+        u32x4_t vf[2][VG * XS];
 #pragma unroll
-        for (int x = 0; x < XS; ++x) vf[0][x] = value(0, x);
+        for (int e = 0; e < VG * XS; ++e) vf[0][e] = value(e / XS, e % XS);
 #pragma unroll
-        for (int i = 0; i < S::ND; ++i) {
+        for (int i = 0; i < S::ND; i += VG) {
             __builtin_amdgcn_sched_barrier(0);
-            if (i + 1 < S::ND) {
+            if (i + VG < S::ND) {
 #pragma unroll
-                for (int x = 0; x < XS; ++x) vf[(i + 1) & 1][x] = value(i + 1, x);
+                for (int e = 0; e < VG * XS; ++e) vf[(i / VG + 1) & 1][e] = value(i + VG + e / XS, e % XS);
             }
 #pragma unroll
-            for (int x = 0; x < XS; ++x) o[i] = T::mfma(vf[i & 1][x], pf[x], o[i]);
+            for (int e = 0; e < VG * XS; ++e) {
+                u32x4_t f = vf[i / VG & 1][e];
+                if constexpr (clean.value) f = finite_values(f);
+                o[i + e / XS] = T::mfma(f, pf[e % XS], o[i + e / XS]);
+            }
         }
     };
     in_acc(o);
+    in_vgpr(qf);                                         // their wait is here, not in the loop
 
-    // The inner loop is the common tile: every row sees all of it and no reference maximum
-    // moves. It has no branches, so the output sums stay in their registers.
-    const int whole = min(t1, first / KT);               // tiles before this are seen whole by every row
-    for (int t = t0; t < t1; ++t) {
+    // The inner loop has no branch that touches the output sums: one that did would move all of
+    // them between register files in every iteration. A reference maximum that moves and a
+    // masked score that is not finite leave the loop and come back.
+    const int whole = first / KT;                        // tiles before this are seen whole by every row
+    bool scored = false;                                 // tile t's scores are at hand
+    for (int t = t0; t < t1;) {
         float top;
-        bool have = false;
-        while (t < whole) {
-            stage(t);
-            scores();
-            top = largest();
-            if (__any(top > m + kSlack)) {
-                have = true;
-                break;
+        bool odd = false;
+        do {
+            if (!scored) {
+                stage(t);
+                scores();
+                if (t >= whole) {
+#pragma unroll
+                    for (int i = 0; i < T::NS; ++i) {
+                        const float x = s[i / T::NO][i % T::NO];
+                        const bool seen = t * KT + T::place(i, grp) < limit, fin = finite_f32(x);
+                        // not finite: so is the key's row, or a query. A row that sees it gets NaN
+                        odd |= !fin;
+                        s[i / T::NO][i % T::NO] = seen ? (fin ? x : NAN) : -INFINITY;
+                    }
+                    odd = __any(odd);
+                }
+                top = largest();
+                if (odd || __any(top > m + kSlack)) break;
             }
             weights(m == -INFINITY ? 0.0f : m);
-            add_values();
-            ++t;
-        }
+            add_values(std::false_type());
+            scored = false;
+        } while (++t < t1);
         if (t >= t1) break;
-        if (!have) {
-            stage(t);
-            scores();
-        }
-        bool odd = false;
-        if (t >= whole) {
-#pragma unroll
-            for (int i = 0; i < T::NS; ++i) {
-                const bool seen = t * KT + T::place(i, grp) < limit;
-                odd |= !finite_f32(s[i / T::NO][i % T::NO]);     // so is the key's row, or a query
-                s[i / T::NO][i % T::NO] = seen ? s[i / T::NO][i % T::NO] : -INFINITY;
-            }
-            top = largest();
-        }
         const float n = fmaxf(m, top);
-        if (__any(n > m + kSlack)) {
-            const float alpha = n == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - n);
-            m = n;
-            l *= alpha;
+        const float alpha = n == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - n);
+        m = n;
+        l *= alpha;
 #pragma unroll
-            for (int i = 0; i < S::ND; ++i) o[i] *= alpha;
+        for (int i = 0; i < S::ND; ++i) {
+            o[i] *= alpha;
             in_acc(o);
         }
-        weights(m == -INFINITY ? 0.0f : m);
-        if (!__any(odd)) {
-            add_values();
-        } else {                                         // rare: see split_value
-            u32x4_t see[XS];
-#pragma unroll
-            for (int j = 0; j < T::NS; j += 2)
-                see[j / 8][j % 8 / 2] = seen_pair(t * KT + T::place(j, grp) < limit, t * KT + T::place(j + 1, grp) < limit);
-#pragma unroll
-            for (int i = 0; i < S::ND; ++i)
-#pragma unroll
-                for (int x = 0; x < XS; ++x) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    u32x4_t g, a1, a2;
-                    split_value(value(i, x), g, a1, a2);
-                    o[i] = T::mfma(g, pf[x], o[i]);
-                    o[i] = T::mfma(a1, see[x], o[i]);
-                    o[i] = T::mfma(a2, see[x], o[i]);
-                }
+        scored = !odd;
+        if (odd) {                                       // rare
+            weights(m == -INFINITY ? 0.0f : m);
+            add_values(std::true_type());
+            in_acc(o);
+            ++t;
         }
-        in_acc(o);
     }
     l = row_sum<T>(l);
     wait_vmcnt<0>();
@@ -377,16 +373,17 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     const int row = T::row(lane), grp = T::grp(lane);
     const int wr = wave % WR, d0 = (wave / WR) * (L / WD);
 
-    const int64_t total = all_tiles(a, sh);
-    int64_t lo = run_start(total, a.grid, blockIdx.x);
-    const int64_t hi = run_start(total, a.grid, blockIdx.x + 1);
-    if (lo >= hi) return;
+    const int64_t total = uniform(all_tiles(a, sh));
+    const int grid = (int)min((int64_t)a.grid, total);
+    if ((int)blockIdx.x >= grid) return;
+    int64_t lo = run_start(total, grid, blockIdx.x);
+    const int64_t hi = run_start(total, grid, blockIdx.x + 1);
     int req;
     int64_t base;
     find_request(a, lo, sh, req, base);
     bool leading = true;                                 // the run's first piece
     while (lo < hi) {
-        const int len = request_len(a, req), tiles = request_tiles(a, req);
+        const int len = uniform(request_len(a, req)), tiles = max(1, (len + KT - 1) / KT);
         const int g = (int)((lo - base) / tiles), t0 = (int)((lo - base) % tiles);
         const int t1 = (int)min((int64_t)tiles, t0 + (hi - lo));
 
@@ -396,16 +393,16 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
         const int j = rc / a.heads, h = rc % a.heads;
         const int64_t qr = (int64_t)req * a.tokens + j;
         const uint16_t *qp = a.q + qr * a.q_row + h * a.q_head;
-        u32x4_t qf[S::KS];
-#pragma unroll
-        for (int k = 0; k < S::KS; ++k)
-            qf[k] = *reinterpret_cast<const u32x4_t *>(qp + k * T::KSTEP + grp * 8);
         const int limit = max(0, len - a.tokens + j + 1);        // keys this row sees
         const int first = max(0, len - a.tokens + 1);            // keys that the request's first token sees
         typename T::acc_t o[S::ND];
         float m, l;
-        run_tiles<T, WR, WD>(a, lds, qf, req, len, t0, t1, limit, first, o, m, l);
-        if (t0 == 0 && t1 == tiles) {
+        run_tiles<T, WR, WD>(a, lds, qp, req, len, t0, t1, limit, first, o, m, l);
+        const bool uncut = t0 == 0 && t1 == tiles;
+        if (t0 == 0 && tid == 0)
+            a.cuts[(int64_t)req * a.groups + g] = make_int2(
+                2 * blockIdx.x + (leading ? 0 : 1), uncut ? (int)blockIdx.x : run_of(total, grid, lo + tiles - 1));
+        if (uncut) {
             if (r < a.rows) {
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;   // no key: zeros
                 uint16_t *op = a.out + qr * a.o_row + h * a.o_head;
@@ -442,32 +439,24 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     }
 }
 
-// Joins the partial sums of a request's row group that was cut between workgroups. A workgroup
-// takes 64 float4 of the group's sums; its 4 waves take the partials in turn.
-template <typename T, int WR, int WD>
-__global__ __launch_bounds__(THREADS) void latent_join_kernel(DecodeArgs a) {
+// Joins the partial sums of the units that were cut between workgroups. A wave takes 64 float4 of a
+// unit's sums, WP waves take its partials in turn and meet in LDS; each asks for 4 partials at
+// once, since nothing but the latency of these loads bounds the kernel.
+template <typename T, int WR, int WD, int WP>
+__global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(DecodeArgs a) {
     typedef Shape<T, WR, WD> S;
-    __shared__ int64_t sh[8];
-    __shared__ f32x4_t so[4][64];
-    __shared__ float sm[4][64], sl[4][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    constexpr int PER = S::MB * L / 4 / 64;              // workgroups a unit
-    const int unit = blockIdx.x / PER, quad = blockIdx.x % PER;
+    constexpr int PER = S::MB * L / 4 / 64;              // waves' shares of a unit
+    constexpr int QUADS = WP > 4 ? 1 : 4 / WP;           // of them, a workgroup's
+    static_assert(PER % QUADS == 0, "whole workgroups a unit");
+    __shared__ f32x4_t so[WP > 1 ? QUADS * WP : 1][64];
+    __shared__ float sm[WP > 1 ? QUADS * WP : 1][64], sl[WP > 1 ? QUADS * WP : 1][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int unit = blockIdx.x / (PER / QUADS);
+    const int quad = blockIdx.x % (PER / QUADS) * QUADS + wave / WP, turn = wave % WP;
+    const int2 cut = a.cuts[unit];
+    const int b0 = cut.x >> 1, pieces = cut.y - b0 + 1;
+    if (pieces <= 1) return;
     const int req = unit / a.groups, g = unit % a.groups;
-    // place of the unit's first tile
-    int64_t v = 0, w = 0, total, before;
-    for (int i = tid; i < a.batch; i += THREADS) {
-        const int64_t n = request_tiles(a, i);
-        v += n;
-        if (i < req) w += n;
-    }
-    block_scan(w, sh, before);
-    block_scan(v, sh, total);
-    total *= a.groups;
-    const int tiles = request_tiles(a, req);
-    const int64_t x0 = before * a.groups + (int64_t)g * tiles, x1 = x0 + tiles;
-    const int b0 = run_of(total, a.grid, x0), b1 = run_of(total, a.grid, x1 - 1);
-    if (b0 == b1) return;
 
     // quad = (wave of the writer, 4-register group) in the partial's order; see the writer
     constexpr int PERW = S::ND * S::NO4;
@@ -483,21 +472,32 @@ __global__ __launch_bounds__(THREADS) void latent_join_kernel(DecodeArgs a) {
         l = l * ca + pl * cb;
         o = o * ca + po * cb;
     };
-    for (int b = b0 + wave; b <= b1; b += 4) {
-        const int64_t lo = run_start(total, a.grid, b);
-        if (lo == run_start(total, a.grid, b + 1)) continue;     // an empty run wrote nothing
-        // a run that began in an earlier unit left this one's partial in its second place
-        const float *part = a.work + (2 * (int64_t)b + (lo < x0 ? 1 : 0)) * part_floats<S::MB>();
-        merge(part[(int64_t)S::MB * L + row], part[(int64_t)S::MB * (L + 1) + row],
-              reinterpret_cast<const f32x4_t *>(part)[(int64_t)quad * 64 + lane]);
-    }
-    so[wave][lane] = o;
-    sm[wave][lane] = m;
-    sl[wave][lane] = l;
-    __syncthreads();
-    if (wave) return;
+    // partial j: the first workgroup's is its run's first or last, the others' their runs' first
+    auto partial = [&](int j) {
+        return a.work + (j == 0 ? (int64_t)cut.x : 2 * (int64_t)(b0 + j)) * part_floats<S::MB>();
+    };
+    for (int j = turn; j < pieces; j += 4 * WP) {
+        float pm[4], pl[4];
+        f32x4_t po[4];
 #pragma unroll
-    for (int u = 1; u < 4; ++u) merge(sm[u][lane], sl[u][lane], so[u][lane]);
+        for (int u = 0; u < 4; ++u) {
+            const float *part = partial(min(j + u * WP, pieces - 1));
+            pm[u] = part[(int64_t)S::MB * L + row];
+            pl[u] = part[(int64_t)S::MB * (L + 1) + row];
+            po[u] = reinterpret_cast<const f32x4_t *>(part)[(int64_t)quad * 64 + lane];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u * WP < pieces) merge(pm[u], pl[u], po[u]);
+    }
+    if constexpr (WP > 1) {
+        so[wave][lane] = o;
+        sm[wave][lane] = m;
+        sl[wave][lane] = l;
+        __syncthreads();
+        if (turn) return;
+        for (int u = 1; u < min(WP, pieces); ++u) merge(sm[wave + u][lane], sl[wave + u][lane], so[wave + u][lane]);
+    }
     const int r = g * S::MB + row;
     if (r >= a.rows) return;
     const int64_t qr = (int64_t)req * a.tokens + r / a.heads;
@@ -510,16 +510,26 @@ __global__ __launch_bounds__(THREADS) void latent_join_kernel(DecodeArgs a) {
         a.lse[qr * a.heads + h] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+template <typename T, int WR, int WD, int WP>
+hipError_t launch_join(const DecodeArgs &a, hipStream_t stream) {
+    constexpr int PER = Shape<T, WR, WD>::MB * L / 4 / 64, QUADS = WP > 4 ? 1 : 4 / WP;
+    const unsigned blocks = (unsigned)((int64_t)a.batch * a.groups * (PER / QUADS));
+    hipLaunchKernelGGL((latent_join_kernel<T, WR, WD, WP>), dim3(blocks), dim3(WP > 4 ? WP * 64 : 256), 0, stream, a);
+    return hipGetLastError();
+}
+
 template <typename T, int WR, int WD>
 hipError_t launch_shape(DecodeArgs a, hipStream_t stream) {
-    typedef Shape<T, WR, WD> S;
+    a.cuts = reinterpret_cast<int2 *>(a.work + 2 * a.grid * part_floats<Shape<T, WR, WD>::MB>());
     hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD>), dim3((unsigned)a.grid), dim3(THREADS), 0, stream, a);
     hipError_t err = hipGetLastError();
     // one workgroup takes every run whole: nothing to join
     if (err != hipSuccess || a.grid == 1) return err;
-    const unsigned join = (unsigned)((int64_t)a.batch * a.groups * (S::MB * L / 4 / 64));
-    hipLaunchKernelGGL((latent_join_kernel<T, WR, WD>), dim3(join), dim3(THREADS), 0, stream, a);
-    return hipGetLastError();
+    // waves that share a unit's partials: about as many as it has on average
+    const int64_t units = (int64_t)a.batch * a.groups;
+    if (a.grid > 16 * units) return launch_join<T, WR, WD, 16>(a, stream);
+    if (a.grid > 4 * units) return launch_join<T, WR, WD, 4>(a, stream);
+    return launch_join<T, WR, WD, 1>(a, stream);
 }
 
 // Rows a workgroup for a request of `rows` query rows: the smallest shape that holds them.
@@ -530,7 +540,8 @@ int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <
 int64_t latent_decode_workspace_bytes(int64_t batch, int64_t tokens, int64_t heads, int cus) {
     const int64_t rows = tokens * heads;
     if (batch == 0 || rows == 0) return 0;
-    return 2 * (int64_t)cus * block_rows(rows) * (L + 2) * (int64_t)sizeof(float);
+    const int mb = block_rows(rows);
+    return 2 * (int64_t)cus * mb * (L + 2) * (int64_t)sizeof(float) + batch * ((rows + mb - 1) / mb) * (int64_t)sizeof(int2);
 }
 
 hipError_t launch_latent_decode(const skinny_latent_decode_args &p, int cus, hipStream_t stream) {

@@ -99,12 +99,10 @@ __device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, co
             const uint16_t *kp = a.k + key * a.k_row + head * a.k_head + chunk;
             const uint16_t *rp = a.kr + key * a.kr_row + chunk;
             const uint16_t *vp = a.v + key * a.v_row + head * a.v_head + chunk;
-            lds_u8 *kd = st + rg * (KSEG * 1024), *vd = st + K_BYTES + rg * (VSEG * 1024);
-            __builtin_amdgcn_global_load_lds((const void *)kp, (lds_void *)kd, 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const void *)(kp + 64), (lds_void *)(kd + 1024), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const void *)rp, (lds_void *)(kd + 2048), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const void *)vp, (lds_void *)vd, 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const void *)(vp + 64), (lds_void *)(vd + 1024), 16, 0, 0);
+            const int kd = lds_address(st + rg * (KSEG * 1024)), vd = lds_address(st + K_BYTES + rg * (VSEG * 1024));
+            load_lds_pieces<2>(kp, kd);
+            load_lds_pieces<1>(rp, kd + 2048);
+            load_lds_pieces<2>(vp, vd);
         }
     };
 #pragma unroll
