@@ -12,6 +12,7 @@
 // Where the queries are too few to fill the chip, a row's keys are split over several
 // workgroups and their partial sums joined by a second kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "latent.hpp"
 
@@ -32,6 +33,9 @@ constexpr int KS = DQ / T::KSTEP;            // K steps of the score product
 constexpr int ND = HD / T::DIMS;             // dim tiles of the output
 constexpr int NT = KT / T::ROWS;             // key subtiles
 constexpr int NP = NT * T::NS;               // weights a lane holds
+
+// the place in a tile of a lane's weight j, counted from its first
+__host__ __device__ constexpr int place0(int j) { return j / T::NS * T::ROWS + 8 * (j % T::NS >> 2) + (j & 3); }
 
 struct PrefillArgs {
     const uint16_t *q, *k, *v, *kr;
@@ -54,6 +58,7 @@ __host__ __device__ inline int64_t split_floats(int64_t nq, int64_t heads) { ret
 __device__ __forceinline__ int start(const int32_t *cu, int i, int64_t n) { return (int)min((int64_t)max(cu[i], 0), n); }
 
 // The sequence whose query tiles hold tile `at`, counted over all sequences; -1: none.
+template <int BM>
 __device__ __forceinline__ int find_tile(const PrefillArgs &a, int at, int &tile) {
     const int lane = threadIdx.x & 63;
     int carry = 0;
@@ -150,9 +155,9 @@ __device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, co
         const int k0 = t * KT;
         const bool mixed = k0 + KT > first;
         if (mixed) {
+            const int left = limit - k0 - T::place(0, grp);      // keys from the lane's first on
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
-                p[i] = k0 + (i / T::NS) * T::ROWS + T::place(i % T::NS, grp) < limit ? p[i] : -INFINITY;
+            for (int i = 0; i < NP; ++i) p[i] = place0(i) < left ? p[i] : -INFINITY;
         }
         float top = p[0];
 #pragma unroll
@@ -198,10 +203,9 @@ __device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, co
         } else {
             u32x4_t see[NP / 8];
 #pragma unroll
-            for (int j = 0; j < NP; j += 2) {
-                const int key = k0 + (j / T::NS) * T::ROWS + T::place(j % T::NS, grp);
-                see[j / 8][j % 8 / 2] = seen_pair(key < limit, key + 1 < limit);
-            }
+            for (int j = 0; j < NP; j += 2)
+                see[j / 8][j % 8 / 2] = seen_pair(place0(j) < limit - k0 - T::place(0, grp),
+                                                  place0(j + 1) < limit - k0 - T::place(0, grp));
 #pragma unroll
             for (int x = 0; x < NP / 8; ++x)
 #pragma unroll
@@ -220,27 +224,27 @@ __device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, co
 
 // Whether the flag is set in any lane of the workgroup (in the ring's memory: two workgroups'
 // rings are all of a CU's LDS). The ring is free before and after.
+template <int N>
 __device__ __forceinline__ bool any_wave(bool flag, uint8_t *lds) {
     volatile int *w = reinterpret_cast<volatile int *>(lds);
     const bool mine = __any(flag);
     if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = mine;
     __syncthreads();
-    const bool any = w[0] | w[1] | w[2] | w[3];
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) any |= w[i];
     __syncthreads();
     return any;
 }
 
-__global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs a) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE_BYTES];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int row = T::row(lane), grp = T::grp(lane);
-    // Block order. Workgroups go to the XCDs in turn; where the heads divide evenly over them an
-    // XCD takes whole heads, one after the other, so that its L2 holds the keys and values its
-    // workgroups share. A head's last query tiles, which see the most keys, come first.
+// What workgroup blockIdx.x works on: split of the keys, head, query tile counted from the last.
+// Workgroups go to the XCDs in turn; where the heads divide evenly over them an XCD takes whole
+// heads, one after the other, so that its L2 holds the keys and values its workgroups share. A
+// head's last query tiles, which see the most keys, come first.
+__device__ __forceinline__ void block_order(const PrefillArgs &a, int &split, int &head, int &at) {
     int b = blockIdx.x;
-    const int split = b % a.splits;
+    split = b % a.splits;
     b /= a.splits;
-    int head, at;
     if (a.heads % 8 == 0 && a.splits == 1) {
         const int j = b >> 3;
         head = (b & 7) + 8 * (j / a.tiles);
@@ -249,39 +253,11 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs 
         head = b % a.heads;
         at = b / a.heads;
     }
-    int tile = 0;
-    const int seq = find_tile(a, a.tiles - 1 - at, tile);
-    if (seq < 0) return;
-    const int q0 = start(a.cu_q, seq, a.nq), lq = start(a.cu_q, seq + 1, a.nq) - q0;
-    const int k0 = start(a.cu_k, seq, a.nk), lk = max(0, start(a.cu_k, seq + 1, a.nk) - k0);
-    const int r = tile * BM + wave * T::ROWS + row, rc = min(r, lq - 1);
-    const int64_t qr = (int64_t)q0 + rc;
+}
 
-    u32x4_t qf[KS];
-    const uint16_t *qp = a.q + qr * a.q_row + head * a.q_head + grp * 8;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const u32x4_t *>(qp + k * T::KSTEP);
-
-    // keys that this row, the workgroup's first row and its last row see
-    auto sees = [&](int x) { return a.causal ? max(0, min(lk, lk - lq + 1 + x)) : lk; };
-    const int limit = sees(rc), first = sees(tile * BM), last = sees(min(tile * BM + BM, lq) - 1);
-    const int n = (last + KT - 1) / KT;
-    const int t0 = (int)((int64_t)n * split / a.splits), t1 = (int)((int64_t)n * (split + 1) / a.splits);
-    f32x16_t o[ND];
-    float m, l;
-    bool safe = false;
-    for (;;) {
-        run_tiles(a, lds, qf, head, k0, lk, t0, t1, limit, first, safe, o, m, l);
-        // a non-finite result where some rows see fewer keys than others: once more, key by key
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-            for (int j = 0; j < T::NO; ++j) odd |= !finite_f32(o[i][j]);
-        if (safe || !any_wave(odd && t1 * KT > first, lds)) break;
-        safe = true;
-    }
-    if (r >= lq) return;
+// A row's results: the output and lse, or its split's partial.
+__device__ __forceinline__ void put_row(const PrefillArgs &a, int split, int64_t qr, int head, int grp,
+                                        const f32x16_t (&o)[ND], float m, float l) {
     if (a.splits == 1) {
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;          // no key: zeros
         uint16_t *op = a.out + qr * a.o_row + head * a.o_head;
@@ -310,6 +286,268 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs 
     }
 }
 
+__device__ __forceinline__ bool not_finite(const f32x16_t (&o)[ND]) {
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int j = 0; j < T::NO; ++j) odd |= !finite_f32(o[i][j]);
+    return odd;
+}
+
+__global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int row = T::row(lane), grp = T::grp(lane);
+    int split, head, at;
+    block_order(a, split, head, at);
+    int tile = 0;
+    const int seq = find_tile<BM>(a, a.tiles - 1 - at, tile);
+    if (seq < 0) return;
+    const int q0 = start(a.cu_q, seq, a.nq), lq = start(a.cu_q, seq + 1, a.nq) - q0;
+    const int k0 = start(a.cu_k, seq, a.nk), lk = max(0, start(a.cu_k, seq + 1, a.nk) - k0);
+    const int r = tile * BM + wave * T::ROWS + row, rc = min(r, lq - 1);
+    const int64_t qr = (int64_t)q0 + rc;
+
+    u32x4_t qf[KS];
+    const uint16_t *qp = a.q + qr * a.q_row + head * a.q_head + grp * 8;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const u32x4_t *>(qp + k * T::KSTEP);
+
+    // keys that this row, the workgroup's first row and its last row see
+    auto sees = [&](int x) { return a.causal ? max(0, min(lk, lk - lq + 1 + x)) : lk; };
+    const int limit = sees(rc), first = sees(tile * BM), last = sees(min(tile * BM + BM, lq) - 1);
+    const int n = (last + KT - 1) / KT;
+    const int t0 = (int)((int64_t)n * split / a.splits), t1 = (int)((int64_t)n * (split + 1) / a.splits);
+    f32x16_t o[ND];
+    float m, l;
+    bool safe = false;
+    for (;;) {
+        run_tiles(a, lds, qf, head, k0, lk, t0, t1, limit, first, safe, o, m, l);
+        // a non-finite result where some rows see fewer keys than others: once more, key by key
+        if (safe || !any_wave<WAVES>(not_finite(o) && t1 * KT > first, lds)) break;
+        safe = true;
+    }
+    if (r < lq) put_row(a, split, qr, head, grp, o, m, l);
+}
+
+// ---- the wide form: 256 query rows a workgroup --------------------------------------------
+// 8 waves of 32 rows, two on each SIMD, that take turns: while waves 0 .. 3 run the matrix
+// instructions of a tile (the value product of the tile before, then its score product), waves
+// 4 .. 7 run their softmax, and the other way round; a barrier ends each turn. Left to themselves
+// two waves of a SIMD fall into step, and then neither hides the other (measured with the narrow
+// form at 8192 tokens x 32 heads: matrix and vector time add up, 890 TFLOP/s). Keys are
+// staged four tiles deep, values three.
+constexpr int WIDE_WAVES = 8, WIDE_THREADS = WIDE_WAVES * 64, WIDE_BM = WIDE_WAVES * T::ROWS;
+constexpr int V_BYTES = KT * HD * 2, K_RING = 4, V_RING = 3;
+constexpr int WIDE_LDS = K_RING * K_BYTES + V_RING * V_BYTES;
+constexpr int GROUP_LOADS = KSEG + VSEG;                 // a wave's, of a tile's keys and a tile's values
+static_assert(WIDE_WAVES * 8 == KT, "a wave stages 8 rows");
+
+__global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(PrefillArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[WIDE_LDS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int row = T::row(lane), grp = T::grp(lane);
+    int split, head, at, tile = 0;
+    block_order(a, split, head, at);
+    const int seq = find_tile<WIDE_BM>(a, a.tiles - 1 - at, tile);
+    if (seq < 0) return;
+    const int q0 = uniform(start(a.cu_q, seq, a.nq)), lq = uniform(start(a.cu_q, seq + 1, a.nq)) - q0;
+    const int k0 = uniform(start(a.cu_k, seq, a.nk)), lk = max(0, uniform(start(a.cu_k, seq + 1, a.nk)) - k0);
+    tile = uniform(tile);
+    const int r0 = tile * WIDE_BM + wave * T::ROWS;      // the wave's first row
+    auto sees = [&](int x) __attribute__((always_inline)) { return a.causal ? max(0, min(lk, lk - lq + 1 + x)) : lk; };
+    const int r = r0 + row, rc = min(r, lq - 1);
+    const int64_t qr = (int64_t)q0 + rc;
+    const int limit = sees(rc);
+    // key tiles: the workgroup's, and of them the wave's; whole: seen whole by every row of the wave
+    const int n = (sees(min(tile * WIDE_BM + WIDE_BM, lq) - 1) + KT - 1) / KT;
+    const int t0 = (int)((int64_t)n * split / a.splits), t1 = (int)((int64_t)n * (split + 1) / a.splits);
+    const int cnt = t1 - t0;
+    const int last = r0 < lq ? (sees(min(r0 + T::ROWS, lq) - 1) + KT - 1) / KT : 0;
+    const int cw = max(0, min(last, t1) - t0), first = sees(min(r0, lq - 1));
+    const int whole = max(0, first / KT - t0);
+
+    lds_u8 *kring = (lds_u8 *)lds, *vring = kring + K_RING * K_BYTES;
+    const int lrow = 8 * wave + (lane >> 3);             // staging: this lane's row of a tile
+    const int chunk = ((lane & 7) ^ swz(lrow)) * 8;
+    const uint16_t *kbase = a.k + head * a.k_head + chunk, *rbase = a.kr + chunk, *vbase = a.v + head * a.v_head + chunk;
+    // past the last tile it is loaded again, so that the counts stay even
+    auto key_of = [&](int i) __attribute__((always_inline)) { return (int64_t)k0 + min(min(t0 + i, t1 - 1) * KT + lrow, lk - 1); };
+    auto load_keys = [&](int i) __attribute__((always_inline)) {
+        const int64_t key = key_of(i);
+        const int dst = lds_address(kring + (i % K_RING) * K_BYTES + wave * (KSEG * 1024));
+        load_lds_pieces<2>(kbase + key * a.k_row, dst);
+        load_lds_pieces<1>(rbase + key * a.kr_row, dst + 2048);
+    };
+    auto load_values = [&](int i) __attribute__((always_inline)) {
+        load_lds_pieces<2>(vbase + key_of(i) * a.v_row, lds_address(vring + (i % V_RING) * V_BYTES + wave * (VSEG * 1024)));
+    };
+    int koff[4], voff[2][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        koff[j] = (row >> 3) * (KSEG * 1024) + (row & 7) * 128 + (((2 * j + grp) ^ swz(row)) << 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int x = 8 * hh + 4 * grp + ((lane & 15) >> 2);
+            const int ch = 4 * j + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+            voff[j][hh] = hh * (VSEG * 1024) + (x & 7) * 128 + ((ch ^ swz(x)) << 4) + (lane & 1) * 8;
+        }
+
+    u32x4_t qf[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+        qf[k] = *reinterpret_cast<const u32x4_t *>(a.q + qr * a.q_row + head * a.q_head + k * T::KSTEP + grp * 8);
+    f32x16_t o[ND], s[NT];
+    float m, l;
+    u32x4_t pf[NP / 8];
+
+    auto scores = [&](int i) __attribute__((always_inline)) {                           // S^T of tile i
+        lds_u8 *st = kring + (i % K_RING) * K_BYTES;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) s[u] = f32x16_t{0.0f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const u32x4_t kf = *(const lds_u32x4 *)(st + koff[k % 4] + u * (T::ROWS / 8) * (KSEG * 1024) + (k / 4) * 1024);
+                s[u] = T::mfma(kf, qf[k], s[u]);
+            }
+    };
+    auto softmax = [&](int i) __attribute__((always_inline)) {
+        if (i >= whole) {
+            const int left = limit - (t0 + i) * KT - T::place(0, grp);   // keys from the lane's first on
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+                s[j / T::NS][j % T::NS] = place0(j) < left ? s[j / T::NS][j % T::NS] : -INFINITY;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int j = 1; j < NP; ++j) top = fmaxf(top, s[j / T::NS][j % T::NS]);
+        top = row_max<T>(top) * a.c;
+        if (__any(top > m + kSlack)) {
+            const float next = fmaxf(m, top);
+            const float alpha = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+            m = next;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] *= alpha;
+        }
+        // weights are rounded to bf16 for the matrix product, see run_tiles
+        const float mu = m == -INFINITY ? 0.0f : m;
+        float p[NP];
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            p[j] = __builtin_amdgcn_exp2f(fmaf(s[j / T::NS][j % T::NS], a.c, -mu));
+            l += p[j];
+        }
+#pragma unroll
+        for (int j = 0; j < NP / 2; ++j) pf[j / 4][j % 4] = pack_bf16(p[2 * j], p[2 * j + 1]);
+    };
+    auto value = [&](int i, int d, int x) __attribute__((always_inline)) {              // tile i, dim tile d, 16 keys x
+        lds_u8 *st = vring + (i % V_RING) * V_BYTES;
+        u32x4_t f;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            lds_u8 *p = st + voff[d % 2][hh] + (d / 2) * 1024 + 2 * x * (VSEG * 1024);
+            const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+            f[2 * hh] = v[0];
+            f[2 * hh + 1] = v[1];
+        }
+        return f;
+    };
+    auto add_values = [&](int i, auto careful) __attribute__((always_inline)) {         // O^T += V^T P^T of tile i
+        if constexpr (careful.value) {                   // see split_value
+            const int left = limit - (t0 + i) * KT - T::place(0, grp);
+#pragma unroll
+            for (int x = 0; x < NP / 8; ++x) {
+                u32x4_t see;
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) see[j / 2] = seen_pair(place0(8 * x + j) < left, place0(8 * x + j + 1) < left);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    u32x4_t g, a1, a2;
+                    split_value(value(i, d, x), g, a1, a2);
+                    o[d] = T::mfma(g, pf[x], o[d]);
+                    o[d] = T::mfma(a1, see, o[d]);
+                    o[d] = T::mfma(a2, see, o[d]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < NP / 8; ++x)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) o[d] = T::mfma(value(i, d, x), pf[x], o[d]);
+        }
+    };
+    // Turn 2i: tile i's keys and tile i - 1's values are staged, and the stages of the keys of tile
+    // i - 2 and of the values of tile i - 2 are free: both groups are done with them
+    auto even_turn = [&](int i) __attribute__((always_inline)) {
+        wait_vmcnt<GROUP_LOADS>();
+        lds_barrier();
+        load_keys(i + 2);
+        load_values(i + 1);
+    };
+    const bool later = wave >= WIDE_WAVES / 2;           // these waves are one turn behind
+    auto matrix_turn = [&](int i) __attribute__((always_inline)) {                      // opens the turn of tile i's matrix instructions
+        if (later) lds_barrier();
+        else even_turn(i);
+    };
+    auto softmax_turn = [&](int i) __attribute__((always_inline)) {
+        if (later) even_turn(i + 1);
+        else lds_barrier();
+    };
+    auto pass = [&](auto careful) __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] = f32x16_t{0.0f};
+        m = -INFINITY;
+        l = 0.0f;
+        if (cnt <= 0) return;
+        load_keys(0);
+        load_keys(1);
+        load_values(0);
+        in_vgpr(qf);                                     // their wait is here, not in the loop
+        if (later) even_turn(0);
+        if (cw > 0) {
+            matrix_turn(0);
+            scores(0);
+            softmax_turn(0);
+            softmax(0);
+        }
+        for (int i = 1; i < cw; ++i) {
+            matrix_turn(i);
+            __builtin_amdgcn_s_setprio(1);
+            add_values(i - 1, careful);
+            scores(i);
+            __builtin_amdgcn_s_setprio(0);
+            softmax_turn(i);
+            softmax(i);
+        }
+        // the last value product, and turns of tiles that this wave's rows do not see
+        if (cw < cnt) matrix_turn(cw);
+        else if (!later) even_turn(cnt);
+        if (cw > 0) add_values(cw - 1, careful);
+        if (cw < cnt) {
+            softmax_turn(cw);
+            for (int i = cw + 1; i < cnt; ++i) {
+                matrix_turn(i);
+                softmax_turn(i);
+            }
+            if (!later) even_turn(cnt);
+        }
+        l = row_sum<T>(l);
+        wait_vmcnt<0>();
+        lds_barrier();
+    };
+    pass(std::false_type());
+    // a non-finite result where some rows see fewer keys than others: once more, with care
+    if (any_wave<WIDE_WAVES>(not_finite(o) && t1 * KT > sees(tile * WIDE_BM), lds)) pass(std::true_type());
+    if (r < lq) put_row(a, split, qr, head, grp, o, m, l);
+}
+
 // Joins the splits of a row and head: 32 lanes, 4 numbers each.
 __global__ __launch_bounds__(256) void latent_prefill_join_kernel(PrefillArgs a) {
     const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), all = a.nq * a.heads;
@@ -335,21 +573,30 @@ __global__ __launch_bounds__(256) void latent_prefill_join_kernel(PrefillArgs a)
     if (a.lse && x == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-int64_t query_tiles(int64_t nq, int64_t batch) { return std::min(nq, nq / BM + batch); }
-
-// Splits of the keys: as many as fill two workgroups a CU, while each keeps 8 key tiles of the
-// average sequence.
-int pick_splits(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus) {
-    const int64_t blocks = query_tiles(nq, batch) * heads;
+// How a call of these sizes runs. The wide form where sequences have rows to fill it.
+struct Plan {
+    bool wide;
+    int64_t tiles;                           // most query tiles that nq rows in batch sequences can need
+    int splits;
+};
+Plan plan(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus) {
+    Plan p;
+    p.wide = nq / batch >= 192;
+    const int bm = p.wide ? WIDE_BM : BM;
+    p.tiles = std::min(nq, nq / bm + batch);
+    // Splits of the keys: as many as fill the CUs (one wide workgroup each, or two narrow ones),
+    // while each keeps 8 key tiles of the average sequence
+    const int64_t room = (p.wide ? 1 : 2) * (int64_t)cus / std::max<int64_t>(1, p.tiles * heads);
     const int64_t most = std::max<int64_t>(1, nk / batch / (8 * KT));
-    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * (int64_t)cus / std::max<int64_t>(1, blocks), most, 32}));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({room, most, 32}));
+    return p;
 }
 
 }  // namespace
 
 int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus) {
     if (nq == 0 || batch == 0 || heads == 0) return 0;
-    const int s = pick_splits(nq, nk, batch, heads, cus);
+    const int s = plan(nq, nk, batch, heads, cus).splits;
     return s == 1 ? 0 : s * split_floats(nq, heads) * (int64_t)sizeof(float);
 }
 
@@ -377,11 +624,16 @@ hipError_t launch_latent_prefill(const skinny_latent_prefill_args &p, int cus, h
     a.nk = p.nk;
     a.batch = (int)p.batch;
     a.heads = (int)p.heads;
-    a.tiles = (int)query_tiles(p.nq, p.batch);
-    a.splits = pick_splits(p.nq, p.nk, p.batch, p.heads, cus);
+    const Plan how = plan(p.nq, p.nk, p.batch, p.heads, cus);
+    a.tiles = (int)how.tiles;
+    a.splits = how.splits;
     a.c = p.scale * kLog2e;
     a.causal = p.causal != 0;
-    hipLaunchKernelGGL(latent_prefill_kernel, dim3((unsigned)(a.tiles * a.heads * a.splits)), dim3(THREADS), 0, stream, a);
+    const dim3 grid((unsigned)(a.tiles * a.heads * a.splits));
+    if (how.wide)
+        hipLaunchKernelGGL(latent_prefill_wide_kernel, grid, dim3(WIDE_THREADS), 0, stream, a);
+    else
+        hipLaunchKernelGGL(latent_prefill_kernel, grid, dim3(THREADS), 0, stream, a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.splits == 1) return err;
     hipLaunchKernelGGL(latent_prefill_join_kernel, dim3((unsigned)((p.nq * a.heads + 7) / 8)), dim3(256), 0, stream, a);

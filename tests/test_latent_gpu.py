@@ -483,3 +483,38 @@ def test_binding_refuses(sk):
                 dict(workspace=small[::2])):
         with pytest.raises(ValueError):
             sk.latent_prefill(**{**ok, **bad})
+
+
+# ------------------------------------------------- prompts long enough for the wide workgroups
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,heads", [
+    ([192], [192], 1), ([255], [255], 3), ([256], [256], 8), ([257], [257], 2), ([511, 513], [511, 513], 2),
+    ([700, 0, 900], [700, 3, 900], 3), ([600, 1], [200, 5], 2), ([1100], [1100], 8), ([300], [63], 1), ([400], [0], 2),
+    ([260], [3000], 2), ([1000, 30, 64], [2500, 30, 65], 1)])
+def test_prefill_wide(sk, lq, lk, heads, causal):
+    prefill_case(sk, lq, lk, heads, causal, seed=sum(lk) + heads)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("heads,past", [(2, 0), (1, 4000)])
+def test_prefill_wide_hidden_values_may_be_anything(sk, heads, past, bad):
+    n0 = 300
+    lq, lk = [n0], [n0 + past]
+    q, k, v, r = prefill_inputs(gen(21), lq, lk, heads)
+    at = past + 170
+    v[at, :, 5] = bad
+    k[past + 290, :, 3] = math.nan
+    kv = torch.cat((k, v), -1).cuda()
+    out, lse = sk.latent_prefill(q.cuda(), kv[:, :, :HEAD], kv[:, :, HEAD:], r.cuda(), starts(lq), starts(lk), SCALE)
+    out, lse = out.cpu(), lse.cpu()
+    assert not bool(torch.isfinite(out[170:, :, 5]).any())
+    assert bool(torch.isnan(out[290:]).all()) and bool(torch.isnan(lse[290:]).all())
+    rest = [i for i in range(HEAD) if i != 5]
+    clean = v.clone()
+    clean[at, :, 5] = 0
+    n = past + 290
+    ref.check_prefill(out[:290][:, :, rest], lse[:290], q[:290], k[:n], clean[:n][:, :, rest], r[:n], [290], [n], SCALE,
+                      True, "rest")
+    n = past + 170
+    ref.check_prefill(out[:170], lse[:170], q[:170], k[:n], v[:n], r[:n], [170], [n], SCALE, True, "before")
