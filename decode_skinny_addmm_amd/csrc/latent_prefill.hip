@@ -336,10 +336,10 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs 
 // instructions of a tile (the value product of the tile before, then its score product), waves
 // 4 .. 7 run their softmax, and the other way round; a barrier ends each turn. Left to themselves
 // two waves of a SIMD fall into step, and then neither hides the other (measured with the narrow
-// form at 8192 tokens x 32 heads: matrix and vector time add up, 890 TFLOP/s). Keys are
-// staged four tiles deep, values three.
+// form at 8192 tokens x 32 heads: matrix and vector time add up, 890 TFLOP/s). Keys and
+// values are staged four tiles deep, all of a CU's LDS.
 constexpr int WIDE_WAVES = 8, WIDE_THREADS = WIDE_WAVES * 64, WIDE_BM = WIDE_WAVES * T::ROWS;
-constexpr int V_BYTES = KT * HD * 2, K_RING = 4, V_RING = 3;
+constexpr int V_BYTES = KT * HD * 2, K_RING = 4, V_RING = 4;
 constexpr int WIDE_LDS = K_RING * K_BYTES + V_RING * V_BYTES;
 constexpr int GROUP_LOADS = KSEG + VSEG;                 // a wave's, of a tile's keys and a tile's values
 static_assert(WIDE_WAVES * 8 == KT, "a wave stages 8 rows");
@@ -374,14 +374,12 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
     const uint16_t *kbase = a.k + head * a.k_head + chunk, *rbase = a.kr + chunk, *vbase = a.v + head * a.v_head + chunk;
     // past the last tile it is loaded again, so that the counts stay even
     auto key_of = [&](int i) __attribute__((always_inline)) { return (int64_t)k0 + min(min(t0 + i, t1 - 1) * KT + lrow, lk - 1); };
-    auto load_keys = [&](int i) __attribute__((always_inline)) {
+    auto load = [&](int i) __attribute__((always_inline)) {
         const int64_t key = key_of(i);
-        const int dst = lds_address(kring + (i % K_RING) * K_BYTES + wave * (KSEG * 1024));
-        load_lds_pieces<2>(kbase + key * a.k_row, dst);
-        load_lds_pieces<1>(rbase + key * a.kr_row, dst + 2048);
-    };
-    auto load_values = [&](int i) __attribute__((always_inline)) {
-        load_lds_pieces<2>(vbase + key_of(i) * a.v_row, lds_address(vring + (i % V_RING) * V_BYTES + wave * (VSEG * 1024)));
+        const int kd = lds_address(kring + (i % K_RING) * K_BYTES + wave * (KSEG * 1024));
+        load_lds_pieces<2>(kbase + key * a.k_row, kd);
+        load_lds_pieces<1>(rbase + key * a.kr_row, kd + 2048);
+        load_lds_pieces<2>(vbase + key * a.v_row, lds_address(vring + (i % V_RING) * V_BYTES + wave * (VSEG * 1024)));
     };
     int koff[4], voff[2][2];
 #pragma unroll
@@ -404,18 +402,6 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
     float m, l;
     u32x4_t pf[NP / 8];
 
-    auto scores = [&](int i) __attribute__((always_inline)) {                           // S^T of tile i
-        lds_u8 *st = kring + (i % K_RING) * K_BYTES;
-#pragma unroll
-        for (int u = 0; u < NT; ++u) s[u] = f32x16_t{0.0f};
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                const u32x4_t kf = *(const lds_u32x4 *)(st + koff[k % 4] + u * (T::ROWS / 8) * (KSEG * 1024) + (k / 4) * 1024);
-                s[u] = T::mfma(kf, qf[k], s[u]);
-            }
-    };
     auto softmax = [&](int i) __attribute__((always_inline)) {
         if (i >= whole) {
             const int left = limit - (t0 + i) * KT - T::place(0, grp);   // keys from the lane's first on
@@ -446,59 +432,99 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
 #pragma unroll
         for (int j = 0; j < NP / 2; ++j) pf[j / 4][j % 4] = pack_bf16(p[2 * j], p[2 * j + 1]);
     };
-    auto value = [&](int i, int d, int x) __attribute__((always_inline)) {              // tile i, dim tile d, 16 keys x
-        lds_u8 *st = vring + (i % V_RING) * V_BYTES;
+    // Places of a staged tile's fragments, one register each; the rest of an address is in the
+    // instruction. (Held in a register so that the compiler does not keep one for every fragment.)
+    auto place_of = [&](lds_u8 *st, int off) __attribute__((always_inline)) {
+        int at = (int)(uintptr_t)st + off;
+        asm volatile("" : "+v"(at));
+        return (lds_u8 *)(uintptr_t)(uint32_t)at;
+    };
+    lds_u8 *kat[4], *vat[2][2];
+    auto find_keys = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kat[j] = place_of(kring + (i % K_RING) * K_BYTES, koff[j]);
+    };
+    auto find_values = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vat[j / 2][j % 2] = place_of(vring + (i % V_RING) * V_BYTES, voff[j / 2][j % 2]);
+    };
+    auto value = [&](int d, int x) __attribute__((always_inline)) {      // dim tile d, 16 keys x
         u32x4_t f;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-            lds_u8 *p = st + voff[d % 2][hh] + (d / 2) * 1024 + 2 * x * (VSEG * 1024);
+            lds_u8 *p = vat[d % 2][hh] + (d / 2) * 1024 + 2 * x * (VSEG * 1024);
             const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
             f[2 * hh] = v[0];
             f[2 * hh + 1] = v[1];
         }
         return f;
     };
-    auto add_values = [&](int i, auto careful) __attribute__((always_inline)) {         // O^T += V^T P^T of tile i
-        if constexpr (careful.value) {                   // see split_value
-            const int left = limit - (t0 + i) * KT - T::place(0, grp);
+    // Matrix instructions of a turn: the value product of the tile before (O^T += V^T P^T), the
+    // score product of this one (S^T = K Q^T), or both. Fragments are read from LDS a group ahead
+    // (a read takes some 130 cycles, more when four waves read; an instruction takes 32), the
+    // first group of the value product before the turn; the scheduling barriers keep the groups
+    // apart.
+    constexpr int G = 8, NV = NP / 8 * ND, NK = KS * NT;
+    static_assert(NV % G == 0 && NK % G == 0, "whole groups");
+    u32x4_t f[2][G];
+    auto key_group = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-            for (int x = 0; x < NP / 8; ++x) {
-                u32x4_t see;
+        for (int e = g * G; e < g * G + G; ++e)
+            f[g & 1][e % G] = *(const lds_u32x4 *)(kat[e / NT % 4] + e % NT * (T::ROWS / 8) * (KSEG * 1024) + e / NT / 4 * 1024);
+    };
+    auto value_group = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) see[j / 2] = seen_pair(place0(8 * x + j) < left, place0(8 * x + j + 1) < left);
+        for (int e = g * G; e < g * G + G; ++e) f[g & 1][e % G] = value(e % ND, e / ND);
+    };
+    static_assert(NV / G % 2 == 0, "the key groups follow in the other half of f");
+    auto value_products = [&](bool keys_follow) __attribute__((always_inline)) {
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    u32x4_t g, a1, a2;
-                    split_value(value(i, d, x), g, a1, a2);
-                    o[d] = T::mfma(g, pf[x], o[d]);
-                    o[d] = T::mfma(a1, see, o[d]);
-                    o[d] = T::mfma(a2, see, o[d]);
-                }
-            }
-        } else {
+        for (int g = 0; g < NV / G; ++g) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (g + 1 < NV / G) value_group(g + 1);
+            else if (keys_follow) key_group(0);
 #pragma unroll
-            for (int x = 0; x < NP / 8; ++x)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) o[d] = T::mfma(value(i, d, x), pf[x], o[d]);
+            for (int e = g * G; e < g * G + G; ++e) o[e % ND] = T::mfma(f[g & 1][e % G], pf[e / ND], o[e % ND]);
         }
     };
-    // Turn 2i: tile i's keys and tile i - 1's values are staged, and the stages of the keys of tile
-    // i - 2 and of the values of tile i - 2 are free: both groups are done with them
-    auto even_turn = [&](int i) __attribute__((always_inline)) {
+    auto score_products = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int g = 0; g < NK / G; ++g) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (g + 1 < NK / G) key_group(g + 1);
+#pragma unroll
+            for (int e = g * G; e < g * G + G; ++e)
+                s[e % NT] = T::mfma(f[g & 1][e % G], qf[e / NT], e / NT ? s[e % NT] : f32x16_t{0.0f});
+        }
+    };
+    // the value product where a value that is not finite may reach only the rows that see it
+    auto value_products_carefully = [&](int i) __attribute__((always_inline)) {
+        const int left = limit - (t0 + i) * KT - T::place(0, grp);
+#pragma unroll
+        for (int x = 0; x < NP / 8; ++x) {
+            u32x4_t see;
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) see[j / 2] = seen_pair(place0(8 * x + j) < left, place0(8 * x + j + 1) < left);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                __builtin_amdgcn_sched_barrier(0);
+                u32x4_t g, a1, a2;
+                split_value(value(d, x), g, a1, a2);
+                o[d] = T::mfma(g, pf[x], o[d]);
+                o[d] = T::mfma(a1, see, o[d]);
+                o[d] = T::mfma(a2, see, o[d]);
+            }
+        }
+    };
+    // Turns. Waves 0 .. 3 have their matrix turn of tile i in turn 2i of the workgroup and their
+    // softmax turn in 2i + 1, the later ones each one turn after. A wave loads its share of a tile's
+    // keys and values at the start of its softmax turn of two (the later waves: three) tiles before
+    // and waits for it at the end of the next one, whose barrier shows it to all in time. The
+    // stages filled held a tile that both groups are done with.
+    const bool later = wave >= WIDE_WAVES / 2;
+    auto next_turn = [&]() __attribute__((always_inline)) {
         wait_vmcnt<GROUP_LOADS>();
         lds_barrier();
-        load_keys(i + 2);
-        load_values(i + 1);
-    };
-    const bool later = wave >= WIDE_WAVES / 2;           // these waves are one turn behind
-    auto matrix_turn = [&](int i) __attribute__((always_inline)) {                      // opens the turn of tile i's matrix instructions
-        if (later) lds_barrier();
-        else even_turn(i);
-    };
-    auto softmax_turn = [&](int i) __attribute__((always_inline)) {
-        if (later) even_turn(i + 1);
-        else lds_barrier();
     };
     auto pass = [&](auto careful) __attribute__((always_inline)) {
 #pragma unroll
@@ -506,38 +532,50 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
         m = -INFINITY;
         l = 0.0f;
         if (cnt <= 0) return;
-        load_keys(0);
-        load_keys(1);
-        load_values(0);
+        for (int i = 0; i < (later ? 3 : 2); ++i) load(i);
         in_vgpr(qf);                                     // their wait is here, not in the loop
-        if (later) even_turn(0);
+        wait_vmcnt<0>();
+        lds_barrier();
+        if (later) lds_barrier();
         if (cw > 0) {
-            matrix_turn(0);
-            scores(0);
-            softmax_turn(0);
+            find_keys(0);
+            key_group(0);
+            score_products();
+            next_turn();
+            load(later ? 3 : 2);
             softmax(0);
+            find_values(0);
+            if constexpr (!careful.value) value_group(0);
+            next_turn();
         }
         for (int i = 1; i < cw; ++i) {
-            matrix_turn(i);
+            find_keys(i);
             __builtin_amdgcn_s_setprio(1);
-            add_values(i - 1, careful);
-            scores(i);
-            __builtin_amdgcn_s_setprio(0);
-            softmax_turn(i);
-            softmax(i);
-        }
-        // the last value product, and turns of tiles that this wave's rows do not see
-        if (cw < cnt) matrix_turn(cw);
-        else if (!later) even_turn(cnt);
-        if (cw > 0) add_values(cw - 1, careful);
-        if (cw < cnt) {
-            softmax_turn(cw);
-            for (int i = cw + 1; i < cnt; ++i) {
-                matrix_turn(i);
-                softmax_turn(i);
+            if constexpr (careful.value) {
+                value_products_carefully(i - 1);
+                key_group(0);
+            } else {
+                value_products(true);
             }
-            if (!later) even_turn(cnt);
+            score_products();
+            __builtin_amdgcn_s_setprio(0);
+            next_turn();
+            load(later ? i + 3 : i + 2);
+            softmax(i);
+            find_values(i);
+            if constexpr (!careful.value) value_group(0);
+            next_turn();
         }
+        if (cw > 0) {
+            if constexpr (careful.value) value_products_carefully(cw - 1);
+            else value_products(false);
+        }
+        for (int i = cw; i < cnt; ++i) {                 // tiles that this wave's rows do not see
+            next_turn();
+            load(later ? i + 3 : i + 2);
+            next_turn();
+        }
+        if (!later) lds_barrier();
         l = row_sum<T>(l);
         wait_vmcnt<0>();
         lds_barrier();
