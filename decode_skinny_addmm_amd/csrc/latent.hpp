@@ -114,7 +114,7 @@ struct Tile32 {                 // v_mfma_f32_32x32x16_bf16: 32 rows per wave
     static __device__ __forceinline__ int row(int lane) { return lane & 31; }
     static __device__ __forceinline__ int grp(int lane) { return lane >> 5; }
     // accumulator register i of lane group g holds matrix row (key or dim) place(i, g)
-    static __device__ __forceinline__ int place(int i, int g) { return 8 * (i >> 2) + 4 * g + (i & 3); }
+    static __host__ __device__ __forceinline__ constexpr int place(int i, int g) { return 8 * (i >> 2) + 4 * g + (i & 3); }
 };
 struct Tile16 {                 // v_mfma_f32_16x16x32_bf16: 16 rows per wave
     static constexpr int ROWS = 16, KSTEP = 32, NS = 8, NO = 4, DIMS = 16;
@@ -125,7 +125,7 @@ struct Tile16 {                 // v_mfma_f32_16x16x32_bf16: 16 rows per wave
     }
     static __device__ __forceinline__ int row(int lane) { return lane & 15; }
     static __device__ __forceinline__ int grp(int lane) { return lane >> 4; }
-    static __device__ __forceinline__ int place(int i, int g) { return 16 * (i >> 2) + 4 * g + (i & 3); }
+    static __host__ __device__ __forceinline__ constexpr int place(int i, int g) { return 16 * (i >> 2) + 4 * g + (i & 3); }
 };
 
 // The largest / the sum of v over the lane groups that share a row.

@@ -31,7 +31,7 @@ constexpr int KT = 32;                       // keys a tile
 constexpr int SEGS = DIM * 2 / 128;          // 128-byte pieces of a row
 constexpr int STAGES = 4;
 constexpr int STAGE_BYTES = KT * DIM * 2;
-constexpr int PW = SEGS + 1;                 // loads a wave issues per stage: pieces and page id
+constexpr int PW = SEGS + 1;                 // loads a wave issues per stage: a page id and pieces
 constexpr int THREADS = 256;
 
 struct DecodeArgs {
@@ -49,6 +49,8 @@ struct DecodeArgs {
     int2 *cuts;                              // a unit (request and row group): its first partial, its last workgroup
     int batch, tokens, heads, pages, page, max_pages;
     int rows, groups, grid;                  // rows a request, row groups a request, workgroups
+    uint32_t page_mul;                       // k / page = (k * page_mul) >> (32 + page_shift); 0: page is 1
+    int page_shift;
     float c;                                 // scale * log2(e)
 };
 
@@ -56,10 +58,15 @@ struct DecodeArgs {
 template <int MB>
 __host__ __device__ constexpr int64_t part_floats() { return (int64_t)MB * (L + 2); }
 
-__device__ __forceinline__ int request_len(const DecodeArgs &a, int i) {
-    const int64_t cap = (int64_t)a.max_pages * a.page;
-    const int n = max(a.lens[i], 0);
-    return cap < n ? (int)cap : n;
+__device__ __forceinline__ int clamp_len(const DecodeArgs &a, int n) {
+    return min(max(n, 0), a.max_pages * a.page);         // at most 2^30: checked by the caller
+}
+__device__ __forceinline__ int request_len(const DecodeArgs &a, int i) { return clamp_len(a, a.lens[i]); }
+// the same for a request that is the same in all lanes, as a scalar load: waiting for a vector
+// load would wait for the ring's loads too
+__device__ __forceinline__ int uniform_len(const DecodeArgs &a, int i) {
+    typedef const __attribute__((address_space(4))) int32_t *constant_ptr;
+    return clamp_len(a, ((constant_ptr)(uintptr_t)a.lens)[i]);
 }
 // tiles of a request; one at least, so that an empty one's outputs are written too
 __device__ __forceinline__ int request_tiles(const DecodeArgs &a, int i) {
@@ -88,35 +95,33 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &t
     return before + s - v;
 }
 
-// Total tiles over all requests and row groups.
-__device__ int64_t all_tiles(const DecodeArgs &a, int64_t *sh) {
-    int64_t v = 0, total;
-    for (int i = threadIdx.x; i < a.batch; i += THREADS) v += request_tiles(a, i);
-    block_scan(v, sh, total);
-    return total * a.groups;
-}
-
-// The request that place x of the line of tiles belongs to, and the place of its first tile.
-// sh: 8 words; the caller's threads all get the answer.
-__device__ void find_request(const DecodeArgs &a, int64_t x, int64_t *sh, int &req, int64_t &base) {
-    int64_t carry = 0;
-    for (int i0 = 0; i0 < a.batch; i0 += THREADS) {
-        const int i = i0 + threadIdx.x;
-        const int64_t v = i < a.batch ? (int64_t)request_tiles(a, i) * a.groups : 0;
-        int64_t total;
-        const int64_t at = carry + block_scan(v, sh, total);
-        if (v > 0 && at <= x && x < at + v) {
-            sh[4] = i;
-            sh[5] = at;
-        }
-        carry += total;
-        if (x < carry) break;                // uniform: carry and x are the same in every thread
+// Where the line of tiles lies: its length, and for place x the request it belongs to and the place
+// of that request's first tile. Thread i counts requests i * per .. i * per + per - 1.
+struct Line {
+    int64_t total, before;                   // of this thread's requests
+    int per;
+    __device__ __forceinline__ void measure(const DecodeArgs &a, int64_t *sh) {
+        per = (a.batch + THREADS - 1) / THREADS;
+        int64_t v = 0;
+        for (int i = threadIdx.x * per; i < min(a.batch, (int)(threadIdx.x + 1) * per); ++i) v += request_tiles(a, i);
+        before = block_scan(v * a.groups, sh, total);
+        total = uniform(total);
     }
-    __syncthreads();
-    req = uniform((int)sh[4]);
-    base = uniform(sh[5]);
-    __syncthreads();
-}
+    __device__ __forceinline__ void find(const DecodeArgs &a, int64_t x, int64_t *sh, int &req, int64_t &base) const {
+        int64_t at = before;
+        for (int i = threadIdx.x * per; i < min(a.batch, (int)(threadIdx.x + 1) * per); ++i) {
+            const int64_t n = (int64_t)request_tiles(a, i) * a.groups;
+            if (at <= x && x < at + n) {
+                sh[4] = i;
+                sh[5] = at;
+            }
+            at += n;
+        }
+        __syncthreads();
+        req = uniform((int)sh[4]);
+        base = uniform(sh[5]);
+    }
+};
 
 // Workgroup b's run of the line: [b * total / grid, (b + 1) * total / grid). Runs leave partials
 // 2b (of the run's first unit) and 2b + 1 (of its last, if that is another).
@@ -132,112 +137,207 @@ struct Shape {
     static constexpr int NO4 = T::NO / 4;                // 4-register groups of a dim tile
     // fragments read ahead of the matrix instructions (they need about 130 cycles; a 32 x 32
     // instruction takes 32 of them): of keys, and of dim tiles of values
-    static constexpr int KG = WR == 4 ? 4 : 6, VG = ND >= 4 ? 2 : 1;
+    // softmax of a tile beside the score product of the next: takes registers that 128 rows x 512
+    // sums leave no room for
+    static constexpr bool FLOW = WR < 4;
+    static constexpr int KG = WR == 4 ? 4 : 6, VG = WR < 4 && ND >= 4 ? 2 : 1;
 };
 
-// One run of tiles [t0, t1) of one request and row group: the wave's sums, maximum and total.
-// limit: keys that the lane's row sees; first: the fewest that any row of the request sees.
+// What a workgroup stages, in order: for each unit (request and row group) of its run, the unit's
+// query rows as QT tiles of 32 rows, then its tiles of keys. One stream through the ring, so that
+// a unit's first tiles are loaded while the last one's outputs are written.
+struct Cursor {
+    int req, g, len, tiles, t, t0, end;      // unit; next item: query tile t + QT if t < 0, else key tile t
+    int64_t left;                            // key tiles of the run from this unit on
+    bool more;
+    __device__ __forceinline__ void enter(const DecodeArgs &a, int first, int qt) {
+        len = uniform_len(a, req);
+        tiles = max(1, (len + KT - 1) / KT);
+        t = -qt;
+        t0 = first;
+        end = (int)min((int64_t)tiles, first + left);
+    }
+};
+// An item whose load is due: this lane's row (of the request's queries, or of its cache page).
+struct Due {
+    int row, req;
+    int kind;                                // 0: none, 1: queries, 2: keys
+};
+
 template <typename T, int WR, int WD>
-__device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, const uint16_t *qp, int req, int len, int t0, int t1, int limit, int first,
-                                          typename T::acc_t (&o)[Shape<T, WR, WD>::ND], float &m, float &l) {
+__global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     typedef Shape<T, WR, WD> S;
     typedef typename T::acc_t acc_t;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE_BYTES + 4 * STAGES * 256];
+    __shared__ int64_t sh[8];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int row = T::row(lane), grp = T::grp(lane);
-    const int d0 = (wave / WR) * (L / WD);               // this wave's first latent dim
+    const int wr = wave % WR, d0 = (wave / WR) * (L / WD);
+    constexpr int QT = (S::MB + KT - 1) / KT;            // query tiles a unit
+
+    Line line;
+    line.measure(a, sh);
+    const int grid = (int)min((int64_t)a.grid, line.total);
+    if ((int)blockIdx.x >= grid) return;
+    int64_t lo = run_start(line.total, grid, blockIdx.x);
+    const int64_t hi = run_start(line.total, grid, blockIdx.x + 1);
+    int req;
+    int64_t base;
+    line.find(a, lo, sh, req, base);
+
+    // ---- the stream of staged tiles
     lds_u8 *ring = (lds_u8 *)lds;
     lds_u8 *ids = ring + STAGES * STAGE_BYTES + wave * (STAGES * 256);
-
-    // staging: wave w takes keys 8w .. 8w+7 of a tile, lane l row l / 8. Keys past the end repeat
-    // the last one (their scores are masked, and what they hold is never an unwritten row)
-    const int kl = 8 * wave + (lane >> 3);
-    const int chunk = ((lane & 7) ^ swz(kl)) * 8;
-    const int32_t *trow = a.table + (int64_t)req * a.t_row;
-    auto key_at = [&](int t) { return max(0, min(t * KT + kl, len - 1)); };
-    auto fetch_id = [&](int t) {                         // page id of this lane's key of tile t
-        load_lds_word(trow + key_at(t) / a.page, lds_address(ids + (t % STAGES) * 256));
+    // Wave w takes rows 8w .. 8w + 7 of a tile, lane l row l / 8. What follows from the lane is worked
+    // out where it is used: registers are short where 128 rows' sums are held
+    auto own_lane = [&]() __attribute__((always_inline)) {
+        int x = lane;
+        asm volatile("" : "+v"(x));
+        return x;
     };
-    auto issue = [&](int t, int id) {                    // tile t -> slot t % STAGES
-        const int k = key_at(t);
-        const int pg = min(max(id, 0), a.pages - 1);     // ids outside the pool are clamped
-        const uint16_t *src = a.cache + (int64_t)pg * a.c_page + (int64_t)(k % a.page) * a.c_row + chunk;
-        load_lds_pieces<SEGS>(src, lds_address(ring + (t % STAGES) * STAGE_BYTES + wave * (SEGS * 1024)));
-    };
-    auto read_id = [&](int t) {
-        return *(__attribute__((address_space(3))) const int32_t *)(ids + (t % STAGES) * 256 + lane * 4);
-    };
-
-#pragma unroll
-    for (int i = 0; i < S::ND; ++i)
-#pragma unroll
-        for (int j = 0; j < T::NO; ++j) o[i][j] = 0.0f;
-    m = -INFINITY;
-    l = 0.0f;
-
-    // the first tiles' ids come straight into registers, the later ones' with the stage before
-    int id0[STAGES - 1];
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) id0[s] = trow[key_at(t0 + s) / a.page];
-    asm volatile("" ::: "memory");                       // the queries' loads go out behind the ids'
-    u32x4_t qf[S::KS];
-#pragma unroll
-    for (int k = 0; k < S::KS; ++k) qf[k] = *reinterpret_cast<const u32x4_t *>(qp + k * T::KSTEP + grp * 8);
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        if (t0 + s < t1) {
-            fetch_id(t0 + s + STAGES - 1);
-            issue(t0 + s, id0[s]);
-        }
+    Cursor c;
+    c.req = req;
+    c.left = hi - lo;
+    c.more = true;
+    {
+        const int tiles = max(1, (uniform_len(a, req) + KT - 1) / KT);
+        c.g = (int)((lo - base) / tiles);
+        c.enter(a, (int)((lo - base) % tiles), QT);
     }
-    // Fragment places within a stage, with the swizzle worked out once. Score product: key row
-    // `row` of each subtile (subtiles start at multiples of 16 rows: the same swizzle), K step k
-    // reads 16-byte chunk k * KSTEP / 8 + grp of the row: one of KA places a 128-byte piece.
+    // takes the next item; its page ids go to place `slot` of the ids' ring
+    auto plan = [&](int slot) __attribute__((always_inline)) {
+        Due d{0, c.req, 0};
+        const int32_t *id = a.table;
+        if (c.more) {
+            const int kl = 8 * wave + (own_lane() >> 3);
+            if (c.t < 0) {                               // rows past the last repeat it
+                d.row = min(c.g * S::MB + (c.t + QT) * KT + kl, a.rows - 1);
+                d.kind = 1;
+                if (++c.t == 0) c.t = c.t0;
+            } else {                                     // keys past the end repeat the last one: masked
+                const int k = max(0, min(c.t * KT + kl, c.len - 1));
+                const int page = a.page_mul ? (int)(__umulhi((uint32_t)k, a.page_mul) >> a.page_shift) : k;
+                id = a.table + c.req * a.t_row + page;
+                d.row = k - page * a.page;
+                d.kind = 2;
+                if (++c.t == c.end) {
+                    c.left -= c.end - c.t0;
+                    c.more = c.left > 0;
+                    if (c.more) {
+                        if (++c.g == a.groups) {
+                            c.g = 0;
+                            ++c.req;
+                        }
+                        c.enter(a, 0, QT);
+                    }
+                }
+            }
+        }
+        load_lds_word(id, lds_address(ids + slot % STAGES * 256));
+        return d;
+    };
+    auto issue = [&](const Due &d, int slot) __attribute__((always_inline)) {
+        const int x = own_lane();
+        const int chunk = ((x & 7) ^ swz(8 * wave + (x >> 3))) * 8;
+        const uint16_t *src;
+        if (d.kind == 2) {                               // ids outside the pool are clamped
+            const int id = *(__attribute__((address_space(3))) const int32_t *)(ids + slot % STAGES * 256 + x * 4);
+            src = a.cache + (int64_t)min(max(id, 0), a.pages - 1) * a.c_page + (int64_t)d.row * a.c_row + chunk;
+        } else {
+            const int j = d.row / a.heads, h = d.row - j * a.heads;
+            src = a.q + ((int64_t)d.req * a.tokens + j) * a.q_row + h * a.q_head + chunk;
+        }
+        load_lds_pieces<SEGS>(src, lds_address(ring + slot % STAGES * STAGE_BYTES + wave * (SEGS * 1024)));
+    };
+    // Item n is staged after step n, which issues item n + 2 and the ids of item n + 4: the stage
+    // that it fills held item n - 2, whose last reader (the value product, one step behind the
+    // score product) is done.
+    int n = -1, issued = 2;
+    Due due0 = plan(0), due1 = plan(1), due2 = plan(2);
+    issue(due0, 0);                                      // queries: their ids are not needed
+    wait_vmcnt<SEGS>();
+    due0 = plan(3);
+    issue(due1, 1);
+    due1 = due2;
+    due2 = due0;
+    lds_u8 *st = ring, *st_before = ring;
+    auto step = [&]() __attribute__((always_inline)) {
+        ++n;
+        if (n + 1 < issued) wait_vmcnt<PW>();
+        else wait_vmcnt<0>();
+        lds_barrier();
+        if (due1.kind) {
+            const Due d = plan(n + 4);
+            issue(due1, n + 2);
+            ++issued;
+            due1 = due2;
+            due2 = d;
+        }
+        st_before = st;
+        st = ring + n % STAGES * STAGE_BYTES;
+    };
+
+    // ---- fragment places within a stage. Score product: key row `row` of each subtile (subtiles
+    // start at multiples of 16 rows: the same swizzle), K step k reads 16-byte chunk
+    // k * KSTEP / 8 + grp of the row. The swizzle is an exclusive or of chunks, so the KA places of a
+    // 128-byte piece differ by one too; they are worked out for each tile from one register.
     constexpr int KA = 64 / T::KSTEP;
-    int koff[KA];
+    const int kbase = (row >> 3) * (SEGS * 1024) + (row & 7) * 128 + ((grp ^ swz(row)) << 4);
+    auto place_of = [&](lds_u8 *from, int off) __attribute__((always_inline)) {
+        int at = (int)(uintptr_t)from + off;
+        asm volatile("" : "+v"(at));                     // one register, the rest is in the instruction
+        return (lds_u8 *)(uintptr_t)(uint32_t)at;
+    };
+    auto find_keys = [&](lds_u8 *from, lds_u8 *(&at)[KA]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < KA; ++j)
-        koff[j] = (row >> 3) * (SEGS * 1024) + (row & 7) * 128 + (((j * (T::KSTEP / 8) + grp) ^ swz(row)) << 4);
-    // Value product: 16-lane group reads keys kv + 0 .. 3 at dims dv + 0 .. 15; the dim tile's
-    // place in its 128-byte piece and the half of the key step change the swizzle
+        for (int j = 0; j < KA; ++j) at[j] = place_of(from, kbase ^ (j * T::KSTEP * 2));
+    };
+    // Value product: 16-lane group reads keys kv + 0 .. 3 at dims dv + 0 .. 15; likewise for the dim
+    // tile's place in its 128-byte piece and for the half of the key step
     constexpr int VA = 64 / T::DIMS;
     const int kv = T::place(0, grp) + ((lane & 15) >> 2);
     const int dv = (T::ROWS == 32 ? ((lane >> 4) & 1) * 16 : 0) + (lane & 3) * 4;
-    int voff[VA][2];
+    const int vbase = (kv >> 3) * (SEGS * 1024) + (d0 >> 6) * 1024 + (kv & 7) * 128 + (((dv >> 3) ^ swz(kv)) << 4) + (dv & 4) * 2;
+    auto find_values = [&](lds_u8 *from, lds_u8 *(&at)[VA][2]) __attribute__((always_inline)) {
+        constexpr int HALF = T::place(4, 0);             // keys between the halves: 8 (another swizzle) or 16
 #pragma unroll
-    for (int j = 0; j < VA; ++j)
+        for (int j = 0; j < VA; ++j)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int r = kv + T::place(4 * hh, 0), ch = (j * T::DIMS + dv) >> 3;
-            voff[j][hh] = (r >> 3) * (SEGS * 1024) + (d0 >> 6) * 1024 + (r & 7) * 128 + ((ch ^ swz(r)) << 4) + (dv & 4) * 2;
-        }
+            for (int hh = 0; hh < 2; ++hh)
+                at[j][hh] = place_of(from, (vbase ^ (j * T::DIMS * 2) ^ (HALF == 8 ? hh * 16 : 0)) + hh * (HALF / 8) * (SEGS * 1024));
+    };
+
     constexpr int NT = KT / T::ROWS;                     // key subtiles: 1 or 2
     constexpr int XS = T::NS / 8;                        // key steps of the value product
-    acc_t s[NT];
-    u32x4_t pf[XS];
-    lds_u8 *st;
-    // waits for tile t, frees slot (t - 1) % STAGES and refills it
-    auto stage = [&](int t) {
-        wait_stages<PW, STAGES - 2>(min(STAGES - 2, t1 - 1 - t));
-        lds_barrier();
-        if (t + STAGES - 1 < t1) {
-            const int id = read_id(t + STAGES - 1);
-            asm volatile("" ::: "memory");
-            fetch_id(t + 2 * (STAGES - 1));
-            issue(t + STAGES - 1, id);
-        }
-        st = ring + (t % STAGES) * STAGE_BYTES;
-    };
-    // S^T = K Q^T. Fragments are read a group ahead of their matrix instructions; the scheduling
-    // barriers keep the compiler from reading whole tiles ahead and spilling
-    auto scores = [&]() {
-        constexpr int KG = S::KG, NG = S::KS * NT / KG;  // fragments a group, groups
-        static_assert(KG * NG == S::KS * NT, "whole groups");
-        auto key_frag = [&](int e) {
-            const int k = e / NT, u = e % NT;
-            return *(const lds_u32x4 *)(st + koff[k % KA] + (u * T::ROWS / 8) * (SEGS * 1024) + (k / KA) * 1024);
-        };
+    constexpr int KG = S::KG, NG = S::KS * NT / KG;      // fragments a group, groups of the score product
+    static_assert(KG * NG == S::KS * NT, "whole groups");
+    u32x4_t qf[S::KS], pf[XS];
+    acc_t o[S::ND], s[NT], next[NT];
+    float m, l;
+
+    // S^T = K Q^T of the staged tile into `to`, and beside it, in slices between the matrix
+    // instructions, the softmax weights of the tile before from s. Fragments are read a group
+    // ahead; the scheduling barriers keep the groups apart, and the compiler from spilling.
+    // Weights are rounded to bf16 for the matrix product (relative 2^-9 each, as the values are);
+    // their sum l is of the unrounded ones.
+    float mu = 0.0f;
+    auto weight_slice = [&](int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < NT; ++u) s[u] = acc_t{0.0f};
+        for (int i = i0; i < i1; i += 2) {
+            const float x = __builtin_amdgcn_exp2f(fmaf(s[i / T::NO][i % T::NO], a.c, -mu));
+            const float y = __builtin_amdgcn_exp2f(fmaf(s[(i + 1) / T::NO][(i + 1) % T::NO], a.c, -mu));
+            l += x;
+            l += y;
+            pf[i / 8][i % 8 / 2] = pack_bf16(x, y);
+        }
+    };
+    auto scores = [&](acc_t (&to)[NT], auto with_weights) __attribute__((always_inline)) {
+        lds_u8 *at[KA];
+        find_keys(st, at);
+        auto key_frag = [&](int e) __attribute__((always_inline)) {
+            const int k = e / NT, u = e % NT;
+            return *(const lds_u32x4 *)(at[k % KA] + (u * T::ROWS / 8) * (SEGS * 1024) + (k / KA) * 1024);
+        };
         u32x4_t kf[2][KG];
 #pragma unroll
         for (int e = 0; e < KG; ++e) kf[0][e] = key_frag(e);
@@ -251,44 +351,29 @@ __device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, con
 #pragma unroll
             for (int e = 0; e < KG; ++e) {
                 const int at = gi * KG + e;
-                s[at % NT] = T::mfma(kf[gi & 1][e], qf[at / NT], s[at % NT]);
+                to[at % NT] = T::mfma(kf[gi & 1][e], qf[at / NT], at / NT ? to[at % NT] : acc_t{0.0f});
             }
+            if constexpr (with_weights.value) weight_slice(T::NS / 2 * gi / NG * 2, T::NS / 2 * (gi + 1) / NG * 2);
         }
-        in_vgpr(s);
-    };
-    auto largest = [&]() {
-        float top = s[0][0];
-#pragma unroll
-        for (int i = 1; i < T::NS; ++i) top = fmaxf(top, s[i / T::NO][i % T::NO]);
-        return row_max<T>(top) * a.c;
-    };
-    // Softmax weights against the reference maximum. They are rounded to bf16 for the matrix
-    // product (relative 2^-9 each, as the values are); their sum l is of the unrounded ones
-    auto weights = [&](float mu) {
-        float p[T::NS];
-#pragma unroll
-        for (int i = 0; i < T::NS; ++i) {
-            p[i] = __builtin_amdgcn_exp2f(fmaf(s[i / T::NO][i % T::NO], a.c, -mu));
-            l += p[i];
-        }
-#pragma unroll
-        for (int i = 0; i < T::NS / 2; ++i) pf[i / 4][i % 4] = pack_bf16(p[2 * i], p[2 * i + 1]);
+        in_vgpr(to);
     };
     // A fragment of V^T: dim tile i, key step x. B register pairs hold keys place(8x + j), j =
     // 0 .. 7, and so does this
-    auto value = [&](int i, int x) {
-        u32x4_t f;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            lds_u8 *at = st + voff[i % VA][hh] + (i / VA) * 1024 + 2 * x * (SEGS * 1024);
-            const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
-            f[2 * hh] = v[0];
-            f[2 * hh + 1] = v[1];
-        }
-        return f;
-    };
     // O^T += V^T P^T; with clean, non-finite values count as 0
-    auto add_values = [&](auto clean) {
+    auto add_values = [&](lds_u8 *from, auto clean) __attribute__((always_inline)) {
+        lds_u8 *at[VA][2];
+        find_values(from, at);
+        auto value = [&](int i, int x) __attribute__((always_inline)) {
+            u32x4_t f;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                lds_u8 *p = at[i % VA][hh] + (i / VA) * 1024 + 2 * x * (SEGS * 1024);
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+                f[2 * hh] = v[0];
+                f[2 * hh + 1] = v[1];
+            }
+            return f;
+        };
         constexpr int VG = S::VG;
         u32x4_t vf[2][VG * XS];
 #pragma unroll
@@ -308,114 +393,158 @@ __device__ __forceinline__ void run_tiles(const DecodeArgs &a, uint8_t *lds, con
             }
         }
     };
-    in_acc(o);
-    in_vgpr(qf);                                         // their wait is here, not in the loop
 
-    // The inner loop has no branch that touches the output sums: one that did would move all of
-    // them between register files in every iteration. A reference maximum that moves and a
-    // masked score that is not finite leave the loop and come back.
-    const int whole = first / KT;                        // tiles before this are seen whole by every row
-    bool scored = false;                                 // tile t's scores are at hand
-    for (int t = t0; t < t1;) {
-        float top;
-        bool odd = false;
-        do {
-            if (!scored) {
-                stage(t);
-                scores();
-                if (t >= whole) {
-#pragma unroll
-                    for (int i = 0; i < T::NS; ++i) {
-                        const float x = s[i / T::NO][i % T::NO];
-                        const bool seen = t * KT + T::place(i, grp) < limit, fin = finite_f32(x);
-                        // not finite: so is the key's row, or a query. A row that sees it gets NaN
-                        odd |= !fin;
-                        s[i / T::NO][i % T::NO] = seen ? (fin ? x : NAN) : -INFINITY;
-                    }
-                    odd = __any(odd);
-                }
-                top = largest();
-                if (odd || __any(top > m + kSlack)) break;
-            }
-            weights(m == -INFINITY ? 0.0f : m);
-            add_values(std::false_type());
-            scored = false;
-        } while (++t < t1);
-        if (t >= t1) break;
-        const float n = fmaxf(m, top);
-        const float alpha = n == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - n);
-        m = n;
-        l *= alpha;
-#pragma unroll
-        for (int i = 0; i < S::ND; ++i) {
-            o[i] *= alpha;
-            in_acc(o);
-        }
-        scored = !odd;
-        if (odd) {                                       // rare
-            weights(m == -INFINITY ? 0.0f : m);
-            add_values(std::true_type());
-            in_acc(o);
-            ++t;
-        }
-    }
-    l = row_sum<T>(l);
-    wait_vmcnt<0>();
-    lds_barrier();                                       // the ring is free again
-}
-
-template <typename T, int WR, int WD>
-__global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
-    typedef Shape<T, WR, WD> S;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE_BYTES + 4 * STAGES * 256];
-    __shared__ int64_t sh[8];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int row = T::row(lane), grp = T::grp(lane);
-    const int wr = wave % WR, d0 = (wave / WR) * (L / WD);
-
-    const int64_t total = uniform(all_tiles(a, sh));
-    const int grid = (int)min((int64_t)a.grid, total);
-    if ((int)blockIdx.x >= grid) return;
-    int64_t lo = run_start(total, grid, blockIdx.x);
-    const int64_t hi = run_start(total, grid, blockIdx.x + 1);
-    int req;
-    int64_t base;
-    find_request(a, lo, sh, req, base);
-    bool leading = true;                                 // the run's first piece
+    bool leading = true;                                 // the run's first unit
     while (lo < hi) {
-        const int len = uniform(request_len(a, req)), tiles = max(1, (len + KT - 1) / KT);
+        const int len = uniform_len(a, req), tiles = max(1, (len + KT - 1) / KT);
         const int g = (int)((lo - base) / tiles), t0 = (int)((lo - base) % tiles);
         const int t1 = (int)min((int64_t)tiles, t0 + (hi - lo));
+        // keys this lane's row sees: it is row (token, head) of the request; rows past the last repeat it
+        const int limit = max(0, len - a.tokens + 1 + min(g * S::MB + wr * T::ROWS + row, a.rows - 1) / a.heads);
+        const int whole = max(0, len - a.tokens + 1) / KT;       // tiles before this: all rows see all of them
 
-        // this lane's row of the request: token j, head h; rows past the last repeat it
-        const int r = g * S::MB + wr * T::ROWS + row;
-        const int rc = min(r, a.rows - 1);
-        const int j = rc / a.heads, h = rc % a.heads;
+        for (int qi = 0; qi < QT; ++qi) {
+            step();
+            if (QT == 1 || qi == wr) {
+                lds_u8 *at[KA];
+                find_keys(st, at);
+#pragma unroll
+                for (int k = 0; k < S::KS; ++k) qf[k] = *(const lds_u32x4 *)(at[k % KA] + (k / KA) * 1024);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < S::ND; ++i) o[i] = acc_t{0.0f};
+        in_acc(o);
+        m = -INFINITY;
+        l = 0.0f;
+
+        // Tile t's scores are in s. What the next step needs to know of them: the row's largest, and
+        // whether a masked tile holds one that is not finite.
+        float top;
+        bool odd, grow;
+        auto inspect = [&](int t) __attribute__((always_inline)) {
+            odd = false;
+            if (t >= whole) {
+#pragma unroll
+                for (int i = 0; i < T::NS; ++i) {
+                    const float x = s[i / T::NO][i % T::NO];
+                    const bool seen = t * KT + T::place(i, grp) < limit, fin = finite_f32(x);
+                    // not finite: so is the key's row, or a query. A row that sees it gets NaN
+                    odd |= !fin;
+                    s[i / T::NO][i % T::NO] = seen ? (fin ? x : NAN) : -INFINITY;
+                }
+                odd = __any(odd);
+            }
+            top = s[0][0];
+#pragma unroll
+            for (int i = 1; i < T::NS; ++i) top = fmaxf(top, s[i / T::NO][i % T::NO]);
+            top = row_max<T>(top) * a.c;
+            grow = __any(top > m + kSlack);
+            mu = m == -INFINITY ? 0.0f : m;
+        };
+        // moves the row's reference maximum to what the scores need
+        auto rescale = [&]() __attribute__((always_inline)) {
+            const float up = fmaxf(m, top);
+            const float alpha = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            mu = m == -INFINITY ? 0.0f : m;
+            l *= alpha;
+            grow = false;
+#pragma unroll
+            for (int i = 0; i < S::ND; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                o[i] *= alpha;
+                in_acc(o);
+            }
+        };
+        // The inner loops have no branch that touches the output sums: one that did would move all
+        // of them between register files in every iteration. A reference maximum that moves and a
+        // non-finite score in a masked tile leave them.
+        bool scored = false;
+        if constexpr (S::FLOW) {
+            for (int t = t0;;) {
+                if (!scored) {
+                    step();
+                    scores(s, std::false_type());
+                    inspect(t);
+                    scored = true;
+                }
+                while (!odd && !grow && t + 1 < t1) {
+                    step();
+                    scores(next, std::true_type());
+                    add_values(st_before, std::false_type());
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) s[u] = next[u];
+                    inspect(++t);
+                }
+                if (grow) {
+                    rescale();
+                    if (!odd && t + 1 < t1) continue;
+                }
+                weight_slice(0, T::NS);
+                if (odd) add_values(st, std::true_type());       // rare
+                else add_values(st, std::false_type());
+                in_acc(o);
+                if (++t == t1) break;
+                scored = false;
+            }
+        } else {
+            for (int t = t0; t < t1;) {
+                do {
+                    if (!scored) {
+                        step();
+                        scores(s, std::false_type());
+                        inspect(t);
+                        if (odd || grow) break;
+                    }
+                    weight_slice(0, T::NS);
+                    add_values(st, std::false_type());
+                    scored = false;
+                } while (++t < t1);
+                if (t >= t1) break;
+                rescale();
+                scored = !odd;
+                if (odd) {                               // rare
+                    weight_slice(0, T::NS);
+                    add_values(st, std::true_type());
+                    in_acc(o);
+                    ++t;
+                }
+            }
+        }
+        l = row_sum<T>(l);
+
+        const int r = g * S::MB + wr * T::ROWS + T::row(own_lane()), rc = min(r, a.rows - 1);
+        const int j = rc / a.heads, h = rc - j * a.heads;
         const int64_t qr = (int64_t)req * a.tokens + j;
-        const uint16_t *qp = a.q + qr * a.q_row + h * a.q_head;
-        const int limit = max(0, len - a.tokens + j + 1);        // keys this row sees
-        const int first = max(0, len - a.tokens + 1);            // keys that the request's first token sees
-        typename T::acc_t o[S::ND];
-        float m, l;
-        run_tiles<T, WR, WD>(a, lds, qp, req, len, t0, t1, limit, first, o, m, l);
         const bool uncut = t0 == 0 && t1 == tiles;
         if (t0 == 0 && tid == 0)
             a.cuts[(int64_t)req * a.groups + g] = make_int2(
-                2 * blockIdx.x + (leading ? 0 : 1), uncut ? (int)blockIdx.x : run_of(total, grid, lo + tiles - 1));
+                2 * blockIdx.x + (leading ? 0 : 1), uncut ? (int)blockIdx.x : run_of(line.total, grid, lo + tiles - 1));
         if (uncut) {
-            if (r < a.rows) {
-                const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;   // no key: zeros
-                uint16_t *op = a.out + qr * a.o_row + h * a.o_head;
+            if (r < a.rows) {                            // the lanes of a row are in this together
+                const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key: zeros
+                uint16_t *op = a.out + qr * a.o_row + h * a.o_head + d0;
+                if (a.lse && grp == 0 && wave / WR == 0) a.lse[qr * a.heads + h] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 #pragma unroll
-                for (int i = 0; i < S::ND; ++i)
+                for (int i = 0; i < S::ND; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    u32x2_t v[S::NO4];
 #pragma unroll
-                    for (int x = 0; x < S::NO4; ++x) {
-                        const u32x2_t v = {pack_bf16(o[i][4 * x] * inv, o[i][4 * x + 1] * inv),
-                                           pack_bf16(o[i][4 * x + 2] * inv, o[i][4 * x + 3] * inv)};
-                        *reinterpret_cast<u32x2_t *>(op + d0 + i * T::DIMS + T::place(4 * x, grp)) = v;
+                    for (int x = 0; x < S::NO4; ++x)
+                        v[x] = u32x2_t{pack_bf16(o[i][4 * x] * inv, o[i][4 * x + 1] * inv),
+                                       pack_bf16(o[i][4 * x + 2] * inv, o[i][4 * x + 3] * inv)};
+                    if constexpr (T::ROWS == 32) {       // the two lanes of a row trade halves: 16-byte stores
+#pragma unroll
+                        for (int x = 0; x < S::NO4; x += 2) {
+                            const auto p = __builtin_amdgcn_permlane32_swap(v[x][0], v[x + 1][0], false, false);
+                            const auto q = __builtin_amdgcn_permlane32_swap(v[x][1], v[x + 1][1], false, false);
+                            *reinterpret_cast<u32x4_t *>(op + i * T::DIMS + 8 * (x + grp)) = u32x4_t{p[0], q[0], p[1], q[1]};
+                        }
+                    } else {
+                        *reinterpret_cast<u32x2_t *>(op + i * T::DIMS + T::place(0, grp)) = v[0];
                     }
-                if (a.lse && grp == 0 && wave / WR == 0)
-                    a.lse[qr * a.heads + h] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+                }
             }
         } else {
             float *part = a.work + (2 * (int64_t)blockIdx.x + (leading ? 0 : 1)) * part_floats<S::MB>();
@@ -567,6 +696,12 @@ hipError_t launch_latent_decode(const skinny_latent_decode_args &p, int cus, hip
     a.page = (int)p.page;
     a.max_pages = (int)p.max_pages;
     a.rows = a.tokens * a.heads;
+    // 2^bits >= page > 2^(bits - 1): the reciprocal 2^(31 + bits) / page, rounded up, fits 32 bits, and
+    // for k < 2^30 its rounding adds less than 2^-(1 + bits) < 1 / page to the quotient: exact
+    int bits = 1;
+    while ((1 << bits) < a.page) ++bits;
+    a.page_mul = a.page == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + bits)) + a.page - 1) / a.page);
+    a.page_shift = bits - 1;
     const int mb = block_rows(a.rows);
     a.groups = (a.rows + mb - 1) / mb;
     a.c = p.scale * kLog2e;
