@@ -59,7 +59,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 }
 
 // ---- loads straight into LDS --------------------------------------------------------------
-// lane l's 16 bytes at src (4 with load_lds_word) go to LDS address lds + 16 l (4 l), and with N
+// lane l's 16 bytes at src (4 with load_lds_word) go to LDS address lds + 16 l (4 l), and of N
 // pieces those at src + 128 i to lds + 1024 i + 16 l. lds is the same in all lanes. Written out
 // because the compiler does not know which staged bytes a read of LDS needs: behind the builtin it
 // waits for every load in flight before the next read, and the ring would hold one stage. Here
@@ -73,23 +73,29 @@ __device__ __forceinline__ void load_lds_word(const void *src, int lds) {
                  :: "s"(lds), "v"(src) : "memory");
 }
 
-#define SKINNY_NEXT_PIECE(o) "\n\ts_add_u32 m0, m0, 896\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:" #o
-template <int N>
-__device__ __forceinline__ void load_lds_pieces(const void *src, int lds) {
-    static_assert(N == 1 || N == 2 || N == 9, "pieces");
-    if constexpr (N == 1)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                     :: "s"(lds), "v"(src) : "memory");
-    else if constexpr (N == 2)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" SKINNY_NEXT_PIECE(128)
-                     :: "s"(lds), "v"(src) : "memory", "scc");
-    else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" SKINNY_NEXT_PIECE(128)
-                     SKINNY_NEXT_PIECE(256) SKINNY_NEXT_PIECE(384) SKINNY_NEXT_PIECE(512) SKINNY_NEXT_PIECE(640)
-                     SKINNY_NEXT_PIECE(768) SKINNY_NEXT_PIECE(896) SKINNY_NEXT_PIECE(1024)
-                     :: "s"(lds), "v"(src) : "memory", "scc");
+// piece I of a row: src + 128 I to lds + 1024 I
+template <int I>
+__device__ __forceinline__ void load_lds_piece(const void *src, int lds) {
+    asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%3"
+                 :: "s"(lds), "v"(src), "i"(896 * I), "i"(128 * I) : "memory", "scc");
 }
-#undef SKINNY_NEXT_PIECE
+template <int N, int I = 0>
+__device__ __forceinline__ void load_lds_pieces(const void *src, int lds) {
+    if constexpr (I < N) {
+        load_lds_piece<I>(src, lds);
+        load_lds_pieces<N, I + 1>(src, lds);
+    }
+}
+// the same in no lane unless `on`: the count of loads in flight goes by either way (called with all
+// lanes active)
+template <int I>
+__device__ __forceinline__ void load_lds_piece_if(bool on, const void *src, int lds) {
+    const uint32_t half = uniform(on ? -1 : 0);
+    const uint64_t lanes = (uint64_t)half << 32 | half;
+    asm volatile("s_add_u32 m0, %0, %2\n\ts_mov_b64 exec, %4\n\tglobal_load_lds_dwordx4 %1, off offset:%3\n\t"
+                 "s_mov_b64 exec, -1"
+                 :: "s"(lds), "v"(src), "i"(896 * I), "i"(128 * I), "s"(lanes) : "memory", "scc");
+}
 
 // ---- staged key and value rows ----------------------------------------------------------
 // Rows come into LDS in blocks of 8 rows x 128 bytes (one direct-to-LDS instruction: lane l

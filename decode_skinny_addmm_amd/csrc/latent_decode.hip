@@ -139,8 +139,8 @@ struct Shape {
     // instruction takes 32 of them): of keys, and of dim tiles of values
     // softmax of a tile beside the score product of the next: takes registers that 128 rows x 512
     // sums leave no room for
-    static constexpr bool FLOW = WR < 4;
-    static constexpr int KG = WR == 4 ? 4 : 6, VG = WR < 4 && ND >= 4 ? 2 : 1;
+    static constexpr bool FLOW = MB < 128;
+    static constexpr int KG = MB == 128 ? 4 : 6, VG = MB < 128 && ND >= 4 ? 2 : 1;
 };
 
 // What a workgroup stages, in order: for each unit (request and row group) of its run, the unit's
@@ -163,6 +163,15 @@ struct Due {
     int row, req;
     int kind;                                // 0: none, 1: queries, 2: keys
 };
+
+// of a row's pieces, those that go out with group `at` of `of` (both known when compiled)
+template <int I = 0>
+__device__ __forceinline__ void pieces_at(int at, int of, bool on, const void *src, int lds) {
+    if constexpr (I < SEGS) {
+        if (I * of / SEGS == at) load_lds_piece_if<I>(on, src, lds);
+        pieces_at<I + 1>(at, of, on, src, lds);
+    }
+}
 
 template <typename T, int WR, int WD>
 __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
@@ -236,47 +245,60 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
         load_lds_word(id, lds_address(ids + slot % STAGES * 256));
         return d;
     };
-    auto issue = [&](const Due &d, int slot) __attribute__((always_inline)) {
+    // where a due item's pieces come from and go to
+    const uint16_t *from = a.cache;
+    int to = 0;
+    auto aim = [&](const Due &d, int slot) __attribute__((always_inline)) {
         const int x = own_lane();
         const int chunk = ((x & 7) ^ swz(8 * wave + (x >> 3))) * 8;
-        const uint16_t *src;
         if (d.kind == 2) {                               // ids outside the pool are clamped
             const int id = *(__attribute__((address_space(3))) const int32_t *)(ids + slot % STAGES * 256 + x * 4);
-            src = a.cache + (int64_t)min(max(id, 0), a.pages - 1) * a.c_page + (int64_t)d.row * a.c_row + chunk;
+            from = a.cache + (int64_t)min(max(id, 0), a.pages - 1) * a.c_page + (int64_t)d.row * a.c_row + chunk;
         } else {
             const int j = d.row / a.heads, h = d.row - j * a.heads;
-            src = a.q + ((int64_t)d.req * a.tokens + j) * a.q_row + h * a.q_head + chunk;
+            from = a.q + ((int64_t)d.req * a.tokens + j) * a.q_row + h * a.q_head + chunk;
         }
-        load_lds_pieces<SEGS>(src, lds_address(ring + slot % STAGES * STAGE_BYTES + wave * (SEGS * 1024)));
+        to = lds_address(ring + slot % STAGES * STAGE_BYTES + wave * (SEGS * 1024));
     };
-    // Item n is staged after step n, which issues item n + 2 and the ids of item n + 4: the stage
-    // that it fills held item n - 2, whose last reader (the value product, one step behind the
-    // score product) is done.
-    int n = -1, issued = 2;
-    Due due0 = plan(0), due1 = plan(1), due2 = plan(2);
-    issue(due0, 0);                                      // queries: their ids are not needed
-    wait_vmcnt<SEGS>();
-    due0 = plan(3);
-    issue(due1, 1);
-    due1 = due2;
-    due2 = due0;
+    // Item n is staged after step n, which takes the ids of item n + 2 LOOK and aims at item n + LOOK;
+    // the pieces of the latter go out between the matrix instructions that follow, one at a time
+    // (ten loads in a row hold a wave up for 1100 cycles). The stage that they fill is free: the
+    // value product is done with item n - 1, or, where it runs one step behind the score product,
+    // with item n - 2.
+    constexpr int LOOK = S::FLOW ? 2 : 3;
+    static_assert(LOOK <= QT + 1, "the items issued before the first step exist");
+    int n = -1;
+    Due due[LOOK];                                       // the next items to be issued
+    {
+        Due early[LOOK];
+#pragma unroll
+        for (int x = 0; x < LOOK; ++x) early[x] = plan(x);
+        due[0] = plan(LOOK);
+        aim(early[0], 0);                                // queries: their ids are not needed
+        load_lds_pieces<SEGS>(from, to);
+        wait_vmcnt<SEGS>();
+#pragma unroll
+        for (int x = 1; x < LOOK; ++x) {
+            due[x] = plan(LOOK + x);
+            aim(early[x], x);
+            load_lds_pieces<SEGS>(from, to);
+        }
+    }
     lds_u8 *st = ring, *st_before = ring;
+    bool live = false;                                   // there is an item to issue
     auto step = [&]() __attribute__((always_inline)) {
         ++n;
-        if (n + 1 < issued) wait_vmcnt<PW>();
-        else wait_vmcnt<0>();
+        wait_vmcnt<PW *(LOOK - 1)>();
         lds_barrier();
-        if (due1.kind) {
-            const Due d = plan(n + 4);
-            issue(due1, n + 2);
-            ++issued;
-            due1 = due2;
-            due2 = d;
-        }
+        live = due[0].kind != 0;
+        const Due d = plan(n + 2 * LOOK);
+        if (live) aim(due[0], n + LOOK);
+#pragma unroll
+        for (int x = 0; x + 1 < LOOK; ++x) due[x] = due[x + 1];
+        due[LOOK - 1] = d;
         st_before = st;
         st = ring + n % STAGES * STAGE_BYTES;
     };
-
     // ---- fragment places within a stage. Score product: key row `row` of each subtile (subtiles
     // start at multiples of 16 rows: the same swizzle), K step k reads 16-byte chunk
     // k * KSTEP / 8 + grp of the row. The swizzle is an exclusive or of chunks, so the KA places of a
@@ -315,7 +337,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     acc_t o[S::ND], s[NT], next[NT];
     float m, l;
 
-    // S^T = K Q^T of the staged tile into `to`, and beside it, in slices between the matrix
+    // S^T = K Q^T of the staged tile into `sum`, and beside it, in slices between the matrix
     // instructions, the softmax weights of the tile before from s. Fragments are read a group
     // ahead; the scheduling barriers keep the groups apart, and the compiler from spilling.
     // Weights are rounded to bf16 for the matrix product (relative 2^-9 each, as the values are);
@@ -331,7 +353,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
             pf[i / 8][i % 8 / 2] = pack_bf16(x, y);
         }
     };
-    auto scores = [&](acc_t (&to)[NT], auto with_weights) __attribute__((always_inline)) {
+    auto scores = [&](acc_t (&sum)[NT], auto with_weights) __attribute__((always_inline)) {
         lds_u8 *at[KA];
         find_keys(st, at);
         auto key_frag = [&](int e) __attribute__((always_inline)) {
@@ -350,12 +372,13 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
             }
 #pragma unroll
             for (int e = 0; e < KG; ++e) {
-                const int at = gi * KG + e;
-                to[at % NT] = T::mfma(kf[gi & 1][e], qf[at / NT], at / NT ? to[at % NT] : acc_t{0.0f});
+                const int k_at = gi * KG + e;
+                sum[k_at % NT] = T::mfma(kf[gi & 1][e], qf[k_at / NT], k_at / NT ? sum[k_at % NT] : acc_t{0.0f});
             }
             if constexpr (with_weights.value) weight_slice(T::NS / 2 * gi / NG * 2, T::NS / 2 * (gi + 1) / NG * 2);
+            pieces_at(gi, NG, live, from, to);
         }
-        in_vgpr(to);
+        in_vgpr(sum);
     };
     // A fragment of V^T: dim tile i, key step x. B register pairs hold keys place(8x + j), j =
     // 0 .. 7, and so does this
@@ -405,9 +428,10 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
 
         for (int qi = 0; qi < QT; ++qi) {
             step();
-            if (QT == 1 || qi == wr) {
+            pieces_at(0, 1, live, from, to);
+            if (qi == wr * T::ROWS / KT) {
                 lds_u8 *at[KA];
-                find_keys(st, at);
+                find_keys(st + wr * T::ROWS % KT / 8 * (SEGS * 1024), at);
 #pragma unroll
                 for (int k = 0; k < S::KS; ++k) qf[k] = *(const lds_u32x4 *)(at[k % KA] + (k / KA) * 1024);
             }
@@ -710,8 +734,8 @@ hipError_t launch_latent_decode(const skinny_latent_decode_args &p, int cus, hip
     a.grid = (int)std::min<int64_t>(cus, most);
     switch (mb) {
         case 16: return launch_shape<Tile16, 1, 4>(a, stream);
-        case 32: return launch_shape<Tile32, 1, 4>(a, stream);
-        case 64: return launch_shape<Tile32, 2, 2>(a, stream);
+        case 32: return launch_shape<Tile16, 2, 2>(a, stream);
+        case 64: return launch_shape<Tile16, 4, 1>(a, stream);
         default: return launch_shape<Tile32, 4, 1>(a, stream);
     }
 }
