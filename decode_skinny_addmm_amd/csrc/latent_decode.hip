@@ -333,6 +333,9 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     constexpr int XS = T::NS / 8;                        // key steps of the value product
     constexpr int KG = S::KG, NG = S::KS * NT / KG;      // fragments a group, groups of the score product
     static_assert(KG * NG == S::KS * NT, "whole groups");
+    // places between matrix instructions where pieces go out: all of a step's, if a value product
+    // follows each score product
+    constexpr int ISSUES = S::FLOW ? NG : NG + S::ND / S::VG;
     u32x4_t qf[S::KS], pf[XS];
     acc_t o[S::ND], s[NT], next[NT];
     float m, l;
@@ -376,16 +379,16 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 sum[k_at % NT] = T::mfma(kf[gi & 1][e], qf[k_at / NT], k_at / NT ? sum[k_at % NT] : acc_t{0.0f});
             }
             if constexpr (with_weights.value) weight_slice(T::NS / 2 * gi / NG * 2, T::NS / 2 * (gi + 1) / NG * 2);
-            pieces_at(gi, NG, live, from, to);
+            pieces_at(gi, ISSUES, live, from, to);
         }
         in_vgpr(sum);
     };
     // A fragment of V^T: dim tile i, key step x. B register pairs hold keys place(8x + j), j =
     // 0 .. 7, and so does this
     // O^T += V^T P^T; with clean, non-finite values count as 0
-    auto add_values = [&](lds_u8 *from, auto clean) __attribute__((always_inline)) {
+    auto add_values = [&](lds_u8 *tile, auto clean) __attribute__((always_inline)) {
         lds_u8 *at[VA][2];
-        find_values(from, at);
+        find_values(tile, at);
         auto value = [&](int i, int x) __attribute__((always_inline)) {
             u32x4_t f;
 #pragma unroll
@@ -414,6 +417,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 if constexpr (clean.value) f = finite_values(f);
                 o[i + e / XS] = T::mfma(f, pf[e % XS], o[i + e / XS]);
             }
+            if constexpr (!S::FLOW) pieces_at(NG + i / VG, ISSUES, live, from, to);
         }
     };
 
@@ -513,27 +517,21 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 scored = false;
             }
         } else {
-            for (int t = t0; t < t1;) {
+            for (int t = t0;;) {
                 do {
-                    if (!scored) {
-                        step();
-                        scores(s, std::false_type());
-                        inspect(t);
-                        if (odd || grow) break;
-                    }
+                    step();
+                    scores(s, std::false_type());
+                    inspect(t);
+                    if (odd || grow) break;
                     weight_slice(0, T::NS);
                     add_values(st, std::false_type());
-                    scored = false;
                 } while (++t < t1);
                 if (t >= t1) break;
                 rescale();
-                scored = !odd;
-                if (odd) {                               // rare
-                    weight_slice(0, T::NS);
-                    add_values(st, std::true_type());
-                    in_acc(o);
-                    ++t;
-                }
+                weight_slice(0, T::NS);
+                add_values(st, std::true_type());
+                in_acc(o);
+                if (++t >= t1) break;
             }
         }
         l = row_sum<T>(l);
@@ -553,11 +551,13 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
 #pragma unroll
                 for (int i = 0; i < S::ND; ++i) {
                     __builtin_amdgcn_sched_barrier(0);
+                    acc_t y[1] = {o[i]};                 // out of the accumulation registers tile by tile
+                    in_vgpr(y);
                     u32x2_t v[S::NO4];
 #pragma unroll
                     for (int x = 0; x < S::NO4; ++x)
-                        v[x] = u32x2_t{pack_bf16(o[i][4 * x] * inv, o[i][4 * x + 1] * inv),
-                                       pack_bf16(o[i][4 * x + 2] * inv, o[i][4 * x + 3] * inv)};
+                        v[x] = u32x2_t{pack_bf16(y[0][4 * x] * inv, y[0][4 * x + 1] * inv),
+                                       pack_bf16(y[0][4 * x + 2] * inv, y[0][4 * x + 3] * inv)};
                     if constexpr (T::ROWS == 32) {       // the two lanes of a row trade halves: 16-byte stores
 #pragma unroll
                         for (int x = 0; x < S::NO4; x += 2) {
@@ -574,10 +574,14 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
             float *part = a.work + (2 * (int64_t)blockIdx.x + (leading ? 0 : 1)) * part_floats<S::MB>();
             f32x4_t *ps = reinterpret_cast<f32x4_t *>(part) + wave * (S::ND * S::NO4 * 64) + lane;
 #pragma unroll
-            for (int i = 0; i < S::ND; ++i)
+            for (int i = 0; i < S::ND; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                acc_t y[1] = {o[i]};
+                in_vgpr(y);
 #pragma unroll
                 for (int x = 0; x < S::NO4; ++x)
-                    ps[(i * S::NO4 + x) * 64] = f32x4_t{o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]};
+                    ps[(i * S::NO4 + x) * 64] = f32x4_t{y[0][4 * x], y[0][4 * x + 1], y[0][4 * x + 2], y[0][4 * x + 3]};
+            }
             if (grp == 0 && wave / WR == 0) {
                 part[(int64_t)S::MB * L + wr * T::ROWS + row] = m;
                 part[(int64_t)S::MB * (L + 1) + wr * T::ROWS + row] = l;
