@@ -383,10 +383,9 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
         }
         in_vgpr(sum);
     };
-    // A fragment of V^T: dim tile i, key step x. B register pairs hold keys place(8x + j), j =
-    // 0 .. 7, and so does this
-    // O^T += V^T P^T; with clean, non-finite values count as 0
-    auto add_values = [&](lds_u8 *tile, auto clean) __attribute__((always_inline)) {
+    // O^T += V^T P^T. An A fragment of V^T is dim tile i, key step x; B register pairs hold keys
+    // place(8x + j), j = 0 .. 7, and so does it. With care, only `which` of the values.
+    auto add_values = [&](lds_u8 *tile, auto with_care, Values which) __attribute__((always_inline)) {
         lds_u8 *at[VA][2];
         find_values(tile, at);
         auto value = [&](int i, int x) __attribute__((always_inline)) {
@@ -400,6 +399,19 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
             }
             return f;
         };
+        if constexpr (with_care.value) {
+#pragma unroll
+            for (int i = 0; i < S::ND; ++i) {
+#pragma unroll
+                for (int x = 0; x < XS; ++x) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    o[i] = T::mfma(pick_values(value(i, x), which), pf[x], o[i]);
+                }
+                if constexpr (!S::FLOW)
+                    if (i % S::VG == S::VG - 1) pieces_at(NG + i / S::VG, ISSUES, live && which != OTHERS, from, to);
+            }
+            return;
+        }
         constexpr int VG = S::VG;
         u32x4_t vf[2][VG * XS];
 #pragma unroll
@@ -413,12 +425,29 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
             }
 #pragma unroll
             for (int e = 0; e < VG * XS; ++e) {
-                u32x4_t f = vf[i / VG & 1][e];
-                if constexpr (clean.value) f = finite_values(f);
-                o[i + e / XS] = T::mfma(f, pf[e % XS], o[i + e / XS]);
+                o[i + e / XS] = T::mfma(vf[i / VG & 1][e], pf[e % XS], o[i + e / XS]);
             }
             if constexpr (!S::FLOW) pieces_at(NG + i / VG, ISSUES, live, from, to);
         }
+    };
+    // The same for tile t; odd: some rows see less of it than others, and it has scores that are not
+    // finite. A latent that is not finite must not reach rows that do not see it, whose weight 0 times
+    // it is NaN; for rows that see it that product is right (its score is -inf, weight 0, or they are
+    // NaN throughout): they get +inf and -inf, each a product of the largest number, the others 0. One
+    // loop, not three copies: the 128-row shape has no registers to spare.
+    auto add_values_carefully = [&](lds_u8 *tile, int t, int limit, bool odd) __attribute__((always_inline)) {
+#pragma clang loop unroll(disable)
+        for (int pass = 0; pass < (odd ? 3 : 1); ++pass) {
+            if (pass) {
+                const uint32_t sign = pass == 1 ? 0u : 0x80008000u;
+                const int left = limit - t * KT;
+#pragma unroll
+                for (int i = 0; i < T::NS; i += 2)
+                    pf[i / 8][i % 8 / 2] = seen_pair(T::place(i, grp) < left, T::place(i + 1, grp) < left) ^ sign;
+            }
+            add_values(tile, std::true_type(), pass ? OTHERS : odd ? FINITE : ALL);
+        }
+        in_acc(o);
     };
 
     bool leading = true;                                 // the run's first unit
@@ -457,9 +486,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 for (int i = 0; i < T::NS; ++i) {
                     const float x = s[i / T::NO][i % T::NO];
                     const bool seen = t * KT + T::place(i, grp) < limit, fin = finite_f32(x);
-                    // not finite: so is the key's row, or a query. A row that sees it gets NaN
-                    odd |= !fin;
-                    s[i / T::NO][i % T::NO] = seen ? (fin ? x : NAN) : -INFINITY;
+                    odd |= !fin;                         // so is the key's row, or a query
+                    s[i / T::NO][i % T::NO] = seen ? x : -INFINITY;
                 }
                 odd = __any(odd);
             }
@@ -500,7 +528,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 while (!odd && !grow && t + 1 < t1) {
                     step();
                     scores(next, std::true_type());
-                    add_values(st_before, std::false_type());
+                    add_values(st_before, std::false_type(), ALL);
 #pragma unroll
                     for (int u = 0; u < NT; ++u) s[u] = next[u];
                     inspect(++t);
@@ -510,8 +538,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                     if (!odd && t + 1 < t1) continue;
                 }
                 weight_slice(0, T::NS);
-                if (odd) add_values(st, std::true_type());       // rare
-                else add_values(st, std::false_type());
+                if (odd) add_values_carefully(st, t, limit, true);       // rare
+                else add_values(st, std::false_type(), ALL);
                 in_acc(o);
                 if (++t == t1) break;
                 scored = false;
@@ -524,13 +552,12 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                     inspect(t);
                     if (odd || grow) break;
                     weight_slice(0, T::NS);
-                    add_values(st, std::false_type());
+                    add_values(st, std::false_type(), ALL);
                 } while (++t < t1);
                 if (t >= t1) break;
                 rescale();
                 weight_slice(0, T::NS);
-                add_values(st, std::true_type());
-                in_acc(o);
+                add_values_carefully(st, t, limit, odd);
                 if (++t >= t1) break;
             }
         }

@@ -518,3 +518,37 @@ def test_prefill_wide_hidden_values_may_be_anything(sk, heads, past, bad):
                       True, "rest")
     n = past + 170
     ref.check_prefill(out[:170], lse[:170], q[:170], k[:n], v[:n], r[:n], [170], [n], SCALE, True, "before")
+
+
+# ------------------------------------------------------------------ rows that do see such numbers
+
+@pytest.mark.parametrize("at", [5, 66])                   # in a tile that all rows see whole, in the last
+@pytest.mark.parametrize("place", [L + 3, 7])             # among the rotated numbers, among the latents
+@pytest.mark.parametrize("heads,tokens", [(8, 1), (8, 4), (16, 4), (32, 4)])
+def test_decode_infinite_keys(sk, heads, tokens, place, at):
+    """A key with an infinite number scores +inf or -inf. Rows where it is +inf get NaN; for the
+    others its weight is 0 (NaN in the output where the infinite number is a latent)."""
+    g = gen(22)
+    n = 70
+    cache, table, lens = paged(g, [n], 16)
+    q = normal(g, tokens, heads, DIM)
+    q[:, :, place] = torch.where(q[:, :, place] >= 0, 1, -1).to(BF) * (q[:, :, place].abs() + 1)
+    k = torch.arange(n)
+    keys = cache[table[0, k // 16].long(), k % 16].double()
+    cache[table[0, at // 16], at % 16, place] = math.inf
+    out, lse = sk.latent_decode(q.cuda(), cache.cuda(), table.cuda(), lens.cuda(), SCALE, tokens=tokens)
+    rows = q.reshape(-1, DIM).double()
+    limit = (n - tokens + 1 + torch.arange(tokens)).repeat_interleave(heads)
+    sees = limit > at
+    seen = (k[None] < limit[:, None]) & (k != at)
+    want = ref.attend(rows, keys, keys[:, :L], SCALE, seen)
+    out, lse = out.reshape(-1, L).cpu(), lse.reshape(-1).cpu()
+    up = sees & (rows[:, place] > 0)
+    assert bool(up.any()) and bool((sees & ~up).any())
+    assert bool(torch.isnan(out[up]).all()) and bool(torch.isnan(lse[up]).all())
+    dims = torch.ones(L, dtype=torch.bool)
+    if place < L:
+        dims[place] = False
+        assert bool(torch.isnan(out[sees & ~up][:, place]).all())
+    e, el, d, pv, pv2 = (x[~up] for x in want)
+    ref.check(out[~up][:, dims], lse[~up], (e[:, dims], el, d, pv[:, dims], pv2[:, dims]), n, "infinite key")
