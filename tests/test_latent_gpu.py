@@ -552,3 +552,33 @@ def test_decode_infinite_keys(sk, heads, tokens, place, at):
         assert bool(torch.isnan(out[sees & ~up][:, place]).all())
     e, el, d, pv, pv2 = (x[~up] for x in want)
     ref.check(out[~up][:, dims], lse[~up], (e[:, dims], el, d, pv[:, dims], pv2[:, dims]), n, "infinite key")
+
+
+def test_workspace_of_a_call_belongs_to_its_stream(sk, monkeypatch):
+    """Partial sums that a call allocates for itself are given back while it may still run on the
+    stream it was given: the next tensor of the current stream must not get their memory."""
+    g = gen(23)
+    cache, table, lens = (t.cuda() for t in paged(g, [4000], 64))
+    q = normal(g, 1, 8, DIM).cuda()
+    p = [t.cuda() for t in prefill_inputs(g, [100], [3000], 2)]
+    used = []
+    module = sk.ops._latent()
+
+    class Watch:
+        decode = staticmethod(lambda *x: used.append((x[9].data_ptr(), x[9].numel())) or module.decode(*x))
+        prefill = staticmethod(lambda *x: used.append((x[10].data_ptr(), x[10].numel())) or module.prefill(*x))
+
+    monkeypatch.setattr(sk.ops, "_latent_module", Watch)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    first = sk.latent_decode(q, cache, table, lens, SCALE, stream=side)
+    at, size = used.pop()
+    assert size > 0 and torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() != at
+    second = sk.latent_prefill(*p, starts([100]), starts([3000]), SCALE, stream=side)
+    at, size = used.pop()
+    assert size > 0 and torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() != at
+    torch.cuda.synchronize()
+    monkeypatch.undo()
+    for got, again in ((first, sk.latent_decode(q, cache, table, lens, SCALE)),
+                       (second, sk.latent_prefill(*p, starts([100]), starts([3000]), SCALE))):
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
