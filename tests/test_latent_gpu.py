@@ -582,3 +582,21 @@ def test_workspace_of_a_call_belongs_to_its_stream(sk, monkeypatch):
     for got, again in ((first, sk.latent_decode(q, cache, table, lens, SCALE)),
                        (second, sk.latent_prefill(*p, starts([100]), starts([3000]), SCALE))):
         assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+# ---------------------------------------------------------- the order of query tiles over sequences
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("count", [2, 64, 65, 256, 257, 700])
+def test_prefill_sequences_of_all_lengths(sk, count, causal):
+    """Tiles go by their number of keys; every one of them once, for batches below and past those that
+    are ordered, with sequences of no queries, of no keys and of more keys than queries."""
+    rng = random.Random(count)
+    lq = [rng.choice((0, 1, 5, 130, 300)) if i % 16 == 3 else rng.choice((0, 1, 9, 33)) for i in range(count)]
+    lk = [max(0, n + rng.choice((0, 0, 70, -4))) for n in lq]
+    prefill_case(sk, lq, lk, 1, causal, seed=count)
+
+
+def test_prefill_wide_sequences_of_all_lengths(sk):
+    prefill_case(sk, [300, 0, 513, 1, 900, 256], [300, 9, 200, 0, 1500, 256], 8, True, seed=31)
+    prefill_case(sk, [300, 0, 513, 1, 900, 256], [300, 9, 200, 0, 1500, 256], 3, False, seed=32)
