@@ -623,29 +623,32 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     }
 }
 
-// Joins the partial sums of the units that were cut between workgroups. A wave takes 64 float4 of a
-// unit's sums, WP waves take its partials in turn and meet in LDS; each asks for 4 partials at
-// once, since nothing but the latency of these loads bounds the kernel.
-template <typename T, int WR, int WD, int WP>
+// Joins the partial sums of the units that were cut between workgroups. A wave's lanes are PL groups:
+// each takes the same 64 / PL float4 of a unit's sums, of every PL-th partial. WP waves share a
+// unit's partials further and meet in LDS; each lane asks for 4 partials at once, since nothing but
+// the latency of these loads bounds the kernel.
+template <typename T, int WR, int WD, int WP, int PL>
 __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(DecodeArgs a) {
     typedef Shape<T, WR, WD> S;
-    constexpr int PER = S::MB * L / 4 / 64;              // waves' shares of a unit
+    constexpr int LANES = 64 / PL, TURNS = WP * PL;      // float4s a wave; partials taken side by side
+    constexpr int PER = S::MB * L / 4 / LANES;           // waves' shares of a unit
     constexpr int QUADS = WP > 4 ? 1 : 4 / WP;           // of them, a workgroup's
     static_assert(PER % QUADS == 0, "whole workgroups a unit");
     __shared__ f32x4_t so[WP > 1 ? QUADS * WP : 1][64];
     __shared__ float sm[WP > 1 ? QUADS * WP : 1][64], sl[WP > 1 ? QUADS * WP : 1][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int unit = blockIdx.x / (PER / QUADS);
-    const int quad = blockIdx.x % (PER / QUADS) * QUADS + wave / WP, turn = wave % WP;
+    const int at = (blockIdx.x % (PER / QUADS) * QUADS + wave / WP) * LANES + lane % LANES;     // float4 of the unit
+    const int turn = wave % WP * PL + lane / LANES;
     const int2 cut = a.cuts[unit];
     const int b0 = cut.x >> 1, pieces = cut.y - b0 + 1;
     if (pieces <= 1) return;
     const int req = unit / a.groups, g = unit % a.groups;
 
-    // quad = (wave of the writer, 4-register group) in the partial's order; see the writer
+    // at = (wave of the writer, 4-register group, its lane) in the partial's order; see the writer
     constexpr int PERW = S::ND * S::NO4;
-    const int ww = quad / PERW, rest = quad % PERW, i = rest / S::NO4, x = rest % S::NO4;
-    const int row = (ww % WR) * T::ROWS + T::row(lane);
+    const int wl = at % 64, ww = at / 64 / PERW, rest = at / 64 % PERW, i = rest / S::NO4, x = rest % S::NO4;
+    const int row = (ww % WR) * T::ROWS + T::row(wl);
     float m = -INFINITY, l = 0.0f;
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
     auto merge = [&](float pm, float pl, f32x4_t po) {
@@ -660,19 +663,27 @@ __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(Dec
     auto partial = [&](int j) {
         return a.work + (j == 0 ? (int64_t)cut.x : 2 * (int64_t)(b0 + j)) * part_floats<S::MB>();
     };
-    for (int j = turn; j < pieces; j += 4 * WP) {
+    for (int j = turn; j < pieces; j += 4 * TURNS) {
         float pm[4], pl[4];
         f32x4_t po[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const float *part = partial(min(j + u * WP, pieces - 1));
+            const float *part = partial(min(j + u * TURNS, pieces - 1));
             pm[u] = part[(int64_t)S::MB * L + row];
             pl[u] = part[(int64_t)S::MB * (L + 1) + row];
-            po[u] = reinterpret_cast<const f32x4_t *>(part)[(int64_t)quad * 64 + lane];
+            po[u] = reinterpret_cast<const f32x4_t *>(part)[at];
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (j + u * WP < pieces) merge(pm[u], pl[u], po[u]);
+            if (j + u * TURNS < pieces) merge(pm[u], pl[u], po[u]);
+    }
+    if constexpr (PL > 1) {                              // the lanes' groups, in order: the first's lanes end with all
+        for (int u = 1; u < min(PL, pieces); ++u) {
+            const int from = u * LANES + lane % LANES;
+            const float pm = __shfl(m, from), pl = __shfl(l, from);
+            const f32x4_t po = {__shfl(o[0], from), __shfl(o[1], from), __shfl(o[2], from), __shfl(o[3], from)};
+            if (lane < LANES) merge(pm, pl, po);
+        }
     }
     if constexpr (WP > 1) {
         so[wave][lane] = o;
@@ -680,7 +691,9 @@ __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(Dec
         sl[wave][lane] = l;
         __syncthreads();
         if (turn) return;
-        for (int u = 1; u < min(WP, pieces); ++u) merge(sm[wave + u][lane], sl[wave + u][lane], so[wave + u][lane]);
+        for (int u = 1; u < min(WP, (pieces + PL - 1) / PL); ++u) merge(sm[wave + u][lane], sl[wave + u][lane], so[wave + u][lane]);
+    } else if (turn) {
+        return;
     }
     const int r = g * S::MB + row;
     if (r >= a.rows) return;
@@ -688,17 +701,17 @@ __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(Dec
     const int h = r % a.heads;
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     const u32x2_t y = {pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
-    const int dim = (ww / WR) * (L / WD) + i * T::DIMS + T::place(4 * x, T::grp(lane));
+    const int dim = (ww / WR) * (L / WD) + i * T::DIMS + T::place(4 * x, T::grp(wl));
     *reinterpret_cast<u32x2_t *>(a.out + qr * a.o_row + h * a.o_head + dim) = y;
-    if (a.lse && T::grp(lane) == 0 && ww / WR == 0 && rest == 0)
+    if (a.lse && T::grp(wl) == 0 && ww / WR == 0 && rest == 0)
         a.lse[qr * a.heads + h] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-template <typename T, int WR, int WD, int WP>
+template <typename T, int WR, int WD, int WP, int PL>
 hipError_t launch_join(const DecodeArgs &a, hipStream_t stream) {
-    constexpr int PER = Shape<T, WR, WD>::MB * L / 4 / 64, QUADS = WP > 4 ? 1 : 4 / WP;
+    constexpr int PER = Shape<T, WR, WD>::MB * L / 4 / (64 / PL), QUADS = WP > 4 ? 1 : 4 / WP;
     const unsigned blocks = (unsigned)((int64_t)a.batch * a.groups * (PER / QUADS));
-    hipLaunchKernelGGL((latent_join_kernel<T, WR, WD, WP>), dim3(blocks), dim3(WP > 4 ? WP * 64 : 256), 0, stream, a);
+    hipLaunchKernelGGL((latent_join_kernel<T, WR, WD, WP, PL>), dim3(blocks), dim3(WP > 4 ? WP * 64 : 256), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -709,11 +722,12 @@ hipError_t launch_shape(DecodeArgs a, hipStream_t stream) {
     hipError_t err = hipGetLastError();
     // one workgroup takes every run whole: nothing to join
     if (err != hipSuccess || a.grid == 1) return err;
-    // waves that share a unit's partials: about as many as it has on average
+    // takers of a unit's partials: about as many as it has on average
     const int64_t units = (int64_t)a.batch * a.groups;
-    if (a.grid > 16 * units) return launch_join<T, WR, WD, 16>(a, stream);
-    if (a.grid > 4 * units) return launch_join<T, WR, WD, 4>(a, stream);
-    return launch_join<T, WR, WD, 1>(a, stream);
+    if (a.grid > 64 * units) return launch_join<T, WR, WD, 16, 4>(a, stream);
+    if (a.grid > 16 * units) return launch_join<T, WR, WD, 16, 1>(a, stream);
+    if (a.grid > 4 * units) return launch_join<T, WR, WD, 4, 1>(a, stream);
+    return launch_join<T, WR, WD, 1, 1>(a, stream);
 }
 
 // Rows a workgroup for a request of `rows` query rows: the smallest shape that holds them.
