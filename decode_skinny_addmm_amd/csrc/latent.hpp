@@ -205,17 +205,15 @@ __device__ __forceinline__ void split_value(u32x4_t f, u32x4_t &g, u32x4_t &a1, 
 }
 __device__ __forceinline__ uint32_t seen_pair(bool lo, bool hi) { return (lo ? kBig : 0u) | (hi ? kBig << 16 : 0u); }
 
-// Which values of a fragment a product takes: all as they are; the finite ones, with 0 for the rest;
-// or the largest number in the places of the rest, with 0 for the finite ones. (The same in all lanes.)
-enum Values { ALL, FINITE, OTHERS };
-__device__ __forceinline__ u32x4_t pick_values(u32x4_t f, Values which) {
-    const uint32_t finite = which == OTHERS ? 0u : ~0u, rest = which == ALL ? ~0u : 0u;
-    const uint32_t put = which == OTHERS ? kBig | kBig << 16 : 0u;
+// f's finite values, with 0 for the rest; with others the largest number in the places of the rest, with
+// 0 for the finite ones (others is the same in all lanes).
+__device__ __forceinline__ u32x4_t pick_values(u32x4_t f, bool others) {
+    const uint32_t keep = others ? 0u : ~0u, put = others ? kBig | kBig << 16 : 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t odd = ((f[i] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) |
                              ((f[i] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-        f[i] = (f[i] & ~odd & finite) | (f[i] & odd & rest) | (odd & put);
+        f[i] = (f[i] & ~odd & keep) | (odd & put);
     }
     return f;
 }

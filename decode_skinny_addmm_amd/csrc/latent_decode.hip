@@ -373,6 +373,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
 #pragma unroll
                 for (int e = 0; e < KG; ++e) kf[(gi + 1) & 1][e] = key_frag((gi + 1) * KG + e);
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int e = 0; e < KG; ++e) {
                 const int k_at = gi * KG + e;
@@ -384,8 +385,9 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
         in_vgpr(sum);
     };
     // O^T += V^T P^T. An A fragment of V^T is dim tile i, key step x; B register pairs hold keys
-    // place(8x + j), j = 0 .. 7, and so does it. With care, only `which` of the values.
-    auto add_values = [&](lds_u8 *tile, auto with_care, Values which) __attribute__((always_inline)) {
+    // place(8x + j), j = 0 .. 7, and so does it. With care, of the values only the finite
+    // ones, or `others`.
+    auto add_values = [&](lds_u8 *tile, auto with_care, bool others) __attribute__((always_inline)) {
         lds_u8 *at[VA][2];
         find_values(tile, at);
         auto value = [&](int i, int x) __attribute__((always_inline)) {
@@ -405,10 +407,10 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
 #pragma unroll
                 for (int x = 0; x < XS; ++x) {
                     __builtin_amdgcn_sched_barrier(0);
-                    o[i] = T::mfma(pick_values(value(i, x), which), pf[x], o[i]);
+                    o[i] = T::mfma(pick_values(value(i, x), others), pf[x], o[i]);
                 }
                 if constexpr (!S::FLOW)
-                    if (i % S::VG == S::VG - 1) pieces_at(NG + i / S::VG, ISSUES, live && which != OTHERS, from, to);
+                    if (i % S::VG == S::VG - 1) pieces_at(NG + i / S::VG, ISSUES, live && !others, from, to);
             }
             return;
         }
@@ -423,6 +425,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
 #pragma unroll
                 for (int e = 0; e < VG * XS; ++e) vf[(i / VG + 1) & 1][e] = value(i + VG + e / XS, e % XS);
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int e = 0; e < VG * XS; ++e) {
                 o[i + e / XS] = T::mfma(vf[i / VG & 1][e], pf[e % XS], o[i + e / XS]);
@@ -430,14 +433,14 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
             if constexpr (!S::FLOW) pieces_at(NG + i / VG, ISSUES, live, from, to);
         }
     };
-    // The same for tile t; odd: some rows see less of it than others, and it has scores that are not
-    // finite. A latent that is not finite must not reach rows that do not see it, whose weight 0 times
-    // it is NaN; for rows that see it that product is right (its score is -inf, weight 0, or they are
-    // NaN throughout): they get +inf and -inf, each a product of the largest number, the others 0. One
+    // The same for tile t with scores that are not finite, of which some rows see less than others. A
+    // latent that is not finite must not reach rows that do not see it, whose weight 0 times it is NaN;
+    // for rows that see it that product is right (its score is -inf, weight 0, or they are NaN
+    // throughout): they get +inf and -inf, each a product of the largest number, the others 0. One
     // loop, not three copies: the 128-row shape has no registers to spare.
-    auto add_values_carefully = [&](lds_u8 *tile, int t, int limit, bool odd) __attribute__((always_inline)) {
+    auto add_values_carefully = [&](lds_u8 *tile, int t, int limit) __attribute__((always_inline)) {
 #pragma clang loop unroll(disable)
-        for (int pass = 0; pass < (odd ? 3 : 1); ++pass) {
+        for (int pass = 0; pass < 3; ++pass) {
             if (pass) {
                 const uint32_t sign = pass == 1 ? 0u : 0x80008000u;
                 const int left = limit - t * KT;
@@ -445,7 +448,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 for (int i = 0; i < T::NS; i += 2)
                     pf[i / 8][i % 8 / 2] = seen_pair(T::place(i, grp) < left, T::place(i + 1, grp) < left) ^ sign;
             }
-            add_values(tile, std::true_type(), pass ? OTHERS : odd ? FINITE : ALL);
+            add_values(tile, std::true_type(), pass > 0);
         }
         in_acc(o);
     };
@@ -469,8 +472,12 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 for (int k = 0; k < S::KS; ++k) qf[k] = *(const lds_u32x4 *)(at[k % KA] + (k / KA) * 1024);
             }
         }
+        float zero = 0.0f;
+        asm volatile("" : "+v"(zero));                   // here: a vector of zeros kept for it would go to scratch memory
 #pragma unroll
-        for (int i = 0; i < S::ND; ++i) o[i] = acc_t{0.0f};
+        for (int i = 0; i < S::ND; ++i)
+#pragma unroll
+            for (int j = 0; j < T::NO; ++j) o[i][j] = zero;
         in_acc(o);
         m = -INFINITY;
         l = 0.0f;
@@ -528,7 +535,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 while (!odd && !grow && t + 1 < t1) {
                     step();
                     scores(next, std::true_type());
-                    add_values(st_before, std::false_type(), ALL);
+                    add_values(st_before, std::false_type(), false);
 #pragma unroll
                     for (int u = 0; u < NT; ++u) s[u] = next[u];
                     inspect(++t);
@@ -538,8 +545,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                     if (!odd && t + 1 < t1) continue;
                 }
                 weight_slice(0, T::NS);
-                if (odd) add_values_carefully(st, t, limit, true);       // rare
-                else add_values(st, std::false_type(), ALL);
+                if (odd) add_values_carefully(st, t, limit);     // rare
+                else add_values(st, std::false_type(), false);
                 in_acc(o);
                 if (++t == t1) break;
                 scored = false;
@@ -547,17 +554,24 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
         } else {
             for (int t = t0;;) {
                 do {
-                    step();
-                    scores(s, std::false_type());
-                    inspect(t);
+                    if (!scored) {
+                        step();
+                        scores(s, std::false_type());
+                        inspect(t);
+                    }
+                    scored = false;
                     if (odd || grow) break;
                     weight_slice(0, T::NS);
-                    add_values(st, std::false_type(), ALL);
+                    add_values(st, std::false_type(), false);
                 } while (++t < t1);
                 if (t >= t1) break;
-                rescale();
+                if (grow) rescale();
+                if (!odd) {
+                    scored = true;
+                    continue;
+                }
                 weight_slice(0, T::NS);
-                add_values_carefully(st, t, limit, odd);
+                add_values_carefully(st, t, limit);      // rare
                 if (++t >= t1) break;
             }
         }
