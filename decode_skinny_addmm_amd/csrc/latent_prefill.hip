@@ -509,6 +509,7 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
             __builtin_amdgcn_sched_barrier(0);
             if (g + 1 < NV / G) value_group(g + 1);
             else if (keys_follow) key_group(0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int e = g * G; e < g * G + G; ++e) o[e % ND] = T::mfma(f[g & 1][e % G], pf[e / ND], o[e % ND]);
         }
@@ -518,6 +519,7 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
         for (int g = 0; g < NK / G; ++g) {
             __builtin_amdgcn_sched_barrier(0);
             if (g + 1 < NK / G) key_group(g + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int e = g * G; e < g * G + G; ++e)
                 s[e % NT] = T::mfma(f[g & 1][e % G], qf[e / NT], e / NT ? s[e % NT] : f32x16_t{0.0f});
