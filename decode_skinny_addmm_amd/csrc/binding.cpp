@@ -163,7 +163,9 @@ const at::Tensor &paged_cache(PyObject *o) {
     return t;
 }
 
+// None: no workspace
 Operand workspace_operand(PyObject *o, at::Device dev) {
+    if (o == Py_None) return Operand{"workspace", nullptr};
     const at::Tensor &t = tensor(o, "workspace");
     if (t.scalar_type() != at::kByte || t.device() != dev || !t.is_contiguous())
         refuse("workspace must be a contiguous uint8 tensor on the inputs' GPU");

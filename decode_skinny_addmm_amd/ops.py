@@ -367,17 +367,35 @@ def latent_append(kv, cache, slots, positions, inv_freq, norm_weight=None, eps: 
     return q_out
 
 
-def _workspace(fn, what, device, *sizes, stream=None):
-    """Device memory of the size that fn gives; of `stream` where one is named: memory that is let go
-    before that stream is done with it then comes back to no other."""
+def _workspace_bytes(fn, what, dev, *sizes) -> int:
+    n = ctypes.c_int64()
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*sizes, ctypes.byref(n))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*sizes, ctypes.byref(n))
+    if st:
+        check(st, what)
+    return n.value
+
+
+def _workspace(fn, what, device, *sizes):
     dev = torch.device(device)
     if dev.type != "cuda":
         raise ValueError("device must be a GPU")
-    n = ctypes.c_int64()
-    with torch.cuda.device(dev):
-        check(fn(*sizes, ctypes.byref(n)), what)
-    with torch.cuda.stream(stream):                          # None: the current one
-        return torch.empty(n.value, dtype=torch.uint8, device=dev)
+    return torch.empty(_workspace_bytes(fn, what, dev, *sizes), dtype=torch.uint8, device=dev)
+
+
+def _call_workspace(fn, what, dev, stream, *sizes):
+    """Workspace of one call, None where it needs none; memory of `stream` where one is named: it is let
+    go before that stream is done with it and must come back to no other."""
+    n = _workspace_bytes(fn, what, dev, *sizes)
+    if not n:
+        return None
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=dev)
 
 
 def latent_decode_workspace(batch: int, tokens: int, heads: int, latent: int = LATENT, device="cuda") -> torch.Tensor:
@@ -420,8 +438,8 @@ def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim
         if lse is None:
             lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = _workspace(lib().skinny_latent_decode_workspace, "skinny_latent_decode_workspace", dev,
-                                   rows // tokens, tokens, heads, stream=stream)
+            workspace = _call_workspace(lib().skinny_latent_decode_workspace, "skinny_latent_decode_workspace", dev,
+                                        stream, rows // tokens, tokens, heads)
     _call(_latent().decode, "skinny_latent_decode_bf16", dev, stream, q, cache, table, lens, scale, tokens, rope_dim, out,
           lse, workspace)
     return out, lse
@@ -450,8 +468,8 @@ def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True
         if lse is None:
             lse = torch.empty((nq, heads), dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = _workspace(lib().skinny_latent_prefill_workspace, "skinny_latent_prefill_workspace", dev, nq,
-                                   k.shape[0], cu_q.shape[0] - 1, heads, stream=stream)
+            workspace = _call_workspace(lib().skinny_latent_prefill_workspace, "skinny_latent_prefill_workspace", dev,
+                                        stream, nq, k.shape[0], cu_q.shape[0] - 1, heads)
     _call(_latent().prefill, "skinny_latent_prefill_bf16", dev, stream, q, k, v, k_rot, cu_q, cu_k, scale, causal, out, lse,
           workspace)
     return out, lse
