@@ -8,7 +8,9 @@
 // takes one token and a run of its heads, 8 heads at a time (8 lanes a head, 16 bytes a lane);
 // lane k of the 8 holds the 4 pairs of frequencies 4k .. 4k + 3 in either order of pairs, so
 // its cosines and sines stay in registers for all heads. Angles are taken in 64 bits (positions
-// are many turns), one a lane for half the wave, and handed round by lane reads.
+// are many turns), one a lane for half the wave, and handed round by lane reads. Measured: 8191 tokens
+// x 128 heads 61 us (287 MB, 4.7 TB/s; a large copy reaches 4.9), one token x 8 heads 2.6 us, of
+// which the launch is most.
 #include <algorithm>
 
 #include "latent.hpp"
@@ -163,7 +165,8 @@ hipError_t launch_latent_append(const skinny_latent_append_args &p, hipStream_t 
     a.heads = a.q ? (int)p.heads : 0;
     a.page = (int)p.page;
     a.interleaved = p.interleaved != 0;
-    // heads a wave: all of a token's while that fills the chip, else as few as 8
+    // heads a wave: all of a token's while that fills the chip (angles once a token), else as few as 8
+    // (128 heads: 1 token 4.4 us against 7.4 in one wave, 256 tokens 4.8 against 9.6)
     const int all = std::max(8, (a.heads + 7) / 8 * 8);
     a.chunk = all;
     while (a.chunk > 8 && a.n * ((all + a.chunk - 1) / a.chunk) < 4096) a.chunk = (a.chunk / 2 + 7) / 8 * 8;

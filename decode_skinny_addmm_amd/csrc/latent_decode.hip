@@ -16,6 +16,11 @@
 //   * 4 waves as WR row groups x WD groups of latent dims: each wave computes the whole scores
 //     of its rows (repeated by the WD waves: matrix time is spare, and no scores cross waves)
 //     and its dims of the output, so the only barrier is the ring's.
+// Measured: one request of 131071 keys x 32 heads 32 us (151 MB, 4.8 TB/s; its inner loop 6 TB/s) and 7
+// for the join; 96 requests of about 4000 keys x 128 heads 132 us (485 MB read, 92 MB of partials
+// written) and 22 for the join. With 128 rows the matrix instructions take 40% of a wave's time, and
+// neither they nor memory bound it alone: registers full of sums and queries leave no room to run a
+// tile's softmax beside the next one's products.
 #include <algorithm>
 #include <type_traits>
 
@@ -135,11 +140,12 @@ struct Shape {
     static constexpr int ND = L / T::DIMS / WD;          // dim tiles a wave
     static constexpr int KS = DIM / T::KSTEP;            // K steps of the score product
     static constexpr int NO4 = T::NO / 4;                // 4-register groups of a dim tile
-    // fragments read ahead of the matrix instructions (they need about 130 cycles; a 32 x 32
-    // instruction takes 32 of them): of keys, and of dim tiles of values
     // softmax of a tile beside the score product of the next: takes registers that 128 rows x 512
     // sums leave no room for
     static constexpr bool FLOW = MB < 128;
+    // fragments read ahead of the matrix instructions (they need about 130 cycles; a 32 x 32
+    // instruction takes 32 of them): of keys, and of dim tiles of values. With 128 rows more of them
+    // cost more than they hide (groups of 6 and 2: 83 -> 86 us for 32 requests x 128 heads x 4000 keys)
     static constexpr int KG = MB == 128 ? 4 : 6, VG = MB < 128 && ND >= 4 ? 2 : 1;
 };
 
@@ -639,8 +645,10 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
 
 // Joins the partial sums of the units that were cut between workgroups. A wave's lanes are PL groups:
 // each takes the same 64 / PL float4 of a unit's sums, of every PL-th partial. WP waves share a
-// unit's partials further and meet in LDS; each lane asks for 4 partials at once, since nothing but
-// the latency of these loads bounds the kernel.
+// unit's partials further and meet in LDS; each lane asks for 4 partials at once. With few units the
+// latency of these loads bounds it (256 partials of 32 rows, 17 MB: 7.0 us, of which the launch and the
+// look-up of the cuts are most; 8.5 with whole waves on a partial), with many their bytes
+// (350 partials of 128 rows, 92 MB: 22 us, 4.7 TB/s).
 template <typename T, int WR, int WD, int WP, int PL>
 __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(DecodeArgs a) {
     typedef Shape<T, WR, WD> S;
@@ -744,7 +752,9 @@ hipError_t launch_shape(DecodeArgs a, hipStream_t stream) {
     return launch_join<T, WR, WD, 1, 1>(a, stream);
 }
 
-// Rows a workgroup for a request of `rows` query rows: the smallest shape that holds them.
+// Rows a workgroup for a request of `rows` query rows: the smallest shape that holds them, since each
+// wave computes all rows of its shape (64 requests x 3000 keys, in us: 16 rows 42 in the 16-row shape,
+// 48 in the 32-row one, 86 in the 128-row one; 32 rows 49, 49, 88; 64 rows 64 and 90).
 int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 }  // namespace

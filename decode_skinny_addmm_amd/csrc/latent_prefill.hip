@@ -10,7 +10,9 @@
 // registers, and reads keys and values in tiles of 64 through two LDS stages of 40 KB; two
 // workgroups share a CU, so that one's softmax runs beside the other's matrix instructions.
 // Where the queries are too few to fill the chip, a row's keys are split over several
-// workgroups and their partial sums joined by a second kernel.
+// workgroups and their partial sums joined by a second kernel. Long sequences go to the wide form
+// below. Measured: 6 prompts of 217 .. 1294 tokens x 32 heads 72 us (144 MB at least: 2 TB/s, 480
+// TFLOP/s), 16 prompts of about 256 42 us (3.6 TB/s), one prompt of 129 x 8 heads 9.5 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -71,7 +73,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 
 // The sequence and its query tile that are number `at` of all: first the tiles that see more keys
 // than sequences have on average, then the others, each sequence's from its last, so that a long
-// prompt among short ones does not start last (4000 tokens before 30 x 200, 16 heads: 162 -> 128 us;
+// prompt among short ones does not start last (4000 tokens before 30 x 200, 16 heads: 162 -> 123 us;
 // all in order of their keys costs short prompts 1 us a workgroup to find). Sequence -1: there
 // are fewer.
 template <int BM>
@@ -362,8 +364,11 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs 
 // instructions of a tile (the value product of the tile before, then its score product), waves
 // 4 .. 7 run their softmax, and the other way round; a barrier ends each turn. Left to themselves
 // two waves of a SIMD fall into step, and then neither hides the other (measured with the narrow
-// form at 8192 tokens x 32 heads: matrix and vector time add up, 890 TFLOP/s). Keys and
-// values are staged four tiles deep, all of a CU's LDS.
+// form at 8192 tokens x 32 heads: matrix and vector time add up, 675 us). Keys and
+// values are staged four tiles deep, all of a CU's LDS. Measured there: 598 us, 1150 TFLOP/s; the
+// matrix cores are busy for 59% of the cycles, at the 1.75 GHz that the power limit leaves (a
+// library product of 16384^3 reaches 1600 TFLOP/s). One wave a SIMD with 64 rows, which reads LDS
+// half as often, takes 787 us: it has to issue all vector and matrix instructions by itself.
 constexpr int WIDE_WAVES = 8, WIDE_THREADS = WIDE_WAVES * 64, WIDE_BM = WIDE_WAVES * T::ROWS;
 constexpr int V_BYTES = KT * HD * 2, K_RING = 4, V_RING = 4;
 constexpr int WIDE_LDS = K_RING * K_BYTES + V_RING * V_BYTES;
@@ -639,7 +644,9 @@ __global__ __launch_bounds__(256) void latent_prefill_join_kernel(PrefillArgs a)
     if (a.lse && x == 0) a.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// How a call of these sizes runs. The wide form where sequences have rows to fill it.
+// How a call of these sizes runs. The wide form where sequences have rows to fill it and keys enough
+// for its longer start (causal, 32 heads, wide and narrow in us: 16 prompts of 256 48 and 43, 8 of 512
+// 51 and 50, 8 of 1024 130 and 138, 2 of 2048 92 and 105, 4 chunks of 300 after 4000 keys 136 and 168).
 struct Plan {
     bool wide;
     int64_t tiles;                           // most query tiles that nq rows in batch sequences can need
@@ -651,7 +658,8 @@ Plan plan(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus) {
     const int bm = p.wide ? WIDE_BM : BM;
     p.tiles = std::min(nq, (nq + batch * (bm - 1)) / bm);
     // Splits of the keys: as many as fill the CUs (one wide workgroup each, or two narrow ones),
-    // while each keeps 8 key tiles of the average sequence
+    // while each keeps 8 key tiles of the average sequence (1024 rows x 16024 keys x 8 heads: 8 splits
+    // 89 us, none 392)
     const int64_t room = (p.wide ? 1 : 2) * (int64_t)cus / std::max<int64_t>(1, p.tiles * heads);
     const int64_t most = std::max<int64_t>(1, nk / batch / (8 * KT));
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({room, most, 32}));
