@@ -327,20 +327,21 @@ def _latent():
     return _latent_module
 
 
-def _gpu_of(name, t):
+def _gpu_of(name, t) -> int:
+    """Index of the GPU that tensor t is on."""
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s must be on the GPU" % name)
-    return t.device
+    return t.get_device()
 
 
-def _call(fn, what, dev, stream, *args):
-    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+def _call(fn, what, gpu, stream, *args):
+    raw = torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == gpu:
         st = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(gpu):
             st = fn(*args, raw)
     if st:
         check(st, what)
@@ -359,10 +360,10 @@ def latent_append(kv, cache, slots, positions, inv_freq, norm_weight=None, eps: 
     [32]). q bf16 [n, heads, 64], the rotated part of every head's query, is turned the same way
     into q_out (allocated where None; may be q itself). Returns q_out, or None without q. kv, cache,
     q and q_out may have strides (multiples of 8, contiguous last dimension)."""
-    dev = _gpu_of("kv", kv)
+    gpu = _gpu_of("kv", kv)
     if q is not None and q_out is None:
-        q_out = torch.empty(tuple(q.shape) if isinstance(q, torch.Tensor) else 0, dtype=torch.bfloat16, device=dev)
-    _call(_latent().append, "skinny_latent_append_bf16", dev, stream, kv, cache, slots, positions, inv_freq, norm_weight,
+        q_out = torch.empty(tuple(q.shape) if isinstance(q, torch.Tensor) else 0, dtype=torch.bfloat16, device=kv.device)
+    _call(_latent().append, "skinny_latent_append_bf16", gpu, stream, kv, cache, slots, positions, inv_freq, norm_weight,
           eps, q, q_out, interleaved)
     return q_out
 
@@ -372,7 +373,7 @@ def _workspace_bytes(fn, what, dev, *sizes) -> int:
     if torch.cuda.current_device() == dev.index:
         st = fn(*sizes, ctypes.byref(n))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(dev):                         # the size follows the device
             st = fn(*sizes, ctypes.byref(n))
     if st:
         check(st, what)
@@ -426,8 +427,9 @@ def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim
     ids outside the cache are clamped. q, cache and out may have strides (multiples of 8,
     contiguous last dimension). workspace: latent_decode_workspace(batch, tokens, heads), kept by
     the caller between calls; allocated for this call where None. Returns (out, lse)."""
-    dev = _gpu_of("q", q)
+    gpu = _gpu_of("q", q)
     if out is None or lse is None or workspace is None:
+        dev = q.device
         if q.dim() != 3:
             raise ValueError("q must be 3-D")
         if tokens < 1:
@@ -440,7 +442,7 @@ def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim
         if workspace is None:
             workspace = _call_workspace(lib().skinny_latent_decode_workspace, "skinny_latent_decode_workspace", dev,
                                         stream, rows // tokens, tokens, heads)
-    _call(_latent().decode, "skinny_latent_decode_bf16", dev, stream, q, cache, table, lens, scale, tokens, rope_dim, out,
+    _call(_latent().decode, "skinny_latent_decode_bf16", gpu, stream, q, cache, table, lens, scale, tokens, rope_dim, out,
           lse, workspace)
     return out, lse
 
@@ -456,8 +458,9 @@ def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True
     float32 [nq, heads] (zeros and -inf where a row sees no key). q, k, v, k_rot and out may have
     strides (multiples of 8, contiguous last dimension). workspace: latent_prefill_workspace(nq,
     nk, batch, heads), allocated for this call where None. Returns (out, lse)."""
-    dev = _gpu_of("q", q)
+    gpu = _gpu_of("q", q)
     if out is None or lse is None or workspace is None:
+        dev = q.device
         if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
             raise ValueError("q and k must be 3-D tensors")
         if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 1:
@@ -470,7 +473,7 @@ def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True
         if workspace is None:
             workspace = _call_workspace(lib().skinny_latent_prefill_workspace, "skinny_latent_prefill_workspace", dev,
                                         stream, nq, k.shape[0], cu_q.shape[0] - 1, heads)
-    _call(_latent().prefill, "skinny_latent_prefill_bf16", dev, stream, q, k, v, k_rot, cu_q, cu_k, scale, causal, out, lse,
+    _call(_latent().prefill, "skinny_latent_prefill_bf16", gpu, stream, q, k, v, k_rot, cu_q, cu_k, scale, causal, out, lse,
           workspace)
     return out, lse
 
