@@ -128,6 +128,20 @@ struct Line {
     }
 };
 
+// Runs that the line is cut into: at most one a CU, and with many rows fewer where that leaves less
+// work. A run of r tiles takes r t, and the total / r runs leave partials of b bytes each, written and
+// read at rate w: r t + 2 b total / (r w) is least at r = sqrt(2 b total / (w t)), so that there are
+// sqrt(total) sqrt(w t / 2 b) runs. With the measured t = 1.7 us for 64 rows and 2.4 for 128, and w =
+// 4.5 TB/s (128 heads: 32 requests x 1000 keys 57 -> 50 us, one of 10000 37 -> 34; 64 heads: 2 x 3000
+// 26 -> 25; of 16 and 32 rows the partials are too small to matter).
+template <int MB>
+__device__ __forceinline__ int runs(int most, int64_t total) {
+    const int grid = (int)min((int64_t)most, total);
+    if constexpr (MB < 64) return grid;
+    constexpr float FACTOR = MB == 64 ? 5.4f : 4.5f;
+    return min(grid, max(1, (int)(FACTOR * sqrtf((float)total))));
+}
+
 // Workgroup b's run of the line: [b * total / grid, (b + 1) * total / grid). Runs leave partials
 // 2b (of the run's first unit) and 2b + 1 (of its last, if that is another).
 __device__ __forceinline__ int64_t run_start(int64_t total, int grid, int b) { return total * b / grid; }
@@ -192,7 +206,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
 
     Line line;
     line.measure(a, sh);
-    const int grid = (int)min((int64_t)a.grid, line.total);
+    const int grid = uniform(runs<S::MB>(a.grid, line.total));
     if ((int)blockIdx.x >= grid) return;
     int64_t lo = run_start(line.total, grid, blockIdx.x);
     const int64_t hi = run_start(line.total, grid, blockIdx.x + 1);
@@ -744,10 +758,11 @@ hipError_t launch_shape(DecodeArgs a, hipStream_t stream) {
     hipError_t err = hipGetLastError();
     // one workgroup takes every run whole: nothing to join
     if (err != hipSuccess || a.grid == 1) return err;
-    // takers of a unit's partials: about as many as it has on average
-    const int64_t units = (int64_t)a.batch * a.groups;
-    if (a.grid > 64 * units) return launch_join<T, WR, WD, 16, 4>(a, stream);
-    if (a.grid > 16 * units) return launch_join<T, WR, WD, 16, 1>(a, stream);
+    // takers of a unit's partials: about as many as it has on average, unless that makes more waves
+    // than the chip holds at once (8 requests x 4000 keys x 128 heads 47 us with 16, 44 with 4)
+    const int64_t units = (int64_t)a.batch * a.groups, waves = units * (Shape<T, WR, WD>::MB * L / 4 / 64), room = 16384;
+    if (a.grid > 64 * units && waves * 64 <= room) return launch_join<T, WR, WD, 16, 4>(a, stream);
+    if (a.grid > 16 * units && waves * 16 <= room) return launch_join<T, WR, WD, 16, 1>(a, stream);
     if (a.grid > 4 * units) return launch_join<T, WR, WD, 4, 1>(a, stream);
     return launch_join<T, WR, WD, 1, 1>(a, stream);
 }
