@@ -365,7 +365,7 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs 
 // 4 .. 7 run their softmax, and the other way round; a barrier ends each turn. Left to themselves
 // two waves of a SIMD fall into step, and then neither hides the other (measured with the narrow
 // form at 8192 tokens x 32 heads: matrix and vector time add up, 675 us). Keys and
-// values are staged four tiles deep, all of a CU's LDS. Measured there: 598 us, 1150 TFLOP/s; the
+// values are staged four tiles deep, all of a CU's LDS. Measured there: 607 us, 1130 TFLOP/s; the
 // matrix cores are busy for 59% of the cycles, at the 1.75 GHz that the power limit leaves (a
 // library product of 16384^3 reaches 1600 TFLOP/s). One wave a SIMD with 64 rows, which reads LDS
 // half as often, takes 787 us: it has to issue all vector and matrix instructions by itself.
