@@ -5,7 +5,7 @@
 //     s_k = scale * q . c_k,   out = sum_k softmax(s)_k z_k,   lse = log sum_k exp(s_k).
 //
 // What bounds it: each cached row is 1152 bytes and serves tokens * heads queries at 2 * 1088
-// operations each, so up to 128 query rows a request the cache's bytes bound it.
+// operations each: up to 64 query rows a request the cache's bytes bound it (beyond, see below).
 //   * A workgroup holds all query rows of a request (up to 128; more go in groups) and reads a
 //     contiguous run of its keys once, in tiles of 32 keys through a ring of 4 LDS stages (three
 //     stages, 110 KB, are in flight behind the one computed on). Keys and values are the same
