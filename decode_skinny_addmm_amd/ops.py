@@ -347,6 +347,16 @@ def _call(fn, what, gpu, stream, *args):
         check(st, what)
 
 
+def _new(shape, dtype, dev, stream):
+    """A tensor that a call allocates: memory of `stream` where one is named. The current stream's could
+    still be in use there, and one that is let go before `stream` is done with it must come back to
+    no other."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def latent_append(kv, cache, slots, positions, inv_freq, norm_weight=None, eps: float = 1e-6, q=None, q_out=None,
                   interleaved: bool = False, stream=None):
     """New tokens' rows into a paged latent cache (skinny_latent_append_bf16), in place.
@@ -359,10 +369,11 @@ def latent_append(kv, cache, slots, positions, inv_freq, norm_weight=None, eps: 
     (i, i + 32) or with interleaved (2i, 2i + 1), turn by positions (int64 [n]) * inv_freq (float64
     [32]). q bf16 [n, heads, 64], the rotated part of every head's query, is turned the same way
     into q_out (allocated where None; may be q itself). Returns q_out, or None without q. kv, cache,
-    q and q_out may have strides (multiples of 8, contiguous last dimension)."""
+    q and q_out may have strides (multiples of 8, contiguous last dimension). Here and below, what a
+    call allocates with `stream` named belongs to that stream, as if made with it current."""
     gpu = _gpu_of("kv", kv)
     if q is not None and q_out is None:
-        q_out = torch.empty(tuple(q.shape) if isinstance(q, torch.Tensor) else 0, dtype=torch.bfloat16, device=kv.device)
+        q_out = _new(tuple(q.shape) if isinstance(q, torch.Tensor) else 0, torch.bfloat16, kv.device, stream)
     _call(_latent().append, "skinny_latent_append_bf16", gpu, stream, kv, cache, slots, positions, inv_freq, norm_weight,
           eps, q, q_out, interleaved)
     return q_out
@@ -388,15 +399,9 @@ def _workspace(fn, what, device, *sizes):
 
 
 def _call_workspace(fn, what, dev, stream, *sizes):
-    """Workspace of one call, None where it needs none; memory of `stream` where one is named: it is let
-    go before that stream is done with it and must come back to no other."""
+    """Workspace of one call, None where it needs none."""
     n = _workspace_bytes(fn, what, dev, *sizes)
-    if not n:
-        return None
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=dev)
+    return _new(n, torch.uint8, dev, stream) if n else None
 
 
 def latent_decode_workspace(batch: int, tokens: int, heads: int, latent: int = LATENT, device="cuda") -> torch.Tensor:
@@ -436,9 +441,9 @@ def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim
             raise ValueError("tokens must be at least 1, got %d" % tokens)
         rows, heads = q.shape[:2]
         if out is None:
-            out = torch.empty((rows, heads, LATENT), dtype=torch.bfloat16, device=dev)
+            out = _new((rows, heads, LATENT), torch.bfloat16, dev, stream)
         if lse is None:
-            lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+            lse = _new((rows, heads), torch.float32, dev, stream)
         if workspace is None:
             workspace = _call_workspace(lib().skinny_latent_decode_workspace, "skinny_latent_decode_workspace", dev,
                                         stream, rows // tokens, tokens, heads)
@@ -467,9 +472,9 @@ def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True
             raise ValueError("cu_q must be a tensor [batch + 1]")
         nq, heads = q.shape[:2]
         if out is None:
-            out = torch.empty((nq, heads, HEAD), dtype=torch.bfloat16, device=dev)
+            out = _new((nq, heads, HEAD), torch.bfloat16, dev, stream)
         if lse is None:
-            lse = torch.empty((nq, heads), dtype=torch.float32, device=dev)
+            lse = _new((nq, heads), torch.float32, dev, stream)
         if workspace is None:
             workspace = _call_workspace(lib().skinny_latent_prefill_workspace, "skinny_latent_prefill_workspace", dev,
                                         stream, nq, k.shape[0], cu_q.shape[0] - 1, heads)

@@ -600,3 +600,31 @@ def test_prefill_sequences_of_all_lengths(sk, count, causal):
 def test_prefill_wide_sequences_of_all_lengths(sk):
     prefill_case(sk, [300, 0, 513, 1, 900, 256], [300, 9, 200, 0, 1500, 256], 8, True, seed=31)
     prefill_case(sk, [300, 0, 513, 1, 900, 256], [300, 9, 200, 0, 1500, 256], 3, False, seed=32)
+
+
+def test_outputs_of_a_call_belong_to_its_stream(sk):
+    """Of a call on another stream the caller takes the outputs and lets lse go, or takes nothing: the next
+    tensors of the current stream must not get memory that the call may still write."""
+    g = gen(27)
+    cache, table, lens = (t.cuda() for t in paged(g, [4000], 64))
+    q, kv = normal(g, 1, 8, DIM).cuda(), normal(g, 1, DIM).cuda()
+    p = [t.cuda() for t in prefill_inputs(g, [100], [3000], 2)] + [starts([100]), starts([3000])]
+    at, f = torch.tensor([4095]).cuda(), inv_freq().cuda()
+    calls = (lambda s: (sk.latent_append(kv, cache, at, at, f, q=q[:, :, L:], stream=s),),
+             lambda s: sk.latent_decode(q, cache, table, lens, SCALE, stream=s),
+             lambda s: sk.latent_prefill(*p, SCALE, stream=s))
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        got = call(side)
+        kinds = [(t.shape, t.dtype, t.data_ptr()) for t in got]
+        kept = got[0]
+        del got
+        for shape, dtype, where in kinds[1:]:
+            assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() != where
+        side.synchronize()
+        assert torch.equal(kept, want[0])
+        shape, dtype, where = kinds[0]
+        del kept
+        assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() != where

@@ -114,3 +114,50 @@ def test_the_binding_wants_the_gpu():
         ops.latent_prefill_workspace(1, 1, 1, 1, device="cpu")
     with pytest.raises(ValueError, match="latent"):
         ops.latent_decode_workspace(1, 1, 1, 256)
+
+
+def test_tensors_of_a_call_belong_to_its_stream(monkeypatch):
+    """What a call allocates is memory of the stream that it was given: memory of the current stream could
+    still be in use there, or go to another tensor while the call runs. Nothing is launched here."""
+    named, inside, made = object(), [], []
+
+    class Inside:
+        def __init__(self, stream):
+            assert stream is named
+
+        def __enter__(self):
+            inside.append(1)
+
+        def __exit__(self, *x):
+            inside.pop()
+
+    empty = torch.empty
+
+    def watched(*x, **k):
+        made.append(bool(inside))
+        return empty(*x, **k)
+
+    class Module:
+        append = decode = prefill = staticmethod(lambda *x: 0)
+
+    class Library:
+        skinny_latent_decode_workspace = skinny_latent_prefill_workspace = None
+
+    monkeypatch.setattr(ops.torch.cuda, "stream", Inside)
+    monkeypatch.setattr(ops.torch, "empty", watched)
+    monkeypatch.setattr(ops, "lib", Library)
+    monkeypatch.setattr(ops, "_latent", Module)
+    monkeypatch.setattr(ops, "_gpu_of", lambda name, t: 0)
+    monkeypatch.setattr(ops, "_call", lambda *x: None)
+    monkeypatch.setattr(ops, "_workspace_bytes", lambda *x: 64)
+    q, i = torch.zeros(2, 4, 576, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+    calls = ((1, lambda s: ops.latent_append(q[:, 0], q, i, i, i, q=q[:, :, 512:], stream=s)),
+             (3, lambda s: ops.latent_decode(q, q, i.view(2, 1), i, 1.0, stream=s)),
+             (3, lambda s: ops.latent_prefill(q[:, :, :192], q, q, q, i, i, 1.0, stream=s)))
+    for count, call in calls:
+        call(named)
+        assert made == [True] * count and not inside
+        made.clear()
+        call(None)
+        assert made == [False] * count
+        made.clear()
