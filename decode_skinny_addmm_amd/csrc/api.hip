@@ -8,6 +8,7 @@
 #include <climits>
 #include <cmath>
 #include <initializer_list>
+#include <utility>
 #include <vector>
 
 #include "common.hpp"
@@ -276,6 +277,17 @@ skinny_status check_stride(int64_t stride, int64_t extent, int64_t least) {
     return stride % 8 ? SKINNY_EALIGN : SKINNY_OK;
 }
 
+// Rows of `width` numbers that are written, in two extents, must not overlap: the larger stride steps over
+// all rows of the smaller one. (Strides have passed check_stride; no product that could leave 64 bits.)
+skinny_status check_apart(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t width) {
+    if (n0 <= 1 || n1 <= 1) return SKINNY_OK;
+    if (s0 < s1) {
+        std::swap(s0, s1);
+        std::swap(n0, n1);
+    }
+    return (s0 - width) / s1 >= n1 - 1 ? SKINNY_OK : SKINNY_EINVAL;
+}
+
 skinny_status first_bad(std::initializer_list<skinny_status> all) {
     for (const skinny_status s : all)
         if (s != SKINNY_OK) return s;
@@ -323,6 +335,9 @@ skinny_status run_latent_append(const skinny_latent_append_args *a, void *stream
     if (st != SKINNY_OK) return st;
     if (a->heads > 65536 || a->n > ((int64_t)1 << 31) / 4 || a->page > INT_MAX || a->pages > INT_MAX) return SKINNY_ENOTSUP;
     if (a->n * ((a->heads + 7) / 8 + 1) > INT_MAX) return SKINNY_ENOTSUP;
+    if (check_apart(a->cache_page_stride, a->pages, a->cache_row_stride, a->page, dim) != SKINNY_OK ||
+        (with_q && check_apart(a->q_out_row_stride, a->n, a->q_out_head_stride, a->heads, a->rope) != SKINNY_OK))
+        return SKINNY_EINVAL;
     if (a->n == 0) return SKINNY_OK;
     if (!a->kv || (!a->cache && a->pages > 0) || !a->slots || !a->positions || !a->inv_freq || (with_q && !a->q_out))
         return SKINNY_EINVAL;
@@ -352,6 +367,7 @@ skinny_status run_latent_decode(const skinny_latent_decode_args *a, void *stream
                                         check_stride(a->out_row_stride, rows, a->latent),
                                         check_stride(a->out_head_stride, a->heads, a->latent)});
     if (st != SKINNY_OK) return st;
+    if (check_apart(a->out_row_stride, rows, a->out_head_stride, a->heads, a->latent) != SKINNY_OK) return SKINNY_EINVAL;
     if (a->batch > 1 && (a->table_stride < a->max_pages || a->table_stride > kMaxStride)) return SKINNY_EINVAL;
     if (!a->q || !a->cache || !a->table || !a->lens || !a->out) return SKINNY_EINVAL;
     const void *wide[] = {a->q, a->cache, a->out, a->workspace};
@@ -383,6 +399,7 @@ skinny_status run_latent_prefill(const skinny_latent_prefill_args *a, void *stre
                                         check_stride(a->out_row_stride, a->nq, a->head_dim),
                                         check_stride(a->out_head_stride, a->heads, a->head_dim)});
     if (st != SKINNY_OK) return st;
+    if (check_apart(a->out_row_stride, a->nq, a->out_head_stride, a->heads, a->head_dim) != SKINNY_OK) return SKINNY_EINVAL;
     if (!a->q || !a->out || !a->cu_q || !a->cu_k || (a->nk > 0 && (!a->k || !a->v || !a->k_rot))) return SKINNY_EINVAL;
     const void *wide[] = {a->q, a->k, a->v, a->k_rot, a->out, a->workspace};
     for (const void *p : wide)

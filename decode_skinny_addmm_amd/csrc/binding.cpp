@@ -109,6 +109,18 @@ void want_rows(const Operand &a) {
     if (a.begin % 16) refuse("%s must be 16-byte aligned", a.name);
 }
 
+// Rows that are written: want_rows, and of two extents the larger stride steps over all rows of the
+// smaller one, so that no two rows share numbers.
+void want_apart_rows(const Operand &a) {
+    want_rows(a);
+    const at::Tensor &t = *a.t;
+    if (t.numel() == 0 || t.dim() != 3 || t.size(0) <= 1 || t.size(1) <= 1) return;
+    const int small = t.stride(0) < t.stride(1) ? 0 : 1;
+    if ((t.stride(1 - small) - t.size(2)) / t.stride(small) < t.size(small) - 1)
+        refuse("%s has shape %s and strides %s: its rows must not overlap", a.name, list(t.sizes()).c_str(),
+               list(t.strides()).c_str());
+}
+
 // Judged on byte spans: views that interleave in one wider tensor count as overlapping.
 void want_apart(const Operand &out, std::initializer_list<const Operand *> others) {
     for (const Operand *b : others)
@@ -202,7 +214,7 @@ PyObject *append(PyObject *const *x) {
         q = operand(x[Q], "q", at::kBFloat16, dev, {n, heads, kRope});
         q_out = operand(x[Q_OUT], "q_out", at::kBFloat16, dev, {n, heads, kRope});
         want_rows(q);
-        want_rows(q_out);
+        want_apart_rows(q_out);
     } else if (x[Q_OUT] != Py_None) {
         refuse("q_out needs q");
     }
@@ -210,7 +222,7 @@ PyObject *append(PyObject *const *x) {
     want_contiguous(positions);
     want_contiguous(freq);
     want_rows(kv);
-    want_rows(cache);
+    want_apart_rows(cache);
     want_apart(cache, {&kv, &slots, &positions, &freq, normed ? &weight : nullptr, queries ? &q : nullptr});
     if (queries) {
         const bool in_place = q.begin == q_out.begin && q.t->strides() == q_out.t->strides();
@@ -267,7 +279,7 @@ PyObject *decode(PyObject *const *x) {
     const Operand work = workspace_operand(x[WORK], dev);
     want_rows(q);
     want_rows(cache);
-    want_rows(out);
+    want_apart_rows(out);
     want_contiguous(lens);
     want_contiguous(lse);
     if ((max_pages > 1 && table.stride(1) != 1) || (batch > 1 && table.stride(0) < max_pages))
@@ -320,7 +332,8 @@ PyObject *prefill(PyObject *const *x) {
     const Operand out = operand(x[OUT], "out", at::kBFloat16, dev, {nq, heads, kHead});
     const Operand lse = operand(x[LSE], "lse", at::kFloat, dev, {nq, heads});
     const Operand work = workspace_operand(x[WORK], dev);
-    for (const Operand *o : {&q, &k, &v, &kr, &out}) want_rows(*o);
+    for (const Operand *o : {&q, &k, &v, &kr}) want_rows(*o);
+    want_apart_rows(out);
     for (const Operand *o : {&cq, &ck, &lse}) want_contiguous(*o);
     want_apart(out, {&q, &k, &v, &kr, &cq, &ck});
     want_apart(lse, {&q, &k, &v, &kr, &cq, &ck, &out});

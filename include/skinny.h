@@ -315,7 +315,9 @@ SKINNY_API skinny_status skinny_kda_verify_bf16(const skinny_kda_args *args, voi
  * softmax statistics and norms; each output is rounded once, and the softmax weights once, to
  * bf16, before they meet the values. Strides are in elements, multiples of 8 (rows are read in
  * 16-byte vectors; a stride whose extent is 1 is not looked at), the innermost is 1, and
- * q, cache, kv, k, v, k_rot, out, q_out must be 16-byte aligned (else SKINNY_EALIGN). Device
+ * q, cache, kv, k, v, k_rot, out, q_out must be 16-byte aligned (else SKINNY_EALIGN). Rows that are
+ * written (of the cache in append, q_out, out) must not overlap: of their two strides the larger one
+ * steps over all rows of the smaller (else SKINNY_EINVAL). Device
  * pointers, asynchronous, capturable, no allocation, as everywhere above.
  *
  * Append. Per token n: z = x / sqrt(mean(x^2) + eps) * w over kv[n, :512] (norm_weight NULL: x as

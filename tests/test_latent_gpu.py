@@ -628,3 +628,32 @@ def test_outputs_of_a_call_belong_to_its_stream(sk):
         shape, dtype, where = kinds[0]
         del kept
         assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() != where
+
+
+def test_overlapping_rows_are_refused(sk):
+    """Rows that are written and share numbers with others are a ValueError; rows in another order, or
+    apart from each other, are not."""
+    g = gen(28)
+    store = torch.zeros(1 << 16, dtype=BF, device="cuda")
+    rows = lambda shape, strides: torch.as_strided(store, shape, strides)
+    cache, table, lens = (t.cuda() for t in paged(g, [20, 40, 31], 16))
+    q, kv = normal(g, 3, 4, DIM).cuda(), normal(g, 3, DIM).cuda()
+    slots, f = torch.arange(3).cuda(), inv_freq().cuda()
+    p = [t.cuda() for t in prefill_inputs(g, [9], [9], 2)] + [starts([9]), starts([9])]
+    step = lambda **k: sk.latent_append(kv, k.pop("cache", cache), slots, slots, f, **k)
+    for strides in ((L, L, 1), (3 * L, L, 1), (L, 2 * L, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            sk.latent_decode(q, cache, table, lens, SCALE, out=rows((3, 4, L), strides))
+    for strides in ((HEAD, HEAD, 1), (HEAD, 8 * HEAD, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            sk.latent_prefill(*p, SCALE, out=rows((9, 2, HEAD), strides))
+    for strides in ((DIM, DIM, 1), (DIM * 3, DIM, 1), (DIM, 2 * DIM, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            step(cache=rows((3, 4, DIM), strides))
+    for strides in ((ROT, ROT, 1), (ROT, 2 * ROT, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            step(q=q[:, :, L:], q_out=rows((3, 4, ROT), strides))
+    for out, strides, call in (((3, 4, L), (L, 3 * L, 1), lambda o: sk.latent_decode(q, cache, table, lens, SCALE, out=o)[0]),
+                               ((9, 2, HEAD), (HEAD + 8, 9 * HEAD + 64, 1), lambda o: sk.latent_prefill(*p, SCALE, out=o)[0]),
+                               ((3, 4, ROT), (ROT, 3 * ROT, 1), lambda o: step(q=q[:, :, L:], q_out=o))):
+        assert torch.equal(call(rows(out, strides)), call(torch.empty(out, dtype=BF, device="cuda")))

@@ -161,3 +161,23 @@ def test_tensors_of_a_call_belong_to_its_stream(monkeypatch):
         call(None)
         assert made == [False] * count
         made.clear()
+
+
+# Rows that are written and share numbers: two tokens or heads would race on them.
+@pytest.mark.parametrize("over", [
+    dict(q_out_row_stride=64, q_out_head_stride=64), dict(q_out_row_stride=64 * 7), dict(q_out_row_stride=64, q_out_head_stride=128),
+    dict(cache_page_stride=576), dict(cache_page_stride=576 * 15), dict(cache_page_stride=576, cache_row_stride=576 * 2),
+    dict(cache_page_stride=576 * 16, cache_row_stride=576 + 64)])
+def test_append_refuses_overlapping_rows(L, over):
+    assert L.skinny_latent_append_bf16(ctypes.byref(append_args(**over)), None) == EINVAL
+
+
+@pytest.mark.parametrize("over", [dict(out_row_stride=512), dict(out_row_stride=512 * 7), dict(out_row_stride=512, out_head_stride=512 * 3),
+                                  dict(out_row_stride=(1 << 40) - 8, out_head_stride=1 << 40)])
+def test_decode_refuses_overlapping_rows(L, over):
+    assert L.skinny_latent_decode_bf16(ctypes.byref(decode_args(**over)), None) == EINVAL
+
+
+@pytest.mark.parametrize("over", [dict(out_row_stride=128), dict(out_row_stride=128 * 3), dict(out_row_stride=128, out_head_stride=128 * 9)])
+def test_prefill_refuses_overlapping_rows(L, over):
+    assert L.skinny_latent_prefill_bf16(ctypes.byref(prefill_args(**over)), None) == EINVAL
