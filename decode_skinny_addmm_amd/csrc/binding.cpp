@@ -73,8 +73,12 @@ struct Operand {
     int64_t stride(int d) const { return t->stride(d); }
 };
 
-// Checks an operand's type, device and shape, and takes its span.
-Operand operand(PyObject *o, const char *name, at::ScalarType type, at::Device dev, std::initializer_list<int64_t> shape) {
+// Checks an operand's type, device and shape, and takes its span. One that is written gets memory of its
+// own here if it still shares that of the tensor it was lazily cloned from; so the written operands of
+// a call are taken first, and those that are views of the same storage find it where it is then.
+enum Use { READ, WRITTEN };
+Operand operand(PyObject *o, const char *name, at::ScalarType type, at::Device dev, std::initializer_list<int64_t> shape,
+                Use use = READ) {
     Operand a{name, &tensor(o, name)};
     const at::Tensor &t = *a.t;
     if (t.layout() != at::kStrided) refuse("%s must be a dense tensor", name);
@@ -83,7 +87,7 @@ Operand operand(PyObject *o, const char *name, at::ScalarType type, at::Device d
                list(t.sizes()).c_str());
     if (t.device() != dev)
         refuse("%s is on %s: all tensors must be on %s", name, t.device().str().c_str(), dev.str().c_str());
-    a.begin = a.end = reinterpret_cast<uintptr_t>(t.const_data_ptr());
+    a.begin = a.end = reinterpret_cast<uintptr_t>(use == WRITTEN ? t.mutable_data_ptr() : t.const_data_ptr());
     if (t.numel() > 0) {
         int64_t last = 0;
         for (int64_t d = 0; d < t.dim(); ++d) last += (t.size(d) - 1) * t.stride(d);
@@ -182,7 +186,7 @@ Operand workspace_operand(PyObject *o, at::Device dev) {
     if (t.scalar_type() != at::kByte || t.device() != dev || !t.is_contiguous())
         refuse("workspace must be a contiguous uint8 tensor on the inputs' GPU");
     Operand w{"workspace", &t};
-    w.begin = reinterpret_cast<uintptr_t>(t.const_data_ptr());
+    w.begin = reinterpret_cast<uintptr_t>(t.mutable_data_ptr());
     w.end = w.begin + t.numel();
     return w;
 }
@@ -193,13 +197,24 @@ PyObject *append(PyObject *const *x) {
     if (tensor(x[KV], "kv").dim() != 2) refuse("kv must be 2-D");
     const int64_t n = tensor(x[KV], "kv").size(0);
     const at::Tensor &c = paged_cache(x[CACHE]);
+    const Operand cache = operand(x[CACHE], "cache", at::kBFloat16, dev, {c.size(0), c.size(1), kDim}, WRITTEN);
+    Operand weight{}, q{}, q_out{};
+    const bool normed = x[WEIGHT] != Py_None, queries = x[Q] != Py_None;
+    int64_t heads = 0;
+    if (queries) {
+        if (tensor(x[Q], "q").dim() != 3) refuse("q must be a tensor [n, heads, %lld]", (long long)kRope);
+        heads = tensor(x[Q], "q").size(1);
+        q_out = operand(x[Q_OUT], "q_out", at::kBFloat16, dev, {n, heads, kRope}, WRITTEN);
+        q = operand(x[Q], "q", at::kBFloat16, dev, {n, heads, kRope});
+        want_rows(q);
+        want_apart_rows(q_out);
+    } else if (x[Q_OUT] != Py_None) {
+        refuse("q_out needs q");
+    }
     const Operand kv = operand(x[KV], "kv", at::kBFloat16, dev, {n, kDim});
-    const Operand cache = operand(x[CACHE], "cache", at::kBFloat16, dev, {c.size(0), c.size(1), kDim});
     const Operand slots = operand(x[SLOTS], "slots", at::kLong, dev, {n});
     const Operand positions = operand(x[POSITIONS], "positions", at::kLong, dev, {n});
     const Operand freq = operand(x[FREQ], "inv_freq", at::kDouble, dev, {kRope / 2});
-    Operand weight{}, q{}, q_out{};
-    const bool normed = x[WEIGHT] != Py_None, queries = x[Q] != Py_None;
     if (normed) {
         weight = operand(x[WEIGHT], "norm_weight", at::kBFloat16, dev, {kLatent});
         want_contiguous(weight);
@@ -207,17 +222,6 @@ PyObject *append(PyObject *const *x) {
     }
     const float eps = number(x[EPS], "eps");
     if (!(eps >= 0.0f)) refuse("eps must not be negative, got %S", x[EPS]);
-    int64_t heads = 0;
-    if (queries) {
-        if (tensor(x[Q], "q").dim() != 3) refuse("q must be a tensor [n, heads, %lld]", (long long)kRope);
-        heads = tensor(x[Q], "q").size(1);
-        q = operand(x[Q], "q", at::kBFloat16, dev, {n, heads, kRope});
-        q_out = operand(x[Q_OUT], "q_out", at::kBFloat16, dev, {n, heads, kRope});
-        want_rows(q);
-        want_apart_rows(q_out);
-    } else if (x[Q_OUT] != Py_None) {
-        refuse("q_out needs q");
-    }
     want_contiguous(slots);
     want_contiguous(positions);
     want_contiguous(freq);
@@ -270,13 +274,13 @@ PyObject *decode(PyObject *const *x) {
     if (rows / tokens != batch || rows % tokens)
         refuse("q has %lld rows: table has %lld requests of %lld tokens", (long long)rows, (long long)batch, (long long)tokens);
     const at::Tensor &c = paged_cache(x[CACHE]);
+    const Operand out = operand(x[OUT], "out", at::kBFloat16, dev, {rows, heads, kLatent}, WRITTEN);
+    const Operand lse = operand(x[LSE], "lse", at::kFloat, dev, {rows, heads}, WRITTEN);
+    const Operand work = workspace_operand(x[WORK], dev);
     const Operand q = operand(x[Q], "q", at::kBFloat16, dev, {rows, heads, kDim});
     const Operand cache = operand(x[CACHE], "cache", at::kBFloat16, dev, {c.size(0), c.size(1), kDim});
     const Operand table = operand(x[TABLE], "table", at::kInt, dev, {batch, max_pages});
     const Operand lens = operand(x[LENS], "lens", at::kInt, dev, {batch});
-    const Operand out = operand(x[OUT], "out", at::kBFloat16, dev, {rows, heads, kLatent});
-    const Operand lse = operand(x[LSE], "lse", at::kFloat, dev, {rows, heads});
-    const Operand work = workspace_operand(x[WORK], dev);
     want_rows(q);
     want_rows(cache);
     want_apart_rows(out);
@@ -323,15 +327,15 @@ PyObject *prefill(PyObject *const *x) {
     if (qt.dim() != 3 || kt.dim() != 3) refuse("q and k must be 3-D tensors");
     if (ct.dim() != 1 || ct.size(0) < 1) refuse("cu_q must be a tensor [batch + 1]");
     const int64_t nq = qt.size(0), heads = qt.size(1), nk = kt.size(0), batch = ct.size(0) - 1;
+    const Operand out = operand(x[OUT], "out", at::kBFloat16, dev, {nq, heads, kHead}, WRITTEN);
+    const Operand lse = operand(x[LSE], "lse", at::kFloat, dev, {nq, heads}, WRITTEN);
+    const Operand work = workspace_operand(x[WORK], dev);
     const Operand q = operand(x[Q], "q", at::kBFloat16, dev, {nq, heads, kQuery});
     const Operand k = operand(x[K], "k", at::kBFloat16, dev, {nk, heads, kHead});
     const Operand v = operand(x[V], "v", at::kBFloat16, dev, {nk, heads, kHead});
     const Operand kr = operand(x[K_ROT], "k_rot", at::kBFloat16, dev, {nk, kRope});
     const Operand cq = operand(x[CU_Q], "cu_q", at::kInt, dev, {batch + 1});
     const Operand ck = operand(x[CU_K], "cu_k", at::kInt, dev, {batch + 1});
-    const Operand out = operand(x[OUT], "out", at::kBFloat16, dev, {nq, heads, kHead});
-    const Operand lse = operand(x[LSE], "lse", at::kFloat, dev, {nq, heads});
-    const Operand work = workspace_operand(x[WORK], dev);
     for (const Operand *o : {&q, &k, &v, &kr}) want_rows(*o);
     want_apart_rows(out);
     for (const Operand *o : {&cq, &ck, &lse}) want_contiguous(*o);

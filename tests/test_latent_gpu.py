@@ -657,3 +657,47 @@ def test_overlapping_rows_are_refused(sk):
                                ((9, 2, HEAD), (HEAD + 8, 9 * HEAD + 64, 1), lambda o: sk.latent_prefill(*p, SCALE, out=o)[0]),
                                ((3, 4, ROT), (ROT, 3 * ROT, 1), lambda o: step(q=q[:, :, L:], q_out=o))):
         assert torch.equal(call(rows(out, strides)), call(torch.empty(out, dtype=BF, device="cuda")))
+
+
+# ----------------------------------------------------------------- tensors that share their memory
+
+def test_lazy_clones_are_written_apart(sk):
+    """A lazily cloned tensor shares its memory until it is written: what it was cloned from stays."""
+    g = gen(26)
+    lens = [2000, 17]
+    cache, table, n = (t.cuda() for t in paged(g, lens, 16))
+    heads = 8
+    kept = []
+
+    def lazy(t):
+        kept.append((t, t.clone()))
+        return t._lazy_clone()
+
+    kv, q = normal(g, 5, DIM).cuda(), normal(g, 5, heads, ROT).cuda()
+    slots, pos = torch.arange(5).cuda(), (torch.arange(5) * 100).cuda()
+    f = inv_freq().cuda()
+    want_cache = cache.clone()
+    want_q = sk.latent_append(kv, want_cache, slots, pos, f, q=q)
+    lazy_cache, lazy_q = lazy(cache), lazy(q)
+    lazy_out = lazy(torch.zeros_like(q))
+    sk.latent_append(kv, lazy_cache, slots, pos, f, q=q, q_out=lazy_out)
+    assert torch.equal(lazy_cache, want_cache) and torch.equal(lazy_out, want_q)
+    sk.latent_append(kv, lazy_cache, slots, pos, f, q=lazy_q, q_out=lazy_q)
+    assert torch.equal(lazy_q, want_q)
+
+    qd = normal(g, 2, heads, DIM).cuda()
+    want = sk.latent_decode(qd, cache, table, n, SCALE)
+    out, lse = lazy(torch.zeros_like(want[0])), lazy(torch.zeros_like(want[1]))
+    work = lazy(torch.zeros_like(sk.latent_decode_workspace(2, 1, heads)))
+    sk.latent_decode(qd, cache, table, n, SCALE, out=out, lse=lse, workspace=work)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+    p = [t.cuda() for t in prefill_inputs(g, [100], [3000], 2)] + [starts([100]), starts([3000])]
+    want = sk.latent_prefill(*p, SCALE)
+    out, lse = lazy(torch.zeros_like(want[0])), lazy(torch.zeros_like(want[1]))
+    work = lazy(torch.zeros_like(sk.latent_prefill_workspace(100, 3000, 1, 2)))
+    assert work.numel() > 0
+    sk.latent_prefill(*p, SCALE, out=out, lse=lse, workspace=work)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for origin, before in kept:
+        assert torch.equal(origin, before)
