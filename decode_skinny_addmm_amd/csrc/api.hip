@@ -269,6 +269,7 @@ skinny_status run_kda(const skinny_kda_args *a, void *stream) {
 // ---- latent attention --------------------------------------------------------------------
 
 constexpr int64_t kMaxStride = (int64_t)1 << 40;         // keeps every offset inside 64 bits
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;  // that one launch can take
 
 // A row stride of an extent: unused if the extent is at most 1, else positive and whole vectors.
 skinny_status check_stride(int64_t stride, int64_t extent, int64_t least) {
@@ -333,7 +334,8 @@ skinny_status run_latent_append(const skinny_latent_append_args *a, void *stream
                                                             check_stride(a->q_out_head_stride, a->heads, a->rope)})
                                                : SKINNY_OK});
     if (st != SKINNY_OK) return st;
-    if (a->heads > 65536 || a->n > ((int64_t)1 << 31) / 4 || a->page > INT_MAX || a->pages > INT_MAX) return SKINNY_ENOTSUP;
+    // a wave a token where there are so many (whole workgroups of 4)
+    if (a->heads > 65536 || a->n > kMaxThreads / 256 * 4 || a->page > INT_MAX || a->pages > INT_MAX) return SKINNY_ENOTSUP;
     if (a->n * ((a->heads + 7) / 8 + 1) > INT_MAX) return SKINNY_ENOTSUP;
     if (check_apart(a->cache_page_stride, a->pages, a->cache_row_stride, a->page, dim) != SKINNY_OK ||
         (with_q && check_apart(a->q_out_row_stride, a->n, a->q_out_head_stride, a->heads, a->rope) != SKINNY_OK))
@@ -358,6 +360,7 @@ skinny_status run_latent_decode(const skinny_latent_decode_args *a, void *stream
     if (a->batch > 1 << 20 || a->tokens > 1 << 20 || a->heads > 1 << 16 || a->tokens * a->heads > 1 << 20 ||
         a->batch * a->tokens * a->heads > 1 << 28 || a->pages > INT_MAX || a->page > 1 << 28 || a->max_pages > 1 << 28 || a->max_pages * a->page > 1 << 30)
         return SKINNY_ENOTSUP;
+    if (latent_decode_join_threads(a->batch, a->tokens, a->heads) > kMaxThreads) return SKINNY_ENOTSUP;
     const int64_t rows = a->batch * a->tokens;
     if (rows == 0 || a->heads == 0) return SKINNY_OK;
     if (a->pages < 1 || a->max_pages < 1) return SKINNY_EINVAL;  // a request's first page is always looked up

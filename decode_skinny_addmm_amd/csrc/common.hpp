@@ -74,6 +74,7 @@ hipError_t launch_kda_verify(const skinny_kda_args &a, hipStream_t stream);
 hipError_t launch_latent_append(const skinny_latent_append_args &a, hipStream_t stream);
 hipError_t launch_latent_decode(const skinny_latent_decode_args &a, int cus, hipStream_t stream);
 int64_t latent_decode_workspace_bytes(int64_t batch, int64_t tokens, int64_t heads, int cus);
+int64_t latent_decode_join_threads(int64_t batch, int64_t tokens, int64_t heads);
 hipError_t launch_latent_prefill(const skinny_latent_prefill_args &a, int cus, hipStream_t stream);
 int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus);
 

@@ -781,6 +781,14 @@ int64_t latent_decode_workspace_bytes(int64_t batch, int64_t tokens, int64_t hea
     return 2 * (int64_t)cus * mb * (L + 2) * (int64_t)sizeof(float) + batch * ((rows + mb - 1) / mb) * (int64_t)sizeof(int2);
 }
 
+// Threads of the join kernel where one wave takes all of a unit's partials: one for each 4 numbers of an
+// output. (Where more waves share them the units are fewer than the CUs, and far from any limit.)
+int64_t latent_decode_join_threads(int64_t batch, int64_t tokens, int64_t heads) {
+    const int64_t rows = tokens * heads;
+    const int mb = block_rows(rows);
+    return batch * ((rows + mb - 1) / mb) * mb * (L / 4);
+}
+
 hipError_t launch_latent_decode(const skinny_latent_decode_args &p, int cus, hipStream_t stream) {
     DecodeArgs a;
     a.q = static_cast<const uint16_t *>(p.q);

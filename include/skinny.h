@@ -326,6 +326,7 @@ SKINNY_API skinny_status skinny_kda_verify_bf16(const skinny_kda_args *args, voi
  * slots[n] % page of cache page slots[n] / page; a slot outside the cache (-1 for padding) writes
  * nothing. q (may be NULL) is every head's rotated part [n, heads, 64], turned into q_out, which
  * may be q itself. Two tokens with one slot leave one of the two rows' numbers in each place.
+ * SKINNY_ENOTSUP: more than 2^26 - 4 tokens, 2^16 heads, or 2^31 - 1 tokens times (groups of 8 heads + 1).
  */
 typedef struct skinny_latent_append_args {
     const void *kv;                 /* [n, 576] */
@@ -354,7 +355,8 @@ SKINNY_API skinny_status skinny_latent_append_bf16(const skinny_latent_append_ar
  * numbers too) never reaches it. Lengths outside 0 .. max_pages * page and page ids outside
  * 0 .. pages - 1 are clamped. scale must be positive and finite. workspace: device memory of
  * skinny_latent_decode_workspace(), 16-byte aligned, whose contents need not be kept; calls
- * that may run at the same time need one each.
+ * that may run at the same time need one each. SKINNY_ENOTSUP: 2^25 query rows or more in all, those of a
+ * request filled up to 16, 32, 64 or a multiple of 128; more than 2^30 places a row of the table.
  */
 typedef struct skinny_latent_decode_args {
     const void *q;                  /* [batch * tokens, heads, 576] */

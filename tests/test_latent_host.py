@@ -181,3 +181,13 @@ def test_decode_refuses_overlapping_rows(L, over):
 @pytest.mark.parametrize("over", [dict(out_row_stride=128), dict(out_row_stride=128 * 3), dict(out_row_stride=128, out_head_stride=128 * 9)])
 def test_prefill_refuses_overlapping_rows(L, over):
     assert L.skinny_latent_prefill_bf16(ctypes.byref(prefill_args(**over)), None) == EINVAL
+
+
+def test_refuses_more_threads_than_a_launch_takes(L):
+    """2^32 threads and more are no launch: the join of a decode call starts 128 a row (rows of a request
+    filled up to 16, 32, 64 or a multiple of 128), append a wave a token."""
+    for batch, tokens, heads in ((1 << 18, 1, 128), (1 << 20, 1, 17), (1 << 19, 1, 64), (1 << 17, 2, 65), (1 << 17, 1, 129)):
+        a = decode_args(batch=batch, tokens=tokens, heads=heads, q_row_stride=heads * 576, out_row_stride=heads * 512)
+        assert L.skinny_latent_decode_bf16(ctypes.byref(a), None) == ENOTSUP
+    for n in ((1 << 26) - 3, 1 << 29):
+        assert L.skinny_latent_append_bf16(ctypes.byref(append_args(n=n)), None) == ENOTSUP
