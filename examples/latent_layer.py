@@ -58,7 +58,6 @@ class LatentLayer:
         self.w_o = weight(hidden, heads * HEAD, fan=heads * HEAD)
         self.norm = torch.ones(LATENT, dtype=torch.bfloat16, device=device)
         self.inv_freq = 10000.0 ** (-torch.arange(0, ROT, 2, dtype=torch.float64, device=device) / ROT)
-        self.workspaces = {}
 
     def _project(self, x, cache, slots, positions):
         """The tokens' queries [n, heads, 192], turned in place, and their rows into the cache."""
@@ -81,9 +80,11 @@ class LatentLayer:
         kv = torch.nn.functional.linear(rows[:, :LATENT], self.w_up).view(-1, self.heads, 2 * HEAD)
         return sk.latent_prefill(q, kv[:, :, :HEAD], kv[:, :, HEAD:], rows[:, LATENT:], starts, starts, self.scale)[0]
 
-    def attend_step(self, x, cache, lens, tokens: int = 1):
+    def attend_step(self, x, cache, lens, tokens: int = 1, workspace=None):
         """The same for each request's `tokens` newest positions: x [batch * tokens, hidden], lens
-        int32 [batch] on the device with the new tokens counted."""
+        int32 [batch] on the device with the new tokens counted. workspace: the caller's
+        sk.latent_decode_workspace(batch, tokens, heads), shared by steps that follow each other on one
+        stream (of all layers); None: made for this step."""
         batch, dev = lens.shape[0], x.device
         request = torch.arange(batch, device=dev).repeat_interleave(tokens)
         positions = lens.long()[request] - tokens + torch.arange(tokens, device=dev).repeat(batch)
@@ -91,10 +92,7 @@ class LatentLayer:
         # q . (w_k z) = (w_k' q) . z: the queries carry the keys' expansion
         absorbed = torch.bmm(q[:, :, :HEAD].transpose(0, 1).contiguous(), self.w_k).transpose(0, 1)
         q = torch.cat((absorbed, q[:, :, HEAD:]), dim=-1)
-        if (batch, tokens) not in self.workspaces:
-            self.workspaces[batch, tokens] = sk.latent_decode_workspace(batch, tokens, self.heads, device=dev)
-        z = sk.latent_decode(q, cache.rows, cache.table, lens, self.scale, tokens=tokens,
-                             workspace=self.workspaces[batch, tokens])[0]
+        z = sk.latent_decode(q, cache.rows, cache.table, lens, self.scale, tokens=tokens, workspace=workspace)[0]
         return torch.bmm(z.transpose(0, 1).contiguous(), self.w_v_t).transpose(0, 1)
 
     def output(self, attended, x):
@@ -120,12 +118,13 @@ def main(argv=None):
     y = layer.output(layer.attend_prompts(x, cache, a.prompts), x)
     print("prompts of %s tokens: output %s" % (a.prompts, tuple(y.shape)), flush=True)
     lens = torch.tensor(a.prompts, dtype=torch.int32, device="cuda")
+    workspace = sk.latent_decode_workspace(len(a.prompts), a.tokens, a.heads)
     for i in range(a.steps):
         x = make(len(a.prompts) * a.tokens)
         lens += a.tokens
         torch.cuda.synchronize()
         t = time.perf_counter()
-        y = layer.output(layer.attend_step(x, cache, lens, a.tokens), x)
+        y = layer.output(layer.attend_step(x, cache, lens, a.tokens, workspace), x)
         torch.cuda.synchronize()
         print("step %d, lengths %s: %.0f us" % (i, lens.tolist(), 1e6 * (time.perf_counter() - t)), flush=True)
     return y
