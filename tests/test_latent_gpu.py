@@ -701,3 +701,49 @@ def test_lazy_clones_are_written_apart(sk):
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     for origin, before in kept:
         assert torch.equal(origin, before)
+
+
+# ------------------------------------------- the wide form without a split, joins of many requests
+
+def wide_and_whole(lq, lk, heads, sk):
+    """That a call of these sizes takes the wide form with its keys whole, as one long prompt of many
+    heads does: the averages that the form is chosen by, and no workspace for partial sums."""
+    assert sum(lq) // len(lq) >= 192 and sum(lk) // len(lk) >= 1024
+    assert sk.latent_prefill_workspace(sum(lq), sum(lk), len(lq), heads).numel() == 0
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,heads", [
+    ([1100, 1030], [1100, 1030], 16), ([1500, 0, 1800], [1500, 0, 1800], 9), ([1300, 200, 1800], [1500, 0, 1800], 9),
+    ([257, 1, 700], [3000, 40, 700], 24), ([1100], [1100], 32)])
+def test_prefill_wide_with_whole_keys(sk, lq, lk, heads, causal):
+    wide_and_whole(lq, lk, heads, sk)
+    prefill_case(sk, lq, lk, heads, causal, seed=sum(lk) + heads)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_prefill_wide_whole_keys_hidden_values(sk, bad):
+    n, heads, at = 1100, 32, 700
+    wide_and_whole([n], [n], heads, sk)
+    q, k, v, r = prefill_inputs(gen(25), [n], [n], heads)
+    v[at, :, 5] = bad
+    k[1000, :, 3] = math.nan
+    out, lse = sk.latent_prefill(q.cuda(), k.cuda(), v.cuda(), r.cuda(), starts([n]), starts([n]), SCALE)
+    out, lse = out.cpu(), lse.cpu()
+    assert not bool(torch.isfinite(out[at:, :, 5]).any())
+    assert bool(torch.isnan(out[1000:]).all()) and bool(torch.isnan(lse[1000:]).all())
+    rest = [i for i in range(HEAD) if i != 5]
+    clean = v.clone()
+    clean[at, :, 5] = 0
+    some = [0, 13, 31]
+    ref.check_prefill(out[:1000, some][:, :, rest], lse[:1000, some], q[:1000, some], k[:1000, some],
+                      clean[:1000, some][:, :, rest], r[:1000], [1000], [1000], SCALE, True, "rest")
+    ref.check_prefill(out[:at, some], lse[:at, some], q[:at, some], k[:at, some], v[:at, some], r[:at], [at], [at], SCALE,
+                      True, "before")
+
+
+@pytest.mark.parametrize("heads,tokens", [(16, 1), (32, 1), (8, 4), (64, 1), (128, 1), (40, 4)])
+def test_decode_many_cut_requests(sk, heads, tokens):
+    """At least 64 requests, so that no more than four runs fall on one, long enough that most are cut."""
+    rng = random.Random(heads + tokens)
+    decode_case(sk, [rng.choice((0, 1, 33, 100, 170, 260)) for _ in range(70)], heads, tokens, 16, seed=heads + tokens)
