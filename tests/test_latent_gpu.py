@@ -747,3 +747,37 @@ def test_decode_many_cut_requests(sk, heads, tokens):
     """At least 64 requests, so that no more than four runs fall on one, long enough that most are cut."""
     rng = random.Random(heads + tokens)
     decode_case(sk, [rng.choice((0, 1, 33, 100, 170, 260)) for _ in range(70)], heads, tokens, 16, seed=heads + tokens)
+
+
+# ----------------------------------------------------- infinities of both signs that some rows see
+
+def both_infinities(sk, n, heads, at):
+    """Key `at` has +inf, NaN, -inf in dims 5, 6, 7 of its value and the next key -inf, -inf, +inf: row
+    `at` sees only the first of them, rows after it both, whose sum is NaN, and rows before neither."""
+    print("both infinities", dict(n=n, heads=heads, at=at), flush=True)
+    q, k, v, r = prefill_inputs(gen(24), [n], [n], heads)
+    v[at, :, 5], v[at, :, 6], v[at, :, 7] = math.inf, math.nan, -math.inf
+    v[at + 1, :, 5], v[at + 1, :, 6], v[at + 1, :, 7] = -math.inf, -math.inf, math.inf
+    out, lse = sk.latent_prefill(q.cuda(), k.cuda(), v.cuda(), r.cuda(), starts([n]), starts([n]), SCALE)
+    out, lse = out.cpu(), lse.cpu()
+    assert bool((out[at, :, 5] == math.inf).all()) and bool((out[at, :, 7] == -math.inf).all())
+    assert bool(torch.isnan(out[at, :, 6]).all())
+    assert bool(torch.isnan(out[at + 1:, :, 5:8]).all())
+    dims = [i for i in range(HEAD) if not 5 <= i < 8]
+    some = slice(0, heads, max(1, heads // 2))
+    ref.check_prefill(out[:, some][:, :, dims], lse[:, some], q[:, some], k[:, some], v[:, some][:, :, dims], r, [n], [n],
+                      SCALE, True, "other numbers")
+    ref.check_prefill(out[:at, some], lse[:at, some], q[:at, some], k[:at, some], v[:at, some], r[:at], [at], [at], SCALE,
+                      True, "rows before")
+
+
+@pytest.mark.parametrize("at", [101, 64, 76, 30])         # pairs of one matrix instruction's 16 keys
+def test_prefill_infinities_of_both_signs(sk, at):
+    both_infinities(sk, 150, 2, at)
+
+
+@pytest.mark.parametrize("at", [700, 1050])
+def test_prefill_wide_infinities_of_both_signs(sk, at):
+    n, heads = 1100, 32
+    wide_and_whole([n], [n], heads, sk)
+    both_infinities(sk, n, heads, at)
