@@ -29,20 +29,6 @@ __device__ __forceinline__ void wait_vmcnt() {
     __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// Wait until at most `later` stages of PW loads each are outstanding (later is uniform).
-template <int PW, int MAXL>
-__device__ __forceinline__ void wait_stages(int later) {
-    if constexpr (MAXL >= 1) {
-        if (later >= MAXL) {
-            wait_vmcnt<PW * MAXL>();
-            return;
-        }
-        wait_stages<PW, MAXL - 1>(later);
-    } else {
-        wait_vmcnt<0>();
-    }
-}
-
 // Barrier ordering the workgroup's LDS accesses: this wave's LDS reads are done, outstanding
 // loads straight into LDS are not waited for (each wave has already waited for those it needs).
 __device__ __forceinline__ void lds_barrier() {

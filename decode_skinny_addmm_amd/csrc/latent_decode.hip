@@ -7,9 +7,9 @@
 // What bounds it: each cached row is 1152 bytes and serves tokens * heads queries at 2 * 1088
 // operations each: up to 64 query rows a request the cache's bytes bound it (beyond, see below).
 //   * A workgroup holds all query rows of a request (up to 128; more go in groups) and reads a
-//     contiguous run of its keys once, in tiles of 32 keys through a ring of 4 LDS stages (three
-//     stages, 110 KB, are in flight behind the one computed on). Keys and values are the same
-//     staged rows.
+//     contiguous run of its keys once, in tiles of 32 keys through a ring of 4 LDS stages (two
+//     stages, 74 KB, are in flight behind the one computed on; three with 128 rows, whose value
+//     product does not run a tile behind). Keys and values are the same staged rows.
 //   * One workgroup a CU; the tiles of all requests are one line, cut into equal runs, one a
 //     workgroup, whatever the lengths (which only the device knows). A request cut between
 //     workgroups leaves fp32 partial sums in the workspace, joined by a second kernel.
@@ -18,9 +18,11 @@
 //     and its dims of the output, so the only barrier is the ring's.
 // Measured: one request of 131071 keys x 32 heads 32 us (151 MB, 4.8 TB/s; its inner loop 6 TB/s) and 7
 // for the join; 96 requests of about 4000 keys x 128 heads 132 us (485 MB read, 92 MB of partials
-// written) and 22 for the join. With 128 rows the matrix instructions take 40% of a wave's time, and
-// neither they nor memory bound it alone: registers full of sums and queries leave no room to run a
-// tile's softmax beside the next one's products.
+// written) and 22 for the join; 64 requests of 3000 keys x 64 heads 55 us (240 MB read) and 7.6 for the
+// join. With 128 rows the matrix instructions take 40% of a wave's time (33% of the kernel's, with its
+// start and its uneven end), and neither they nor memory bound it alone: in this layout of one wave a
+// SIMD, registers full of sums and queries leave no room to run a tile's softmax beside the next one's
+// products.
 #include <algorithm>
 #include <type_traits>
 
@@ -131,9 +133,10 @@ struct Line {
 // Runs that the line is cut into: at most one a CU, and with many rows fewer where that leaves less
 // work. A run of r tiles takes r t, and the total / r runs leave partials of b bytes each, written and
 // read at rate w: r t + 2 b total / (r w) is least at r = sqrt(2 b total / (w t)), so that there are
-// sqrt(total) sqrt(w t / 2 b) runs. With the measured t = 1.7 us for 64 rows and 2.4 for 128, and w =
-// 4.5 TB/s (128 heads: 32 requests x 1000 keys 57 -> 50 us, one of 10000 37 -> 34; 64 heads: 2 x 3000
-// 26 -> 25; of 16 and 32 rows the partials are too small to matter).
+// sqrt(total) sqrt(w t / 2 b) runs. With the measured t = 1.7 us for 64 rows and 2.4 for 128 (64 requests
+// of 3000, 6000 and 12000 keys give 1.8 to 1.9 and 2.2 to 2.6, which moves the factors by 6% at most)
+// and w = 4.5 TB/s (128 heads: 32 requests x 1000 keys 57 -> 50 us, one of 10000 37 -> 34; 64 heads:
+// 2 x 3000 26 -> 25; of 16 and 32 rows the partials are too small to matter).
 template <int MB>
 __device__ __forceinline__ int runs(int most, int64_t total) {
     const int grid = (int)min((int64_t)most, total);
@@ -363,8 +366,9 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     // S^T = K Q^T of the staged tile into `sum`, and beside it, in slices between the matrix
     // instructions, the softmax weights of the tile before from s. Fragments are read a group
     // ahead; the scheduling barriers keep the groups apart, and the compiler from spilling.
-    // Weights are rounded to bf16 for the matrix product (relative 2^-9 each, as the values are);
-    // their sum l is of the unrounded ones.
+    // Weights are rounded to bf16 for the matrix product, whose operands are of one type (by 2^-8 relative
+    // at most, independently of each other: an output's error grows from the 0.0017 of its own rounding
+    // to 0.0022 at most in the listed cases); their sum l is of the unrounded ones.
     float mu = 0.0f;
     auto weight_slice = [&](int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll

@@ -12,7 +12,9 @@
 // Where the queries are too few to fill the chip, a row's keys are split over several
 // workgroups and their partial sums joined by a second kernel. Long sequences go to the wide form
 // below. Measured: 6 prompts of 217 .. 1294 tokens x 32 heads 72 us (144 MB at least: 2 TB/s, 480
-// TFLOP/s), 16 prompts of about 256 42 us (3.6 TB/s), one prompt of 129 x 8 heads 9.5 us.
+// TFLOP/s; not causal 103 us, 670 TFLOP/s), 16 prompts of about 256 42 us (3.6 TB/s), one prompt of 129 x
+// 8 heads 9.5 us. Beside its matrix instructions (27% of the cycles with the 6 prompts) a tile waits for
+// all its loads, and each matrix instruction for its fragment from LDS, which is not read ahead as in the wide form.
 #include <algorithm>
 #include <type_traits>
 
@@ -202,8 +204,9 @@ __device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, co
             p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], a.c, -mu));
             l += p[i];
         }
-        // weights are rounded to bf16 for the matrix product (relative 2^-9 each, as the values
-        // are); their sum l is of the unrounded ones
+        // weights are rounded to bf16 for the matrix product, whose operands are of one type (by 2^-8
+        // relative at most, independently of each other: an output's error grows from the 0.0016 of
+        // its own rounding to 0.0019 .. 0.0023); their sum l is of the unrounded ones
         u32x4_t pf[NP / 8];
 #pragma unroll
         for (int i = 0; i < NP / 2; ++i) pf[i / 4][i % 4] = pack_bf16(p[2 * i], p[2 * i + 1]);
@@ -367,7 +370,8 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs 
 // form at 8192 tokens x 32 heads: matrix and vector time add up, 675 us). Keys and
 // values are staged four tiles deep, all of a CU's LDS. Measured there: 607 us, 1130 TFLOP/s; the
 // matrix cores are busy for 59% of the cycles, at the 1.75 GHz that the power limit leaves (a
-// library product of 16384^3 reaches 1600 TFLOP/s). One wave a SIMD with 64 rows, which reads LDS
+// library product of 16384^3 reaches 1600 TFLOP/s); not causal, 4096 tokens x 32 heads, 314 us, 1090
+// TFLOP/s. One wave a SIMD with 64 rows, which reads LDS
 // half as often, takes 787 us: it has to issue all vector and matrix instructions by itself.
 constexpr int WIDE_WAVES = 8, WIDE_THREADS = WIDE_WAVES * 64, WIDE_BM = WIDE_WAVES * T::ROWS;
 constexpr int V_BYTES = KT * HD * 2, K_RING = 4, V_RING = 4;
