@@ -9,18 +9,17 @@ from . import synth  # noqa: F401  (input generators; no arithmetic of the opera
 
 __all__ = ["synth", "addmm", "addmm_default", "addmm_acc_f32", "addmm_shard", "addmm_shard_acc_f32",
            "kbit_gemv", "kbit_gemv_acc_f32", "kda_verify", "latent_append", "latent_decode",
-           "latent_decode_workspace", "latent_prefill", "latent_prefill_workspace", "select_config", "configs", "config_resources", "version",
-           "config_kernel"]
+           "latent_decode_workspace", "latent_prefill", "latent_prefill_workspace",
+           "latent_tree_mask", "latent_tree_decode", "latent_window_decode", "latent_window_prefill",
+           "latent_window_prefill_workspace", "latent_key_weights", "latent_select", "latent_keep", "select_config", "configs",
+           "config_resources", "version", "config_kernel"]
 
 
 def __getattr__(name):
     if name == "ops":
         import importlib
         return importlib.import_module(".ops", __name__)
-    if name in ("addmm", "addmm_default", "addmm_acc_f32", "addmm_shard", "addmm_shard_acc_f32",
-                "kbit_gemv", "kbit_gemv_acc_f32", "kda_verify", "latent_append", "latent_decode",
-                "latent_decode_workspace", "latent_prefill", "latent_prefill_workspace", "select_config", "configs",
-                "config_resources", "version", "config_kernel"):
+    if name in __all__:
         from . import ops
         return getattr(ops, name)
     raise AttributeError(name)

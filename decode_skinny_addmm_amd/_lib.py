@@ -27,7 +27,10 @@ EXPORTED = ("skinny_addmm_bf16", "skinny_select_config", "skinny_addmm_bf16_with
             "skinny_addmm_bf16_acc_f32", "skinny_addmm_bf16_shard", "skinny_addmm_bf16_shard_acc_f32",
             "skinny_kbit_gemv_bf16", "skinny_kbit_gemv_bf16_acc_f32", "skinny_kda_verify_bf16",
             "skinny_latent_append_bf16", "skinny_latent_decode_bf16", "skinny_latent_prefill_bf16",
-            "skinny_latent_decode_workspace", "skinny_latent_prefill_workspace", "skinny_num_configs", "skinny_get_config",
+            "skinny_latent_decode_workspace", "skinny_latent_prefill_workspace", "skinny_latent_masked_decode_bf16",
+            "skinny_latent_tree_mask", "skinny_latent_window_prefill_bf16", "skinny_latent_window_prefill_workspace",
+            "skinny_latent_key_weights_bf16", "skinny_latent_select", "skinny_latent_keep_bf16",
+            "skinny_num_configs", "skinny_get_config",
             "skinny_config_resources", "skinny_status_string", "skinny_last_hip_error",
             "skinny_version", "skinny_probe_null", "skinny_probe_read", "skinny_probe_copy",
             "skinny_probe_read_rows", "skinny_probe_spin", "skinny_config_kernel_name")
@@ -82,6 +85,31 @@ class SkinnyLatentPrefillArgs(ctypes.Structure):
                      [("scale", ctypes.c_float), ("causal", ctypes.c_int32)])
 
 
+class SkinnyLatentMask(ctypes.Structure):
+    """skinny_latent_mask of include/skinny.h."""
+    _fields_ = _args("tree depth", "tree_stride depth_stride window sinks", [])
+
+
+class SkinnyLatentKeyWeightsArgs(ctypes.Structure):
+    """skinny_latent_key_weights_args of include/skinny.h."""
+    _fields_ = _args("q cache table lens lse weights",
+                     "q_row_stride q_head_stride cache_page_stride cache_row_stride table_stride weights_stride "
+                     "batch tokens heads pages page max_pages columns latent rope",
+                     [("scale", ctypes.c_float)])
+
+
+class SkinnyLatentSelectArgs(ctypes.Structure):
+    """skinny_latent_select_args of include/skinny.h."""
+    _fields_ = _args("weights lens kept counts", "weights_stride batch columns budget sinks recent", [])
+
+
+class SkinnyLatentKeepArgs(ctypes.Structure):
+    """skinny_latent_keep_args of include/skinny.h."""
+    _fields_ = _args("cache table lens kept counts new_lens weights new_weights",
+                     "cache_page_stride cache_row_stride table_stride kept_stride weights_stride new_weights_stride "
+                     "batch tokens most pages page max_pages columns latent rope", [])
+
+
 class SkinnyError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -126,6 +154,13 @@ def lib() -> ctypes.CDLL:
     L.skinny_latent_prefill_bf16.argtypes = [ctypes.POINTER(SkinnyLatentPrefillArgs), vp]
     L.skinny_latent_decode_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
     L.skinny_latent_prefill_workspace.argtypes = [i64, i64, i64, i64, ctypes.POINTER(i64)]
+    L.skinny_latent_masked_decode_bf16.argtypes = [ctypes.POINTER(SkinnyLatentDecodeArgs), ctypes.POINTER(SkinnyLatentMask), vp]
+    L.skinny_latent_tree_mask.argtypes = [vp, vp, vp, i64, i64, vp]
+    L.skinny_latent_window_prefill_bf16.argtypes = [ctypes.POINTER(SkinnyLatentPrefillArgs), i64, i64, vp]
+    L.skinny_latent_window_prefill_workspace.argtypes = [i64, i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
+    L.skinny_latent_key_weights_bf16.argtypes = [ctypes.POINTER(SkinnyLatentKeyWeightsArgs), vp]
+    L.skinny_latent_select.argtypes = [ctypes.POINTER(SkinnyLatentSelectArgs), vp]
+    L.skinny_latent_keep_bf16.argtypes = [ctypes.POINTER(SkinnyLatentKeepArgs), vp]
     L.skinny_select_config.argtypes = [i64, i64, i64, cfgp]
     L.skinny_get_config.argtypes = [ctypes.c_int32, cfgp]
     L.skinny_config_resources.argtypes = [cfgp, ctypes.POINTER(SkinnyResources)]
@@ -146,7 +181,9 @@ def lib() -> ctypes.CDLL:
               "skinny_addmm_bf16_shard", "skinny_addmm_bf16_shard_acc_f32",
               "skinny_kbit_gemv_bf16", "skinny_kbit_gemv_bf16_acc_f32", "skinny_kda_verify_bf16",
               "skinny_latent_append_bf16", "skinny_latent_decode_bf16", "skinny_latent_prefill_bf16",
-              "skinny_latent_decode_workspace", "skinny_latent_prefill_workspace", "skinny_select_config", "skinny_get_config", "skinny_config_resources",
+              "skinny_latent_decode_workspace", "skinny_latent_prefill_workspace", "skinny_latent_masked_decode_bf16",
+              "skinny_latent_tree_mask", "skinny_latent_window_prefill_bf16", "skinny_latent_window_prefill_workspace",
+              "skinny_latent_key_weights_bf16", "skinny_latent_select", "skinny_latent_keep_bf16", "skinny_select_config", "skinny_get_config", "skinny_config_resources",
               "skinny_num_configs", "skinny_last_hip_error"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L

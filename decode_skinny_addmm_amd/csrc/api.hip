@@ -350,7 +350,23 @@ skinny_status run_latent_append(const skinny_latent_append_args *a, void *stream
     return hip_status(launch_latent_append(*a, static_cast<hipStream_t>(stream)));
 }
 
-skinny_status run_latent_decode(const skinny_latent_decode_args *a, void *stream) {
+// What a masked decode call adds.
+skinny_status check_mask(const skinny_latent_decode_args &a, const skinny_latent_mask &m) {
+    if (m.window < 0 || m.sinks < 0) return SKINNY_EINVAL;
+    if (!m.tree) return SKINNY_OK;
+    if (a.tokens > 512) return SKINNY_ENOTSUP;
+    const int64_t words = a.tokens * ((a.tokens + 31) / 32);
+    if (m.tree_stride < 0 || m.tree_stride > kMaxStride || (m.tree_stride > 0 && m.tree_stride < words)) return SKINNY_EINVAL;
+    if (!aligned(m.tree, 4) || (m.depth && !aligned(m.depth, 4))) return SKINNY_EALIGN;
+    if (m.window == 0) return SKINNY_OK;
+    if (m.window < a.tokens || !m.depth || m.depth_stride < 0 || m.depth_stride > kMaxStride ||
+        (m.depth_stride > 0 && m.depth_stride < a.tokens))
+        return SKINNY_EINVAL;
+    return SKINNY_OK;
+}
+
+// m NULL: no mask
+skinny_status run_latent_decode(const skinny_latent_decode_args *a, const skinny_latent_mask *m, void *stream) {
     if (!a || a->batch < 0 || a->tokens < 1 || a->heads < 0 || a->pages < 0 || a->page < 1 || a->max_pages < 0 ||
         a->workspace_bytes < 0 || !(a->scale > 0.0f) || !(a->scale < INFINITY))
         return SKINNY_EINVAL;
@@ -362,6 +378,8 @@ skinny_status run_latent_decode(const skinny_latent_decode_args *a, void *stream
         return SKINNY_ENOTSUP;
     if (latent_decode_join_threads(a->batch, a->tokens, a->heads) > kMaxThreads) return SKINNY_ENOTSUP;
     const int64_t rows = a->batch * a->tokens;
+    const skinny_status masked = m ? check_mask(*a, *m) : SKINNY_OK;
+    if (masked != SKINNY_OK) return masked;
     if (rows == 0 || a->heads == 0) return SKINNY_OK;
     if (a->pages < 1 || a->max_pages < 1) return SKINNY_EINVAL;  // a request's first page is always looked up
     const skinny_status st = first_bad({check_stride(a->q_row_stride, rows, dim), check_stride(a->q_head_stride, a->heads, dim),
@@ -381,10 +399,12 @@ skinny_status run_latent_decode(const skinny_latent_decode_args *a, void *stream
     if (!cus) return SKINNY_EHIP;
     if (a->workspace_bytes < latent_decode_workspace_bytes(a->batch, a->tokens, a->heads, cus) || !a->workspace)
         return SKINNY_EINVAL;
-    return hip_status(launch_latent_decode(*a, cus, static_cast<hipStream_t>(stream)));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return hip_status(m ? launch_latent_masked_decode(*a, *m, cus, s) : launch_latent_decode(*a, cus, s));
 }
 
-skinny_status run_latent_prefill(const skinny_latent_prefill_args *a, void *stream) {
+// window 0: none
+skinny_status run_latent_prefill(const skinny_latent_prefill_args *a, int64_t window, int64_t sinks, void *stream) {
     if (!a || a->nq < 0 || a->nk < 0 || a->batch < 0 || a->heads < 0 || a->workspace_bytes < 0 || !(a->scale > 0.0f) ||
         !(a->scale < INFINITY))
         return SKINNY_EINVAL;
@@ -410,9 +430,97 @@ skinny_status run_latent_prefill(const skinny_latent_prefill_args *a, void *stre
     if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || (a->lse && !aligned(a->lse, 4))) return SKINNY_EALIGN;
     const int cus = device_cus();
     if (!cus) return SKINNY_EHIP;
-    const int64_t need = latent_prefill_workspace_bytes(a->nq, a->nk, a->batch, a->heads, cus);
+    const int64_t need = latent_prefill_workspace_bytes(a->nq, a->nk, a->batch, a->heads, window, sinks, cus);
     if (a->workspace_bytes < need || (need > 0 && !a->workspace)) return SKINNY_EINVAL;
-    return hip_status(launch_latent_prefill(*a, cus, static_cast<hipStream_t>(stream)));
+    return hip_status(launch_latent_prefill(*a, window, sinks, cus, static_cast<hipStream_t>(stream)));
+}
+
+skinny_status latent_prefill_workspace(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int64_t window, int64_t sinks,
+                                       int64_t *bytes) {
+    if (!bytes || nq < 0 || nk < 0 || batch < 0 || heads < 0 || window < 0 || sinks < 0) return SKINNY_EINVAL;
+    if (nq > 1 << 30 || nk > 1 << 30 || batch > 1 << 20 || heads > 1 << 16) return SKINNY_ENOTSUP;
+    const int cus = device_cus();
+    if (!cus) return SKINNY_EHIP;
+    *bytes = latent_prefill_workspace_bytes(nq, nk, batch, heads, window, sinks, cus);
+    return SKINNY_OK;
+}
+
+skinny_status run_latent_key_weights(const skinny_latent_key_weights_args *a, void *stream) {
+    if (!a || a->batch < 0 || a->tokens < 1 || a->heads < 0 || a->pages < 0 || a->page < 1 || a->max_pages < 0 ||
+        a->columns < 0 || !(a->scale > 0.0f) || !(a->scale < INFINITY))
+        return SKINNY_EINVAL;
+    if (a->latent != 512 || a->rope != 64) return SKINNY_ENOTSUP;
+    const int64_t dim = a->latent + a->rope;
+    if (a->batch > 1 << 20 || a->tokens > 1 << 20 || a->heads > 1 << 16 || a->tokens * a->heads > 1 << 20 ||
+        a->pages > INT_MAX || a->page > 1 << 28 || a->max_pages > 1 << 28 || a->max_pages * a->page > 1 << 30)
+        return SKINNY_ENOTSUP;
+    const int64_t rows = a->batch * a->tokens;
+    if (rows == 0 || a->heads == 0 || a->columns == 0 || a->max_pages == 0) return SKINNY_OK;
+    if (a->pages < 1) return SKINNY_EINVAL;
+    const skinny_status st = first_bad({check_stride(a->q_row_stride, rows, dim), check_stride(a->q_head_stride, a->heads, dim),
+                                        check_stride(a->cache_page_stride, a->pages, dim),
+                                        check_stride(a->cache_row_stride, a->page, dim)});
+    if (st != SKINNY_OK) return st;
+    if (a->batch > 1 && (a->table_stride < a->max_pages || a->table_stride > kMaxStride || a->weights_stride < a->columns ||
+                         a->weights_stride > kMaxStride))
+        return SKINNY_EINVAL;
+    if (!a->q || !a->cache || !a->table || !a->lens || !a->lse || !a->weights) return SKINNY_EINVAL;
+    if (!aligned(a->q, 16) || !aligned(a->cache, 16) || !aligned(a->table, 4) || !aligned(a->lens, 4) || !aligned(a->lse, 4) ||
+        !aligned(a->weights, 4))
+        return SKINNY_EALIGN;
+    const int cus = device_cus();
+    if (!cus) return SKINNY_EHIP;
+    return hip_status(launch_latent_key_weights(*a, cus, static_cast<hipStream_t>(stream)));
+}
+
+skinny_status run_latent_select(const skinny_latent_select_args *a, void *stream) {
+    if (!a || a->batch < 0 || a->columns < 0 || a->budget < 0 || a->sinks < 0 || a->recent < 0) return SKINNY_EINVAL;
+    if (a->batch > 1 << 20 || a->columns > 1 << 30 || a->budget > 1 << 30) return SKINNY_ENOTSUP;
+    if (a->sinks > a->budget || a->recent > a->budget - a->sinks) return SKINNY_EINVAL;
+    if (a->batch == 0) return SKINNY_OK;
+    if (a->batch > 1 && (a->weights_stride < a->columns || a->weights_stride > kMaxStride)) return SKINNY_EINVAL;
+    if (!a->lens || !a->counts || (!a->weights && a->columns) || (!a->kept && a->budget)) return SKINNY_EINVAL;
+    if (!aligned(a->weights, 4) || !aligned(a->lens, 4) || !aligned(a->kept, 4) || !aligned(a->counts, 4)) return SKINNY_EALIGN;
+    return hip_status(launch_latent_select(*a, static_cast<hipStream_t>(stream)));
+}
+
+skinny_status run_latent_keep(const skinny_latent_keep_args *a, void *stream) {
+    if (!a || a->batch < 0 || a->tokens < 0 || a->most < 0 || a->pages < 0 || a->page < 1 || a->max_pages < 0 || a->columns < 0)
+        return SKINNY_EINVAL;
+    if (a->latent != 512 || a->rope != 64) return SKINNY_ENOTSUP;
+    const int64_t dim = a->latent + a->rope;
+    if (a->batch > 65535 || a->tokens > 1 << 20 || a->most > 1 << 30 || a->pages > INT_MAX || a->page > 1 << 28 ||
+        a->max_pages > 1 << 28 || a->max_pages * a->page > 1 << 30 || a->columns > 1 << 30)
+        return SKINNY_ENOTSUP;
+    if (a->batch == 0) return SKINNY_OK;
+    if (a->max_pages > 0 && a->pages < 1) return SKINNY_EINVAL;
+    const skinny_status st = first_bad({check_stride(a->cache_page_stride, a->pages, dim), check_stride(a->cache_row_stride, a->page, dim)});
+    if (st != SKINNY_OK) return st;
+    if (check_apart(a->cache_page_stride, a->pages, a->cache_row_stride, a->page, dim) != SKINNY_OK) return SKINNY_EINVAL;
+    if (a->batch > 1 && (a->table_stride < a->max_pages || a->table_stride > kMaxStride || a->kept_stride < a->most ||
+                         a->kept_stride > kMaxStride))
+        return SKINNY_EINVAL;
+    if (!a->lens || !a->counts || !a->new_lens || a->new_lens == a->lens || (!a->kept && a->most) ||
+        (a->max_pages > 0 && (!a->cache || !a->table)) || (!a->weights != !a->new_weights && a->columns))
+        return SKINNY_EINVAL;
+    if (a->weights && a->batch > 1 && (a->weights_stride < a->columns || a->weights_stride > kMaxStride ||
+                                       a->new_weights_stride < a->columns || a->new_weights_stride > kMaxStride))
+        return SKINNY_EINVAL;
+    if (!aligned(a->cache, 16)) return SKINNY_EALIGN;
+    const void *words[] = {a->table, a->lens, a->kept, a->counts, a->new_lens, a->weights, a->new_weights};
+    for (const void *p : words)
+        if (!aligned(p, 4)) return SKINNY_EALIGN;
+    return hip_status(launch_latent_keep(*a, static_cast<hipStream_t>(stream)));
+}
+
+skinny_status run_latent_tree_mask(const int32_t *parents, int32_t *mask, int32_t *depth, int64_t batch, int64_t tokens,
+                                   void *stream) {
+    if (batch < 0 || tokens < 0) return SKINNY_EINVAL;
+    if (tokens > 512 || batch > 1 << 20) return SKINNY_ENOTSUP;
+    if (batch == 0 || tokens == 0) return SKINNY_OK;
+    if (!parents || !mask || !depth) return SKINNY_EINVAL;
+    if (!aligned(parents, 4) || !aligned(mask, 4) || !aligned(depth, 4)) return SKINNY_EALIGN;
+    return hip_status(launch_latent_tree_mask(parents, mask, depth, batch, tokens, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -425,11 +533,39 @@ skinny_status skinny_latent_append_bf16(const skinny_latent_append_args *args, v
 }
 
 skinny_status skinny_latent_decode_bf16(const skinny_latent_decode_args *args, void *stream) {
-    return skinny::run_latent_decode(args, stream);
+    return skinny::run_latent_decode(args, nullptr, stream);
+}
+
+skinny_status skinny_latent_masked_decode_bf16(const skinny_latent_decode_args *args, const skinny_latent_mask *mask,
+                                               void *stream) {
+    return mask ? skinny::run_latent_decode(args, mask, stream) : SKINNY_EINVAL;
+}
+
+skinny_status skinny_latent_tree_mask(const int32_t *parents, int32_t *mask, int32_t *depth, int64_t batch, int64_t tokens,
+                                      void *stream) {
+    return skinny::run_latent_tree_mask(parents, mask, depth, batch, tokens, stream);
 }
 
 skinny_status skinny_latent_prefill_bf16(const skinny_latent_prefill_args *args, void *stream) {
-    return skinny::run_latent_prefill(args, stream);
+    return skinny::run_latent_prefill(args, 0, 0, stream);
+}
+
+skinny_status skinny_latent_window_prefill_bf16(const skinny_latent_prefill_args *args, int64_t window, int64_t sinks,
+                                                void *stream) {
+    if (!args || !args->causal || window < 1 || sinks < 0) return SKINNY_EINVAL;
+    return skinny::run_latent_prefill(args, window, sinks, stream);
+}
+
+skinny_status skinny_latent_key_weights_bf16(const skinny_latent_key_weights_args *args, void *stream) {
+    return skinny::run_latent_key_weights(args, stream);
+}
+
+skinny_status skinny_latent_select(const skinny_latent_select_args *args, void *stream) {
+    return skinny::run_latent_select(args, stream);
+}
+
+skinny_status skinny_latent_keep_bf16(const skinny_latent_keep_args *args, void *stream) {
+    return skinny::run_latent_keep(args, stream);
 }
 
 skinny_status skinny_latent_decode_workspace(int64_t batch, int64_t tokens, int64_t heads, int64_t *bytes) {
@@ -442,12 +578,13 @@ skinny_status skinny_latent_decode_workspace(int64_t batch, int64_t tokens, int6
 }
 
 skinny_status skinny_latent_prefill_workspace(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int64_t *bytes) {
-    if (!bytes || nq < 0 || nk < 0 || batch < 0 || heads < 0) return SKINNY_EINVAL;
-    if (nq > 1 << 30 || nk > 1 << 30 || batch > 1 << 20 || heads > 1 << 16) return SKINNY_ENOTSUP;
-    const int cus = skinny::device_cus();
-    if (!cus) return SKINNY_EHIP;
-    *bytes = skinny::latent_prefill_workspace_bytes(nq, nk, batch, heads, cus);
-    return SKINNY_OK;
+    return skinny::latent_prefill_workspace(nq, nk, batch, heads, 0, 0, bytes);
+}
+
+skinny_status skinny_latent_window_prefill_workspace(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int64_t window,
+                                                     int64_t sinks, int64_t *bytes) {
+    if (window < 1) return SKINNY_EINVAL;
+    return skinny::latent_prefill_workspace(nq, nk, batch, heads, window, sinks, bytes);
 }
 
 skinny_status skinny_kda_verify_bf16(const skinny_kda_args *args, void *stream) {

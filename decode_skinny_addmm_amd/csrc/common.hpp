@@ -73,10 +73,20 @@ hipError_t launch_kda_verify(const skinny_kda_args &a, hipStream_t stream);
 // workspace size of one call must be given the same number.
 hipError_t launch_latent_append(const skinny_latent_append_args &a, hipStream_t stream);
 hipError_t launch_latent_decode(const skinny_latent_decode_args &a, int cus, hipStream_t stream);
+hipError_t launch_latent_masked_decode(const skinny_latent_decode_args &a, const skinny_latent_mask &m, int cus,
+                                       hipStream_t stream);
 int64_t latent_decode_workspace_bytes(int64_t batch, int64_t tokens, int64_t heads, int cus);
 int64_t latent_decode_join_threads(int64_t batch, int64_t tokens, int64_t heads);
-hipError_t launch_latent_prefill(const skinny_latent_prefill_args &a, int cus, hipStream_t stream);
-int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus);
+// window 0: none
+hipError_t launch_latent_prefill(const skinny_latent_prefill_args &a, int64_t window, int64_t sinks, int cus,
+                                 hipStream_t stream);
+int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int64_t window, int64_t sinks,
+                                       int cus);
+hipError_t launch_latent_tree_mask(const int32_t *parents, int32_t *mask, int32_t *depth, int64_t batch, int64_t tokens,
+                                   hipStream_t stream);
+hipError_t launch_latent_key_weights(const skinny_latent_key_weights_args &a, int cus, hipStream_t stream);
+hipError_t launch_latent_select(const skinny_latent_select_args &a, hipStream_t stream);
+hipError_t launch_latent_keep(const skinny_latent_keep_args &a, hipStream_t stream);
 
 // Registries filled by each kernel family's translation unit.
 const KernelEntry *gemv_entries(int *count);

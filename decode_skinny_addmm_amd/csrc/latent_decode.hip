@@ -24,9 +24,10 @@
 // SIMD, registers full of sums and queries leave no room to run a tile's softmax beside the next one's
 // products.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
-#include "latent.hpp"
+#include "latent_line.hpp"
 
 namespace skinny {
 namespace {
@@ -56,10 +57,19 @@ struct DecodeArgs {
     int2 *cuts;                              // a unit (request and row group): its first partial, its last workgroup
     int batch, tokens, heads, pages, page, max_pages;
     int rows, groups, grid;                  // rows a request, row groups a request, workgroups
-    uint32_t page_mul;                       // k / page = (k * page_mul) >> (32 + page_shift); 0: page is 1
+    uint32_t page_mul;                       // see page_of
     int page_shift;
     float c;                                 // scale * log2(e)
 };
+
+// What a row sees of the context is bounded, or the new tokens are a tree: see skinny_latent_mask.
+struct MaskedArgs : DecodeArgs {
+    const int32_t *tree, *depth;             // NULL: a chain
+    int64_t tree_row, depth_row;             // strides of a request
+    int words;                               // of a token in tree
+    int window, sinks;                       // window 0: the whole context, sinks 0
+};
+constexpr int MOST_WORDS = 16;               // trees of 512 tokens
 
 // One partial: MB rows x 512 sums in the waves' own register order, then MB maxima, MB sums.
 template <int MB>
@@ -75,60 +85,35 @@ __device__ __forceinline__ int uniform_len(const DecodeArgs &a, int i) {
     typedef const __attribute__((address_space(4))) int32_t *constant_ptr;
     return clamp_len(a, ((constant_ptr)(uintptr_t)a.lens)[i]);
 }
-// tiles of a request; one at least, so that an empty one's outputs are written too
-__device__ __forceinline__ int request_tiles(const DecodeArgs &a, int i) {
-    return max(1, (request_len(a, i) + KT - 1) / KT);
-}
-
-// Sum of v over the workgroup's threads before this one, and over all of them.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &total) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int64_t s = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(s, d);
-        if (lane >= d) s += o;
-    }
-    __syncthreads();
-    if (lane == 63) sh[wave] = s;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) {
-        if (w < wave) before += sh[w];
-        total += sh[w];
-    }
-    return before + s - v;
-}
-
-// Where the line of tiles lies: its length, and for place x the request it belongs to and the place
-// of that request's first tile. Thread i counts requests i * per .. i * per + per - 1.
-struct Line {
-    int64_t total, before;                   // of this thread's requests
-    int per;
-    __device__ __forceinline__ void measure(const DecodeArgs &a, int64_t *sh) {
-        per = (a.batch + THREADS - 1) / THREADS;
-        int64_t v = 0;
-        for (int i = threadIdx.x * per; i < min(a.batch, (int)(threadIdx.x + 1) * per); ++i) v += request_tiles(a, i);
-        before = block_scan(v * a.groups, sh, total);
-        total = uniform(total);
-    }
-    __device__ __forceinline__ void find(const DecodeArgs &a, int64_t x, int64_t *sh, int &req, int64_t &base) const {
-        int64_t at = before;
-        for (int i = threadIdx.x * per; i < min(a.batch, (int)(threadIdx.x + 1) * per); ++i) {
-            const int64_t n = (int64_t)request_tiles(a, i) * a.groups;
-            if (at <= x && x < at + n) {
-                sh[4] = i;
-                sh[5] = at;
-            }
-            at += n;
-        }
-        __syncthreads();
-        req = uniform((int)sh[4]);
-        base = uniform(sh[5]);
-    }
+// The key tiles that a request's rows see between them, in the order in which they are taken: one at
+// least, so that an empty request's outputs are written too. With a window they are those of the
+// first keys and, `skip` further on, those from the first row's window on. (Positions rise by one a step of
+// the chain or tree, the first row's is the lowest, and windows do not begin past it.)
+struct Tiles {
+    int count, head, skip;
+    __device__ __forceinline__ int at(int t) const { return t < head ? t : t + skip; }
 };
+__device__ __forceinline__ Tiles tiles_of(const DecodeArgs &, int len) { return {max(1, (len + KT - 1) / KT), INT_MAX, 0}; }
+__device__ __forceinline__ Tiles tiles_of(const MaskedArgs &a, int len) {
+    Tiles s{max(1, (len + KT - 1) / KT), INT_MAX, 0};
+    if (a.window) {
+        const int head = (min(a.sinks, len) + KT - 1) / KT, from = max(0, len - a.tokens + 1 - a.window) / KT;
+        if (from > head) {
+            s.head = head;
+            s.skip = from - head;
+            s.count -= s.skip;
+        }
+    }
+    return s;
+}
+template <typename A>
+__device__ __forceinline__ int request_tiles(const A &a, int i) { return tiles_of(a, request_len(a, i)).count; }
+
+// Bits b of a tile of keys that starts at k0 with k0 + b < x.
+__device__ __forceinline__ uint32_t keys_below(int x, int k0) {
+    const int n = x - k0;
+    return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
+}
 
 // Runs that the line is cut into: at most one a CU, and with many rows fewer where that leaves less
 // work. A run of r tiles takes r t, and the total / r runs leave partials of b bytes each, written and
@@ -144,12 +129,6 @@ __device__ __forceinline__ int runs(int most, int64_t total) {
     constexpr float FACTOR = MB == 64 ? 5.4f : 4.5f;
     return min(grid, max(1, (int)(FACTOR * sqrtf((float)total))));
 }
-
-// Workgroup b's run of the line: [b * total / grid, (b + 1) * total / grid). Runs leave partials
-// 2b (of the run's first unit) and 2b + 1 (of its last, if that is another).
-__device__ __forceinline__ int64_t run_start(int64_t total, int grid, int b) { return total * b / grid; }
-// the workgroup whose run holds place x (no run is empty: grid <= total)
-__device__ __forceinline__ int run_of(int64_t total, int grid, int64_t x) { return (int)(((x + 1) * grid - 1) / total); }
 
 template <typename T, int WR, int WD>
 struct Shape {
@@ -170,15 +149,17 @@ struct Shape {
 // query rows as QT tiles of 32 rows, then its tiles of keys. One stream through the ring, so that
 // a unit's first tiles are loaded while the last one's outputs are written.
 struct Cursor {
-    int req, g, len, tiles, t, t0, end;      // unit; next item: query tile t + QT if t < 0, else key tile t
+    int req, g, len, t, t0, end;             // unit; next item: query tile t + QT if t < 0, else key tile t
+    Tiles tiles;
     int64_t left;                            // key tiles of the run from this unit on
     bool more;
-    __device__ __forceinline__ void enter(const DecodeArgs &a, int first, int qt) {
+    template <typename A>
+    __device__ __forceinline__ void enter(const A &a, int first, int qt) {
         len = uniform_len(a, req);
-        tiles = max(1, (len + KT - 1) / KT);
+        tiles = tiles_of(a, len);
         t = -qt;
         t0 = first;
-        end = (int)min((int64_t)tiles, first + left);
+        end = (int)min((int64_t)tiles.count, first + left);
     }
 };
 // An item whose load is due: this lane's row (of the request's queries, or of its cache page).
@@ -196,18 +177,21 @@ __device__ __forceinline__ void pieces_at(int at, int of, bool on, const void *s
     }
 }
 
-template <typename T, int WR, int WD>
-__global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
+// MASKED: of the keys before its own, a row sees those of a mask, held a tile as 32 bits.
+template <typename T, int WR, int WD, bool MASKED>
+__global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional_t<MASKED, MaskedArgs, DecodeArgs> a) {
     typedef Shape<T, WR, WD> S;
     typedef typename T::acc_t acc_t;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE_BYTES + 4 * STAGES * 256];
     __shared__ int64_t sh[8];
+    // of each wave's rows, the tree's words and behind them where a row's window begins
+    __shared__ uint32_t masks[MASKED ? THREADS / 64 * T::ROWS * (MOST_WORDS + 1) : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int row = T::row(lane), grp = T::grp(lane);
     const int wr = wave % WR, d0 = (wave / WR) * (L / WD);
     constexpr int QT = (S::MB + KT - 1) / KT;            // query tiles a unit
 
-    Line line;
+    Line<decltype(a), THREADS> line;
     line.measure(a, sh);
     const int grid = uniform(runs<S::MB>(a.grid, line.total));
     if ((int)blockIdx.x >= grid) return;
@@ -232,7 +216,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     c.left = hi - lo;
     c.more = true;
     {
-        const int tiles = max(1, (uniform_len(a, req) + KT - 1) / KT);
+        const int tiles = tiles_of(a, uniform_len(a, req)).count;
         c.g = (int)((lo - base) / tiles);
         c.enter(a, (int)((lo - base) % tiles), QT);
     }
@@ -247,8 +231,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 d.kind = 1;
                 if (++c.t == 0) c.t = c.t0;
             } else {                                     // keys past the end repeat the last one: masked
-                const int k = max(0, min(c.t * KT + kl, c.len - 1));
-                const int page = a.page_mul ? (int)(__umulhi((uint32_t)k, a.page_mul) >> a.page_shift) : k;
+                const int k = max(0, min(c.tiles.at(c.t) * KT + kl, c.len - 1));
+                const int page = page_of(a, k);
                 id = a.table + c.req * a.t_row + page;
                 d.row = k - page * a.page;
                 d.kind = 2;
@@ -462,15 +446,13 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
     // for rows that see it that product is right (its score is -inf, weight 0, or they are NaN
     // throughout): they get +inf and -inf, each a product of the largest number, the others 0. One
     // loop, not three copies: the 128-row shape has no registers to spare.
-    auto add_values_carefully = [&](lds_u8 *tile, int t, int limit) __attribute__((always_inline)) {
+    auto add_values_carefully = [&](lds_u8 *tile, auto sees) __attribute__((always_inline)) {
 #pragma clang loop unroll(disable)
         for (int pass = 0; pass < 3; ++pass) {
             if (pass) {
                 const uint32_t sign = pass == 1 ? 0u : 0x80008000u;
-                const int left = limit - t * KT;
 #pragma unroll
-                for (int i = 0; i < T::NS; i += 2)
-                    pf[i / 8][i % 8 / 2] = seen_pair(T::place(i, grp) < left, T::place(i + 1, grp) < left) ^ sign;
+                for (int i = 0; i < T::NS; i += 2) pf[i / 8][i % 8 / 2] = seen_pair(sees(i), sees(i + 1)) ^ sign;
             }
             add_values(tile, std::true_type(), pass > 0);
         }
@@ -479,12 +461,51 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
 
     bool leading = true;                                 // the run's first unit
     while (lo < hi) {
-        const int len = uniform_len(a, req), tiles = max(1, (len + KT - 1) / KT);
+        const int len = uniform_len(a, req);
+        const Tiles span = tiles_of(a, len);
+        const int tiles = span.count;
         const int g = (int)((lo - base) / tiles), t0 = (int)((lo - base) % tiles);
         const int t1 = (int)min((int64_t)tiles, t0 + (hi - lo));
         // keys this lane's row sees: it is row (token, head) of the request; rows past the last repeat it
         const int limit = max(0, len - a.tokens + 1 + min(g * S::MB + wr * T::ROWS + row, a.rows - 1) / a.heads);
-        const int whole = max(0, len - a.tokens + 1) / KT;       // tiles before this: all rows see all of them
+        int whole = max(0, len - a.tokens + 1) / KT;             // tiles before this: all rows see all of them
+        int some = 0;                                            // (with a window: those from this one on)
+        if constexpr (MASKED) {
+            // The row's words, and where its window begins, come to LDS: the masks of a unit's few tiles that are
+            // not seen whole are made from them where they are needed, and no registers are held for them.
+            const int j = min(g * S::MB + wr * T::ROWS + row, a.rows - 1) / a.heads;
+            uint32_t *mine = masks + wave * T::ROWS * (MOST_WORDS + 1) + row;
+            int begin = 0;
+            if (a.tree) {
+                whole = max(0, len - a.tokens) / KT;
+                const int32_t *words = a.tree + req * a.tree_row + (int64_t)j * a.words;
+                for (int w = grp; w < a.words; w += 64 / T::ROWS) mine[w * T::ROWS] = words[w];
+                if (a.window) begin = len - a.tokens + 1 - a.window + min(max(a.depth[req * a.depth_row + j], 0), a.tokens - 1);
+            } else if (a.window) {
+                begin = limit - a.window;
+            }
+            if (grp == 0) mine[MOST_WORDS * T::ROWS] = max(0, begin);
+            if (a.window) some = (max(0, len - a.window) + KT - 1) / KT;
+        }
+        // of tile t of the line, the keys that this lane's row sees: bit b for key b of it
+        auto seen_keys = [&](int t) __attribute__((always_inline)) -> uint32_t {
+            const int k0 = span.at(t) * KT;
+            if constexpr (!MASKED) {
+                return keys_below(limit, k0);
+            } else {
+                const uint32_t *mine = masks + wave * T::ROWS * (MOST_WORDS + 1) + row;
+                const int own = len - a.tokens;                  // the first new token
+                uint32_t seen = keys_below(a.tree ? own : limit, k0);
+                if (a.window) seen &= keys_below(a.sinks, k0) | ~keys_below((int)mine[MOST_WORDS * T::ROWS], k0);
+                if (a.tree && k0 + KT > own) {
+                    const int first = k0 - own, w = first >> 5;  // w of -1: the tile begins in the context
+                    const uint32_t low = w >= 0 && w < a.words ? mine[w * T::ROWS] : 0u;
+                    const uint32_t high = w + 1 < a.words ? mine[(w + 1) * T::ROWS] : 0u;
+                    seen |= (uint32_t)(((uint64_t)high << 32 | low) >> (first & 31)) & keys_below(len, k0);
+                }
+                return seen;
+            }
+        };
 
         for (int qi = 0; qi < QT; ++qi) {
             step();
@@ -512,11 +533,13 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
         bool odd, grow;
         auto inspect = [&](int t) __attribute__((always_inline)) {
             odd = false;
-            if (t >= whole) {
+            const int at = MASKED ? span.at(t) : t;
+            if (at >= whole || (MASKED && at < some)) {
+                const uint32_t keys = MASKED ? seen_keys(t) >> T::place(0, grp) : 0u;
 #pragma unroll
                 for (int i = 0; i < T::NS; ++i) {
                     const float x = s[i / T::NO][i % T::NO];
-                    const bool seen = t * KT + T::place(i, grp) < limit, fin = finite_f32(x);
+                    const bool seen = MASKED ? keys >> T::place(i, 0) & 1 : t * KT + T::place(i, grp) < limit, fin = finite_f32(x);
                     odd |= !fin;                         // so is the key's row, or a query
                     s[i / T::NO][i % T::NO] = seen ? x : -INFINITY;
                 }
@@ -544,6 +567,11 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                 in_acc(o);
             }
         };
+        auto sees_of = [&](int t) __attribute__((always_inline)) {
+            const uint32_t keys = MASKED ? seen_keys(t) : 0u;
+            const int left = limit - t * KT;
+            return [=](int i) { return MASKED ? keys >> T::place(i, grp) & 1 : T::place(i, grp) < left; };
+        };
         // The inner loops have no branch that touches the output sums: one that did would move all
         // of them between register files in every iteration. A reference maximum that moves and a
         // non-finite score in a masked tile leave them.
@@ -569,7 +597,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                     if (!odd && t + 1 < t1) continue;
                 }
                 weight_slice(0, T::NS);
-                if (odd) add_values_carefully(st, t, limit);     // rare
+                if (odd) add_values_carefully(st, sees_of(t));     // rare
                 else add_values(st, std::false_type(), false);
                 in_acc(o);
                 if (++t == t1) break;
@@ -595,7 +623,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(DecodeArgs a) {
                     continue;
                 }
                 weight_slice(0, T::NS);
-                add_values_carefully(st, t, limit);      // rare
+                add_values_carefully(st, sees_of(t));      // rare
                 if (++t >= t1) break;
             }
         }
@@ -755,10 +783,10 @@ hipError_t launch_join(const DecodeArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <typename T, int WR, int WD>
-hipError_t launch_shape(DecodeArgs a, hipStream_t stream) {
+template <typename T, int WR, int WD, typename A>
+hipError_t launch_shape(A a, hipStream_t stream) {
     a.cuts = reinterpret_cast<int2 *>(a.work + 2 * a.grid * part_floats<Shape<T, WR, WD>::MB>());
-    hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD>), dim3((unsigned)a.grid), dim3(THREADS), 0, stream, a);
+    hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, std::is_same_v<A, MaskedArgs>>), dim3((unsigned)a.grid), dim3(THREADS), 0, stream, a);
     hipError_t err = hipGetLastError();
     // one workgroup takes every run whole: nothing to join
     if (err != hipSuccess || a.grid == 1) return err;
@@ -793,7 +821,7 @@ int64_t latent_decode_join_threads(int64_t batch, int64_t tokens, int64_t heads)
     return batch * ((rows + mb - 1) / mb) * mb * (L / 4);
 }
 
-hipError_t launch_latent_decode(const skinny_latent_decode_args &p, int cus, hipStream_t stream) {
+static DecodeArgs decode_args(const skinny_latent_decode_args &p, int cus) {
     DecodeArgs a;
     a.q = static_cast<const uint16_t *>(p.q);
     a.q_row = p.q_row_stride;
@@ -816,24 +844,42 @@ hipError_t launch_latent_decode(const skinny_latent_decode_args &p, int cus, hip
     a.page = (int)p.page;
     a.max_pages = (int)p.max_pages;
     a.rows = a.tokens * a.heads;
-    // 2^bits >= page > 2^(bits - 1): the reciprocal 2^(31 + bits) / page, rounded up, fits 32 bits, and
-    // for k < 2^30 its rounding adds less than 2^-(1 + bits) < 1 / page to the quotient: exact
-    int bits = 1;
-    while ((1 << bits) < a.page) ++bits;
-    a.page_mul = a.page == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + bits)) + a.page - 1) / a.page);
-    a.page_shift = bits - 1;
+    page_reciprocal(a.page, a.page_mul, a.page_shift);
     const int mb = block_rows(a.rows);
     a.groups = (a.rows + mb - 1) / mb;
     a.c = p.scale * kLog2e;
     // no more workgroups than the line can have tiles
     const int64_t most = (int64_t)a.batch * a.groups * std::max<int64_t>(1, (p.max_pages * p.page + KT - 1) / KT);
     a.grid = (int)std::min<int64_t>(cus, most);
-    switch (mb) {
+    return a;
+}
+
+template <typename A>
+static hipError_t launch(const A &a, hipStream_t stream) {
+    switch (block_rows(a.rows)) {
         case 16: return launch_shape<Tile16, 1, 4>(a, stream);
         case 32: return launch_shape<Tile16, 2, 2>(a, stream);
         case 64: return launch_shape<Tile16, 4, 1>(a, stream);
         default: return launch_shape<Tile32, 4, 1>(a, stream);
     }
+}
+
+hipError_t launch_latent_decode(const skinny_latent_decode_args &p, int cus, hipStream_t stream) {
+    return launch(decode_args(p, cus), stream);
+}
+
+hipError_t launch_latent_masked_decode(const skinny_latent_decode_args &p, const skinny_latent_mask &m, int cus,
+                                       hipStream_t stream) {
+    MaskedArgs a;
+    static_cast<DecodeArgs &>(a) = decode_args(p, cus);
+    a.tree = m.tree;
+    a.depth = m.depth;
+    a.tree_row = m.tree_stride;
+    a.depth_row = m.depth_stride;
+    a.words = (int)((p.tokens + 31) / 32);
+    a.window = (int)std::min<int64_t>(m.window, INT_MAX / 2);
+    a.sinks = m.window ? (int)std::min<int64_t>(m.sinks, INT_MAX / 2) : 0;
+    return launch(a, stream);
 }
 
 }  // namespace skinny

@@ -1,0 +1,87 @@
+// latent_line.hpp -- one line of work for requests whose lengths only the device knows (gfx950 only).
+//
+// The key tiles of all requests, one request after the other (times `groups` for kernels that take a
+// request's rows in groups), form a line. Workgroups take equal runs of it, whatever the lengths.
+// An argument struct A names batch and groups, and request_tiles(a, i) the tiles of request i.
+#pragma once
+
+#include "latent.hpp"
+
+namespace skinny {
+namespace latent {
+
+// Sum of v over the workgroup's threads before this one, and over all of them.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &total) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int64_t s = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up(s, d);
+        if (lane >= d) s += o;
+    }
+    __syncthreads();
+    if (lane == 63) sh[wave] = s;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        if (w < wave) before += sh[w];
+        total += sh[w];
+    }
+    return before + s - v;
+}
+
+// Where the line of tiles lies: its length, and for place x the request it belongs to and the place
+// of that request's first tile. Thread i counts requests i * per .. i * per + per - 1.
+template <typename A, int THREADS>
+struct Line {
+    static constexpr int WAVES = THREADS / 64;           // sh holds WAVES + 2 numbers
+    int64_t total, before;                   // of this thread's requests
+    int per;
+    __device__ __forceinline__ void measure(const A &a, int64_t *sh) {
+        per = (a.batch + THREADS - 1) / THREADS;
+        int64_t v = 0;
+        for (int i = threadIdx.x * per; i < min(a.batch, (int)(threadIdx.x + 1) * per); ++i) v += request_tiles(a, i);
+        before = block_scan<THREADS>(v * a.groups, sh, total);
+        total = uniform(total);
+    }
+    __device__ __forceinline__ void find(const A &a, int64_t x, int64_t *sh, int &req, int64_t &base) const {
+        int64_t at = before;
+        for (int i = threadIdx.x * per; i < min(a.batch, (int)(threadIdx.x + 1) * per); ++i) {
+            const int64_t n = (int64_t)request_tiles(a, i) * a.groups;
+            if (at <= x && x < at + n) {
+                sh[WAVES] = i;
+                sh[WAVES + 1] = at;
+            }
+            at += n;
+        }
+        __syncthreads();
+        req = uniform((int)sh[WAVES]);
+        base = uniform(sh[WAVES + 1]);
+    }
+};
+
+// Workgroup b's run of the line: [b * total / grid, (b + 1) * total / grid). Runs leave partials
+// 2b (of the run's first unit) and 2b + 1 (of its last, if that is another).
+__device__ __forceinline__ int64_t run_start(int64_t total, int grid, int b) { return total * b / grid; }
+// the workgroup whose run holds place x (no run is empty: grid <= total)
+__device__ __forceinline__ int run_of(int64_t total, int grid, int64_t x) { return (int)(((x + 1) * grid - 1) / total); }
+
+// k / page for 0 <= k < 2^30: (k * page_mul) >> (32 + page_shift), page_mul 0 for a page of 1.
+// 2^bits >= page > 2^(bits - 1): the reciprocal 2^(31 + bits) / page, rounded up, fits 32 bits, and
+// for k < 2^30 its rounding adds less than 2^-(1 + bits) < 1 / page to the quotient: exact
+inline void page_reciprocal(int page, uint32_t &mul, int &shift) {
+    int bits = 1;
+    while ((1 << bits) < page) ++bits;
+    mul = page == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + bits)) + page - 1) / page);
+    shift = bits - 1;
+}
+template <typename A>
+__device__ __forceinline__ int page_of(const A &a, int k) {
+    return a.page_mul ? (int)(__umulhi((uint32_t)k, a.page_mul) >> a.page_shift) : k;
+}
+
+}  // namespace latent
+}  // namespace skinny

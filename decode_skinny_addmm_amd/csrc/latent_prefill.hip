@@ -16,6 +16,7 @@
 // 8 heads 9.5 us. Beside its matrix instructions (27% of the cycles with the 6 prompts) a tile waits for
 // all its loads, and each matrix instruction for its fragment from LDS, which is not read ahead as in the wide form.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "latent.hpp"
@@ -55,6 +56,48 @@ struct PrefillArgs {
     float c;
     bool causal;
 };
+
+// Causal, and of the keys before a query's own it sees the last `window` (its own among them) and the
+// first `sinks`.
+struct WindowArgs : PrefillArgs {
+    int window, sinks;
+};
+// The key tiles that queries see between them, of which the first sees `fewest` keys without a window and the
+// last `most`, in the order in which they are taken: with a window those of the first keys and,
+// `skip` further on, those from the first query's window on.
+struct Tiles {
+    int count, head, skip;
+    __device__ __forceinline__ int at(int t) const { return t < head ? t : t + skip; }
+    // how many of them lie before tile x of the sequence
+    __device__ __forceinline__ int before(int x) const { return x <= head ? x : max(head, x - skip); }
+};
+__device__ __forceinline__ Tiles tiles_of(const PrefillArgs &, int, int most) { return {(most + KT - 1) / KT, INT_MAX, 0}; }
+__device__ __forceinline__ Tiles tiles_of(const WindowArgs &a, int fewest, int most) {
+    Tiles s{(most + KT - 1) / KT, INT_MAX, 0};
+    const int head = (min(a.sinks, most) + KT - 1) / KT, from = max(0, fewest - a.window) / KT;
+    if (from > head) {
+        s.head = head;
+        s.skip = from - head;
+        s.count -= s.skip;
+    }
+    return s;
+}
+// Whether a query that sees `limit` keys without a window sees key k (`left`: limit, window's begin and
+// first keys, all counted from the lane's first key of the tile).
+struct Left {
+    int limit, begin, sinks;
+    template <bool WINDOW>
+    __device__ __forceinline__ bool sees(int k) const {
+        return WINDOW ? k < limit && (k >= begin || k < sinks) : k < limit;
+    }
+};
+__device__ __forceinline__ Left left_of(const PrefillArgs &, int limit, int k0) { return {limit - k0, 0, 0}; }
+__device__ __forceinline__ Left left_of(const WindowArgs &a, int limit, int k0) {
+    return {limit - k0, limit - a.window - k0, a.sinks - k0};
+}
+// The first tile from which on a query of a workgroup that sees `most` keys sees its tiles to their begin.
+__device__ __forceinline__ int first_whole(const PrefillArgs &, int) { return 0; }
+__device__ __forceinline__ int first_whole(const WindowArgs &a, int most) { return (max(0, most - a.window) + KT - 1) / KT; }
 
 // One row's partial: 128 sums; maxima and totals follow all rows' sums.
 __host__ __device__ inline int64_t split_floats(int64_t nq, int64_t heads) { return nq * heads * (HD + 2); }
@@ -107,12 +150,14 @@ __device__ __forceinline__ int find_tile(const PrefillArgs &a, int at, int &tile
     return -1;
 }
 
-// One pass over key tiles [t0, t1). limit: keys that the lane's row sees; first: the fewest that
-// any row of the workgroup sees. safe: non-finite values in tiles that some row sees in part
+// One pass over key tiles [t0, t1) of `span`. limit: keys that the lane's row sees (without a window);
+// first, most: the fewest and the most that any row of the workgroup sees. safe: non-finite values in tiles that some row sees in part
 // reach only the rows that see them (see split_value).
-__device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, const u32x4_t (&qf)[KS], int head,
-                                          int64_t k0row, int lk, int t0, int t1, int limit, int first, bool safe,
-                                          f32x16_t (&o)[ND], float &m, float &l) {
+template <typename A>
+__device__ __forceinline__ void run_tiles(const A &a, uint8_t *lds, const u32x4_t (&qf)[KS], int head, int64_t k0row,
+                                          int lk, const Tiles &span, int t0, int t1, int limit, int first, int most,
+                                          bool safe, f32x16_t (&o)[ND], float &m, float &l) {
+    constexpr bool WINDOW = std::is_same_v<A, WindowArgs>;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row = T::row(lane), grp = T::grp(lane);
     lds_u8 *ring = (lds_u8 *)lds;
@@ -125,7 +170,7 @@ __device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, co
         for (int u = 0; u < 2; ++u) {
             const int rg = 2 * wave + u, r = 8 * rg + (lane >> 3);
             const int chunk = ((lane & 7) ^ swz(r)) * 8;
-            const int64_t key = k0row + min(t * KT + r, lk - 1);
+            const int64_t key = k0row + min(span.at(t) * KT + r, lk - 1);
             const uint16_t *kp = a.k + key * a.k_row + head * a.k_head + chunk;
             const uint16_t *rp = a.kr + key * a.kr_row + chunk;
             const uint16_t *vp = a.v + key * a.v_row + head * a.v_head + chunk;
@@ -177,12 +222,12 @@ __device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, co
         float p[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) p[i] = s[i / T::NS][i % T::NS];
-        const int k0 = t * KT;
-        const bool mixed = k0 + KT > first;
+        const int at = span.at(t), k0 = at * KT;
+        const bool mixed = k0 + KT > first || (WINDOW && at < first_whole(a, most));
+        const Left left = left_of(a, limit, k0 + T::place(0, grp));
         if (mixed) {
-            const int left = limit - k0 - T::place(0, grp);      // keys from the lane's first on
 #pragma unroll
-            for (int i = 0; i < NP; ++i) p[i] = place0(i) < left ? p[i] : -INFINITY;
+            for (int i = 0; i < NP; ++i) p[i] = left.sees<WINDOW>(place0(i)) ? p[i] : -INFINITY;
         }
         float top = p[0];
 #pragma unroll
@@ -230,8 +275,7 @@ __device__ __forceinline__ void run_tiles(const PrefillArgs &a, uint8_t *lds, co
             u32x4_t see[NP / 8];
 #pragma unroll
             for (int j = 0; j < NP; j += 2)
-                see[j / 8][j % 8 / 2] = seen_pair(place0(j) < limit - k0 - T::place(0, grp),
-                                                  place0(j + 1) < limit - k0 - T::place(0, grp));
+                see[j / 8][j % 8 / 2] = seen_pair(left.sees<WINDOW>(place0(j)), left.sees<WINDOW>(place0(j + 1)));
 #pragma unroll
             for (int x = 0; x < NP / 8; ++x)
 #pragma unroll
@@ -326,7 +370,8 @@ __device__ __forceinline__ bool not_finite(const f32x16_t (&o)[ND]) {
     return odd;
 }
 
-__global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs a) {
+template <typename A>
+__global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(A a) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE_BYTES];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int row = T::row(lane), grp = T::grp(lane);
@@ -348,15 +393,17 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(PrefillArgs 
     // keys that this row, the workgroup's first row and its last row see
     auto sees = [&](int x) { return a.causal ? max(0, min(lk, lk - lq + 1 + x)) : lk; };
     const int limit = sees(rc), first = sees(tile * BM), last = sees(min(tile * BM + BM, lq) - 1);
-    const int n = (last + KT - 1) / KT;
+    const Tiles span = tiles_of(a, first, last);
+    const int n = span.count;
     const int t0 = (int)((int64_t)n * split / a.splits), t1 = (int)((int64_t)n * (split + 1) / a.splits);
     f32x16_t o[ND];
     float m, l;
     bool safe = false;
     for (;;) {
-        run_tiles(a, lds, qf, head, k0, lk, t0, t1, limit, first, safe, o, m, l);
+        run_tiles(a, lds, qf, head, k0, lk, span, t0, t1, limit, first, last, safe, o, m, l);
         // a non-finite result where some rows see fewer keys than others: once more, key by key
-        if (safe || !any_wave<WAVES>(not_finite(o) && t1 * KT > first, lds)) break;
+        const bool some = std::is_same_v<A, WindowArgs> || t1 * KT > first;
+        if (safe || !any_wave<WAVES>(not_finite(o) && some, lds)) break;
         safe = true;
     }
     if (r < lq) put_row(a, split, (int64_t)q0 + r, head, grp, o, m, l);
@@ -379,7 +426,9 @@ constexpr int WIDE_LDS = K_RING * K_BYTES + V_RING * V_BYTES;
 constexpr int GROUP_LOADS = KSEG + VSEG;                 // a wave's, of a tile's keys and a tile's values
 static_assert(WIDE_WAVES * 8 == KT, "a wave stages 8 rows");
 
-__global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(PrefillArgs a) {
+template <typename A>
+__global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(A a) {
+    constexpr bool WINDOW = std::is_same_v<A, WindowArgs>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[WIDE_LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int row = T::row(lane), grp = T::grp(lane);
@@ -396,19 +445,22 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
     const int64_t qr = (int64_t)q0 + rc;
     const int limit = sees(rc);
     // key tiles: the workgroup's, and of them the wave's; whole: seen whole by every row of the wave
-    const int n = (sees(min(tile * WIDE_BM + WIDE_BM, lq) - 1) + KT - 1) / KT;
+    const int fewest = sees(tile * WIDE_BM), most = sees(min(tile * WIDE_BM + WIDE_BM, lq) - 1);
+    const Tiles span = tiles_of(a, fewest, most);
+    const int n = span.count;
     const int t0 = (int)((int64_t)n * split / a.splits), t1 = (int)((int64_t)n * (split + 1) / a.splits);
     const int cnt = t1 - t0;
-    const int last = r0 < lq ? (sees(min(r0 + T::ROWS, lq) - 1) + KT - 1) / KT : 0;
+    const int last = r0 < lq ? span.before((sees(min(r0 + T::ROWS, lq) - 1) + KT - 1) / KT) : 0;
     const int cw = max(0, min(last, t1) - t0), first = sees(min(r0, lq - 1));
-    const int whole = max(0, first / KT - t0);
+    const int whole = max(0, span.before(first / KT) - t0);
+    const int some = first_whole(a, r0 < lq ? sees(min(r0 + T::ROWS, lq) - 1) : 0);
 
     lds_u8 *kring = (lds_u8 *)lds, *vring = kring + K_RING * K_BYTES;
     const int lrow = 8 * wave + (lane >> 3);             // staging: this lane's row of a tile
     const int chunk = ((lane & 7) ^ swz(lrow)) * 8;
     const uint16_t *kbase = a.k + head * a.k_head + chunk, *rbase = a.kr + chunk, *vbase = a.v + head * a.v_head + chunk;
     // past the last tile it is loaded again, so that the counts stay even
-    auto key_of = [&](int i) __attribute__((always_inline)) { return (int64_t)k0 + min(min(t0 + i, t1 - 1) * KT + lrow, lk - 1); };
+    auto key_of = [&](int i) __attribute__((always_inline)) { return (int64_t)k0 + min(span.at(min(t0 + i, t1 - 1)) * KT + lrow, lk - 1); };
     auto load = [&](int i) __attribute__((always_inline)) {
         const int64_t key = key_of(i);
         const int kd = lds_address(kring + (i % K_RING) * K_BYTES + wave * (KSEG * 1024));
@@ -438,11 +490,11 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
     u32x4_t pf[NP / 8];
 
     auto softmax = [&](int i) __attribute__((always_inline)) {
-        if (i >= whole) {
-            const int left = limit - (t0 + i) * KT - T::place(0, grp);   // keys from the lane's first on
+        if (i >= whole || (WINDOW && span.at(t0 + i) < some)) {
+            const Left left = left_of(a, limit, span.at(t0 + i) * KT + T::place(0, grp));
 #pragma unroll
             for (int j = 0; j < NP; ++j)
-                s[j / T::NS][j % T::NS] = place0(j) < left ? s[j / T::NS][j % T::NS] : -INFINITY;
+                s[j / T::NS][j % T::NS] = left.sees<WINDOW>(place0(j)) ? s[j / T::NS][j % T::NS] : -INFINITY;
         }
         float top = s[0][0];
 #pragma unroll
@@ -536,12 +588,13 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
     };
     // the value product where a value that is not finite may reach only the rows that see it
     auto value_products_carefully = [&](int i) __attribute__((always_inline)) {
-        const int left = limit - (t0 + i) * KT - T::place(0, grp);
+        const Left left = left_of(a, limit, span.at(t0 + i) * KT + T::place(0, grp));
 #pragma unroll
         for (int x = 0; x < NP / 8; ++x) {
             u32x4_t see;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) see[j / 2] = seen_pair(place0(8 * x + j) < left, place0(8 * x + j + 1) < left);
+            for (int j = 0; j < 8; j += 2) 
+                see[j / 2] = seen_pair(left.sees<WINDOW>(place0(8 * x + j)), left.sees<WINDOW>(place0(8 * x + j + 1)));
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -619,7 +672,7 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(Prefi
     };
     pass(std::false_type());
     // a non-finite result where some rows see fewer keys than others: once more, with care
-    if (any_wave<WIDE_WAVES>(not_finite(o) && t1 * KT > sees(tile * WIDE_BM), lds)) pass(std::true_type());
+    if (any_wave<WIDE_WAVES>(not_finite(o) && (WINDOW || t1 * KT > fewest), lds)) pass(std::true_type());
     if (r < lq) put_row(a, split, qr, head, grp, o, m, l);
 }
 
@@ -656,30 +709,39 @@ struct Plan {
     int64_t tiles;                           // most query tiles that nq rows in batch sequences can need
     int splits;
 };
-Plan plan(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus) {
+// keys: those that a workgroup takes, on average.
+Plan plan(int64_t nq, int64_t keys, int64_t batch, int64_t heads, int cus) {
     Plan p;
-    p.wide = nq / batch >= 192 && nk / batch >= 1024;
+    p.wide = nq / batch >= 192 && keys >= 1024;
     const int bm = p.wide ? WIDE_BM : BM;
     p.tiles = std::min(nq, (nq + batch * (bm - 1)) / bm);
     // Splits of the keys: as many as fill the CUs (one wide workgroup each, or two narrow ones),
     // while each keeps 8 key tiles of the average sequence (1024 rows x 16024 keys x 8 heads: 8 splits
     // 89 us, none 392)
     const int64_t room = (p.wide ? 1 : 2) * (int64_t)cus / std::max<int64_t>(1, p.tiles * heads);
-    const int64_t most = std::max<int64_t>(1, nk / batch / (8 * KT));
+    const int64_t most = std::max<int64_t>(1, keys / (8 * KT));
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({room, most, 32}));
     return p;
 }
 
+// Keys that a workgroup takes, on average; with a window what its rows see between them.
+int64_t keys_taken(int64_t nk, int64_t batch, int64_t window, int64_t sinks) {
+    const int64_t keys = nk / batch;
+    return window ? std::min(keys, std::min(keys, window) + std::min(keys, sinks) + BM) : keys;
+}
+
 }  // namespace
 
-int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int cus) {
+int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int64_t window, int64_t sinks,
+                                       int cus) {
     if (nq == 0 || batch == 0 || heads == 0) return 0;
-    const int s = plan(nq, nk, batch, heads, cus).splits;
+    const int s = plan(nq, keys_taken(nk, batch, window, sinks), batch, heads, cus).splits;
     return s == 1 ? 0 : s * split_floats(nq, heads) * (int64_t)sizeof(float);
 }
 
-hipError_t launch_latent_prefill(const skinny_latent_prefill_args &p, int cus, hipStream_t stream) {
-    PrefillArgs a;
+hipError_t launch_latent_prefill(const skinny_latent_prefill_args &p, int64_t window, int64_t sinks, int cus,
+                                 hipStream_t stream) {
+    WindowArgs a;
     a.q = static_cast<const uint16_t *>(p.q);
     a.k = static_cast<const uint16_t *>(p.k);
     a.v = static_cast<const uint16_t *>(p.v);
@@ -702,20 +764,27 @@ hipError_t launch_latent_prefill(const skinny_latent_prefill_args &p, int cus, h
     a.nk = p.nk;
     a.batch = (int)p.batch;
     a.heads = (int)p.heads;
-    const Plan how = plan(p.nq, p.nk, p.batch, p.heads, cus);
+    const Plan how = plan(p.nq, keys_taken(p.nk, p.batch, window, sinks), p.batch, p.heads, cus);
     a.tiles = (int)how.tiles;
     a.average = (int)(p.nk / p.batch);
     a.splits = how.splits;
     a.c = p.scale * kLog2e;
     a.causal = p.causal != 0;
+    a.window = (int)std::min<int64_t>(window, INT_MAX / 2);
+    a.sinks = (int)std::min<int64_t>(sinks, INT_MAX / 2);
+    const PrefillArgs &whole = a;
     const dim3 grid((unsigned)(a.tiles * a.heads * a.splits));
-    if (how.wide)
-        hipLaunchKernelGGL(latent_prefill_wide_kernel, grid, dim3(WIDE_THREADS), 0, stream, a);
+    if (how.wide && window)
+        hipLaunchKernelGGL((latent_prefill_wide_kernel<WindowArgs>), grid, dim3(WIDE_THREADS), 0, stream, a);
+    else if (how.wide)
+        hipLaunchKernelGGL((latent_prefill_wide_kernel<PrefillArgs>), grid, dim3(WIDE_THREADS), 0, stream, whole);
+    else if (window)
+        hipLaunchKernelGGL((latent_prefill_kernel<WindowArgs>), grid, dim3(THREADS), 0, stream, a);
     else
-        hipLaunchKernelGGL(latent_prefill_kernel, grid, dim3(THREADS), 0, stream, a);
+        hipLaunchKernelGGL((latent_prefill_kernel<PrefillArgs>), grid, dim3(THREADS), 0, stream, whole);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.splits == 1) return err;
-    hipLaunchKernelGGL(latent_prefill_join_kernel, dim3((unsigned)((p.nq * a.heads + 7) / 8)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(latent_prefill_join_kernel, dim3((unsigned)((p.nq * a.heads + 7) / 8)), dim3(256), 0, stream, whole);
     return hipGetLastError();
 }
 

@@ -322,7 +322,10 @@ def _latent():
             raise RuntimeError("the _latent module is not built; run `python -m decode_skinny_addmm_amd.build` or "
                                "__graft_entry__.build()") from e
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                      for f in (L.skinny_latent_append_bf16, L.skinny_latent_decode_bf16, L.skinny_latent_prefill_bf16)))
+                      for f in (L.skinny_latent_append_bf16, L.skinny_latent_decode_bf16, L.skinny_latent_prefill_bf16,
+                                L.skinny_latent_masked_decode_bf16, L.skinny_latent_tree_mask,
+                                L.skinny_latent_window_prefill_bf16, L.skinny_latent_key_weights_bf16,
+                                L.skinny_latent_select, L.skinny_latent_keep_bf16)))
         _latent_module = module
     return _latent_module
 
@@ -418,20 +421,8 @@ def latent_prefill_workspace(nq: int, nk: int, batch: int, heads: int, device="c
                       heads)
 
 
-def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim: int = ROPE, out=None, lse=None,
-                  workspace=None, stream=None):
-    """Absorbed latent attention of each request's newest tokens over a paged latent cache
-    (skinny_latent_decode_bf16).
-
-    q bf16 [batch * tokens, heads, 576]: queries that already carry the key projection, and their
-    rotated parts. cache bf16 [pages, page_size, 576]; table int32 [batch, max_pages]: each
-    request's pages; lens int32 [batch]: its cached tokens, the new ones among them. Token j of
-    request i sees keys below lens[i] - tokens + j + 1; out bf16 [batch * tokens, heads, 512] is
-    the softmax-weighted sum of the keys' latents, lse float32 [batch * tokens, heads] the log of
-    the softmax's sum (zeros and -inf where a row sees no key). Lengths beyond the table and page
-    ids outside the cache are clamped. q, cache and out may have strides (multiples of 8,
-    contiguous last dimension). workspace: latent_decode_workspace(batch, tokens, heads), kept by
-    the caller between calls; allocated for this call where None. Returns (out, lse)."""
+def _decode_outputs(q, tokens, out, lse, workspace, stream):
+    """The GPU of a decode call, and its out, lse and workspace, made for the call where None."""
     gpu = _gpu_of("q", q)
     if out is None or lse is None or workspace is None:
         dev = q.device
@@ -447,22 +438,31 @@ def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim
         if workspace is None:
             workspace = _call_workspace(lib().skinny_latent_decode_workspace, "skinny_latent_decode_workspace", dev,
                                         stream, rows // tokens, tokens, heads)
+    return gpu, out, lse, workspace
+
+
+def latent_decode(q, cache, table, lens, scale: float, tokens: int = 1, rope_dim: int = ROPE, out=None, lse=None,
+                  workspace=None, stream=None):
+    """Absorbed latent attention of each request's newest tokens over a paged latent cache
+    (skinny_latent_decode_bf16).
+
+    q bf16 [batch * tokens, heads, 576]: queries that already carry the key projection, and their
+    rotated parts. cache bf16 [pages, page_size, 576]; table int32 [batch, max_pages]: each
+    request's pages; lens int32 [batch]: its cached tokens, the new ones among them. Token j of
+    request i sees keys below lens[i] - tokens + j + 1; out bf16 [batch * tokens, heads, 512] is
+    the softmax-weighted sum of the keys' latents, lse float32 [batch * tokens, heads] the log of
+    the softmax's sum (zeros and -inf where a row sees no key). Lengths beyond the table and page
+    ids outside the cache are clamped. q, cache and out may have strides (multiples of 8,
+    contiguous last dimension). workspace: latent_decode_workspace(batch, tokens, heads), kept by
+    the caller between calls; allocated for this call where None. Returns (out, lse)."""
+    gpu, out, lse, workspace = _decode_outputs(q, tokens, out, lse, workspace, stream)
     _call(_latent().decode, "skinny_latent_decode_bf16", gpu, stream, q, cache, table, lens, scale, tokens, rope_dim, out,
           lse, workspace)
     return out, lse
 
 
-def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True, out=None, lse=None, workspace=None,
-                   stream=None):
-    """Expanded latent attention of prompts (skinny_latent_prefill_bf16).
-
-    q bf16 [nq, heads, 192] (a head's 128 numbers, then its 64 rotated ones), k and v bf16 [nk,
-    heads, 128], k_rot bf16 [nk, 64] shared by all heads; cu_q, cu_k int32 [batch + 1]: where each
-    sequence's queries and keys start, rising from 0 to nq and nk. causal: a sequence's last query
-    sees its last key, the one before it one key fewer, and so on. out bf16 [nq, heads, 128], lse
-    float32 [nq, heads] (zeros and -inf where a row sees no key). q, k, v, k_rot and out may have
-    strides (multiples of 8, contiguous last dimension). workspace: latent_prefill_workspace(nq,
-    nk, batch, heads), allocated for this call where None. Returns (out, lse)."""
+def _prefill_outputs(q, k, cu_q, out, lse, workspace, stream, fn, what, *sizes):
+    """The GPU of a prefill call, and its out, lse and workspace, made for the call where None."""
     gpu = _gpu_of("q", q)
     if out is None or lse is None or workspace is None:
         dev = q.device
@@ -476,11 +476,156 @@ def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True
         if lse is None:
             lse = _new((nq, heads), torch.float32, dev, stream)
         if workspace is None:
-            workspace = _call_workspace(lib().skinny_latent_prefill_workspace, "skinny_latent_prefill_workspace", dev,
-                                        stream, nq, k.shape[0], cu_q.shape[0] - 1, heads)
+            workspace = _call_workspace(fn, what, dev, stream, nq, k.shape[0], cu_q.shape[0] - 1, heads, *sizes)
+    return gpu, out, lse, workspace
+
+
+def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True, out=None, lse=None, workspace=None,
+                   stream=None):
+    """Expanded latent attention of prompts (skinny_latent_prefill_bf16).
+
+    q bf16 [nq, heads, 192] (a head's 128 numbers, then its 64 rotated ones), k and v bf16 [nk,
+    heads, 128], k_rot bf16 [nk, 64] shared by all heads; cu_q, cu_k int32 [batch + 1]: where each
+    sequence's queries and keys start, rising from 0 to nq and nk. causal: a sequence's last query
+    sees its last key, the one before it one key fewer, and so on. out bf16 [nq, heads, 128], lse
+    float32 [nq, heads] (zeros and -inf where a row sees no key). q, k, v, k_rot and out may have
+    strides (multiples of 8, contiguous last dimension). workspace: latent_prefill_workspace(nq,
+    nk, batch, heads), allocated for this call where None. Returns (out, lse)."""
+    gpu, out, lse, workspace = _prefill_outputs(q, k, cu_q, out, lse, workspace, stream,
+                                                lib().skinny_latent_prefill_workspace, "skinny_latent_prefill_workspace")
     _call(_latent().prefill, "skinny_latent_prefill_bf16", gpu, stream, q, k, v, k_rot, cu_q, cu_k, scale, causal, out, lse,
           workspace)
     return out, lse
+
+
+def latent_tree_mask(parents, mask=None, depth=None, stream=None):
+    """Rows of trees of drafted tokens (skinny_latent_tree_mask), for latent_tree_decode.
+
+    parents int32 [batch, tokens], at most 512 tokens: each token's parent among the earlier ones of its
+    request; any other number (-1) where it follows the context. Returns mask int32 [batch, tokens,
+    ceil(tokens / 32)], where bit d % 32 of word d / 32 says that a token sees token d (itself and those above
+    it), and depth int32 [batch, tokens]: how many stand above it, so that it has position
+    lens - tokens + depth. One call serves all layers of a step."""
+    gpu = _gpu_of("parents", parents)
+    if parents.dim() != 2:
+        raise ValueError("parents must be a tensor [batch, tokens]")
+    batch, tokens = parents.shape
+    if mask is None:
+        mask = _new((batch, tokens, (tokens + 31) // 32), torch.int32, parents.device, stream)
+    if depth is None:
+        depth = _new((batch, tokens), torch.int32, parents.device, stream)
+    _call(_latent().tree_mask, "skinny_latent_tree_mask", gpu, stream, parents, mask, depth)
+    return mask, depth
+
+
+def latent_tree_decode(q, cache, table, lens, mask, scale: float, window: int = 0, sinks: int = 0, depth=None,
+                       rope_dim: int = ROPE, out=None, lse=None, workspace=None, stream=None):
+    """latent_decode of requests whose newest tokens are a tree (skinny_latent_masked_decode_bf16).
+
+    mask int32 [batch, tokens, ceil(tokens / 32)], as from latent_tree_mask (its first dimension may have stride
+    0: one tree for all): token j sees the context, which is the first lens[i] - tokens keys, and those of
+    the new tokens whose bit is set. The number of new tokens, 512 at most, is the mask's. window (at least
+    `tokens`; 0: none): of the context only the keys among the last `window` up to a token's own position, which
+    depth (int32 [batch, tokens], as from latent_tree_mask) tells, and the first `sinks`. The rest as in
+    latent_decode; workspace: latent_decode_workspace(batch, tokens, heads). Returns (out, lse)."""
+    if not isinstance(mask, torch.Tensor) or mask.dim() != 3 or mask.shape[1] < 1:
+        raise ValueError("mask must be a tensor [batch, tokens, ceil(tokens / 32)]")
+    tokens = mask.shape[1]
+    gpu, out, lse, workspace = _decode_outputs(q, tokens, out, lse, workspace, stream)
+    _call(_latent().tree_decode, "skinny_latent_masked_decode_bf16", gpu, stream, q, cache, table, lens, scale, tokens,
+          rope_dim, out, lse, workspace, mask, depth, window, sinks)
+    return out, lse
+
+
+def latent_window_decode(q, cache, table, lens, scale: float, window: int, sinks: int = 0, tokens: int = 1,
+                         rope_dim: int = ROPE, out=None, lse=None, workspace=None, stream=None):
+    """latent_decode with a sliding window (skinny_latent_masked_decode_bf16): a token at position p
+    (its own key among those it sees) sees the last `window` keys, k > p - window, and the first `sinks`,
+    k < sinks. Keys that no row of a request sees are not read. The rest as in latent_decode. Returns
+    (out, lse)."""
+    gpu, out, lse, workspace = _decode_outputs(q, tokens, out, lse, workspace, stream)
+    _call(_latent().window_decode, "skinny_latent_masked_decode_bf16", gpu, stream, q, cache, table, lens, scale, tokens,
+          rope_dim, out, lse, workspace, window, sinks)
+    return out, lse
+
+
+def latent_window_prefill_workspace(nq: int, nk: int, batch: int, heads: int, window: int, sinks: int = 0,
+                                    device="cuda") -> torch.Tensor:
+    """Device memory for the partial sums of a latent_window_prefill call of these sizes (may be empty)."""
+    return _workspace(lib().skinny_latent_window_prefill_workspace, "skinny_latent_window_prefill_workspace", device, nq,
+                      nk, batch, heads, window, sinks)
+
+
+def latent_window_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, window: int, sinks: int = 0, out=None, lse=None,
+                          workspace=None, stream=None):
+    """Causal latent_prefill with a sliding window (skinny_latent_window_prefill_bf16): a query at position p of
+    its sequence sees keys k <= p with k > p - window or k < sinks. The rest as in latent_prefill;
+    workspace: latent_window_prefill_workspace(nq, nk, batch, heads, window, sinks). Returns (out, lse)."""
+    for name, value, least in (("window", window, 1), ("sinks", sinks, 0)):
+        if not hasattr(value, "__index__") or value < least:
+            raise ValueError("%s must be a whole number of at least %d, got %s" % (name, least, value))
+    gpu, out, lse, workspace = _prefill_outputs(q, k, cu_q, out, lse, workspace, stream,
+                                                lib().skinny_latent_window_prefill_workspace,
+                                                "skinny_latent_window_prefill_workspace", window, sinks)
+    _call(_latent().window_prefill, "skinny_latent_window_prefill_bf16", gpu, stream, q, k, v, k_rot, cu_q, cu_k, scale,
+          True, out, lse, workspace, window, sinks)
+    return out, lse
+
+
+def latent_key_weights(q, cache, table, lens, lse, weights, scale: float, tokens: int = 1, rope_dim: int = ROPE,
+                       stream=None):
+    """Adds to weights what latent_decode's softmax gave each key (skinny_latent_key_weights_bf16), in place.
+
+    q, cache, table, lens, scale, tokens as in latent_decode, lse float32 [batch * tokens, heads] as it returned:
+    weights float32 [batch, columns] (rows may lie apart) gets at [i, k] the sum over request i's rows
+    that see key k of exp(scale * q . key - lse). Keys without a column are left out. With `tokens` the last ones
+    of a prompt it tells which of the prompt's keys they look at. Returns weights."""
+    gpu = _gpu_of("q", q)
+    _call(_latent().key_weights, "skinny_latent_key_weights_bf16", gpu, stream, q, cache, table, lens, lse, weights, scale,
+          tokens, rope_dim)
+    return weights
+
+
+def latent_select(weights, lens, budget: int, sinks: int = 0, recent: int = 0, kept=None, counts=None, stream=None):
+    """Which keys of each request stay in the cache (skinny_latent_select).
+
+    weights float32 [batch, columns], lens int32 [batch]. Of more than `budget` keys the first `sinks`, the last
+    `recent` and the largest weights between them stay (of equal ones the first; a NaN is larger than any
+    number); of fewer, all. Returns kept int32 [batch, budget], rising, -1 behind the last, and counts int32
+    [batch], for latent_keep."""
+    gpu = _gpu_of("weights", weights)
+    if weights.dim() != 2:
+        raise ValueError("weights must be a tensor [batch, columns]")
+    if budget < 0:
+        raise ValueError("budget must not be negative, got %d" % budget)
+    if kept is None:
+        kept = _new((weights.shape[0], budget), torch.int32, weights.device, stream)
+    if counts is None:
+        counts = _new((weights.shape[0],), torch.int32, weights.device, stream)
+    _call(_latent().select, "skinny_latent_select", gpu, stream, weights, lens, budget, sinks, recent, kept, counts)
+    return kept, counts
+
+
+def latent_keep(cache, table, lens, kept, counts, tokens: int = 0, weights=None, new_lens=None, new_weights=None,
+                stream=None):
+    """Moves the rows that stay in a paged latent cache together, in place (skinny_latent_keep_bf16).
+
+    kept int32 [batch, most], rising, of which counts int32 [batch] count. With tokens 0 they are numbers of
+    request i's lens[i] rows, and go to places 0, 1, ... (after latent_select). With tokens > 0 they count
+    from the first of its newest `tokens` rows, all earlier rows stay, and they go to the places
+    behind those: the accepted path of a tree. A number smaller than its place in the list, or of no row, leaves its new
+    place's row as it is; rows behind the last kept one keep their numbers. The pages must be the request's own.
+    weights float32 [batch, columns]: each key's, which go along into new_weights (0 behind the last). Returns
+    (new_lens int32 [batch], new_weights or None); neither may be lens or weights itself."""
+    gpu = _gpu_of("cache", cache)
+    if new_lens is None:
+        new_lens = _new(tuple(lens.shape) if isinstance(lens, torch.Tensor) else 0, torch.int32, cache.device, stream)
+    if weights is not None and new_weights is None:
+        new_weights = _new(tuple(weights.shape) if isinstance(weights, torch.Tensor) else 0, torch.float32, cache.device,
+                           stream)
+    _call(_latent().keep, "skinny_latent_keep_bf16", gpu, stream, cache, table, lens, kept, counts, tokens, new_lens, weights,
+          new_weights)
+    return new_lens, new_weights
 
 
 def select_config(M: int, N: int = 7168, K: int = 3584) -> dict:

@@ -408,6 +408,111 @@ SKINNY_API skinny_status skinny_latent_prefill_bf16(const skinny_latent_prefill_
 SKINNY_API skinny_status skinny_latent_prefill_workspace(int64_t nq, int64_t nk, int64_t batch, int64_t heads,
                                                          int64_t *bytes);
 
+/*
+ * What of the cache a new token sees. Token j of a request with n cached rows, `tokens` of them new,
+ * whose first new one is base = n - tokens:
+ *   tree NULL: the tokens are a chain, and token j sees keys k <= base + j, its own among them; with
+ *       window > 0 only those with k > base + j - window or k < sinks.
+ *   tree: token j sees the context, keys k < base, and new token d where bit d % 32 of word d / 32 of its
+ *       row of `tree` is set (skinny_latent_tree_mask makes the rows of a tree given by its
+ *       parents: a node and those above it). With window > 0, of the context only keys
+ *       k > base + depth[j] - window or k < sinks: a node at depth d (from 0) stands at position base + d.
+ */
+typedef struct skinny_latent_mask {
+    const int32_t *tree;            /* [batch, tokens, (tokens + 31) / 32] contiguous in a request, or NULL */
+    const int32_t *depth;           /* [batch, tokens], 0 .. tokens - 1 (clamped); used with a tree and a window */
+    int64_t tree_stride, depth_stride;   /* between requests; 0: all share one tree */
+    int64_t window, sinks;          /* window 0: the whole context */
+} skinny_latent_mask;
+
+/*
+ * Decode under a mask: skinny_latent_decode_bf16 (its sizes, workspace, refusals, and what it says of rows that
+ * see no key and of keys that a row does not see) with each token's keys as `mask` says. Key
+ * tiles outside of all rows' windows are not read. SKINNY_EINVAL: a negative window, stride or number of sinks,
+ * a window under `tokens` or without depth beside a tree; SKINNY_ENOTSUP: trees of more than 512 tokens.
+ */
+SKINNY_API skinny_status skinny_latent_masked_decode_bf16(const skinny_latent_decode_args *args,
+                                                          const skinny_latent_mask *mask, void *stream);
+
+/* The rows of trees given by their parents: parents [batch, tokens], each an earlier token of the same request
+ * (any other number: the token follows the context); mask [batch, tokens, (tokens + 31) / 32] gets each token's
+ * own bit and those of the tokens above it, depth [batch, tokens] their number. All contiguous. */
+SKINNY_API skinny_status skinny_latent_tree_mask(const int32_t *parents, int32_t *mask, int32_t *depth, int64_t batch,
+                                                 int64_t tokens, void *stream);
+
+/*
+ * Prefill with a window: skinny_latent_prefill_bf16 (causal must be set), where query x, which stands at
+ * position p = lk - lq + x of its sequence, sees keys k <= p with k > p - window or k < sinks. window at
+ * least 1, sinks not negative. Its workspace: skinny_latent_window_prefill_workspace() bytes.
+ */
+SKINNY_API skinny_status skinny_latent_window_prefill_bf16(const skinny_latent_prefill_args *args, int64_t window,
+                                                           int64_t sinks, void *stream);
+SKINNY_API skinny_status skinny_latent_window_prefill_workspace(int64_t nq, int64_t nk, int64_t batch, int64_t heads,
+                                                                int64_t window, int64_t sinks, int64_t *bytes);
+
+/*
+ * Key weights: weights[i, k] += sum over the rows (token j, head h) of request i that see key k
+ * (k <= lens[i] - tokens + j) of exp(scale * q . cache_k - lse[row]), for the keys k < lens[i] that have a column:
+ * what a decode call with the same arguments gave each key, added up. Keys and requests as in decode. The order of
+ * the sums is fixed. Other places of weights are left as they are. Refusals as in decode.
+ */
+typedef struct skinny_latent_key_weights_args {
+    const void *q;                  /* [batch * tokens, heads, 576] */
+    const void *cache;              /* [pages, page, 576] */
+    const int32_t *table;           /* [batch, max_pages], rows table_stride apart */
+    const int32_t *lens;            /* [batch] */
+    const float *lse;               /* [batch * tokens, heads] */
+    float *weights;                 /* [batch, columns], rows weights_stride apart */
+    int64_t q_row_stride, q_head_stride, cache_page_stride, cache_row_stride, table_stride, weights_stride;
+    int64_t batch, tokens, heads, pages, page, max_pages, columns, latent, rope;
+    float scale;
+} skinny_latent_key_weights_args;
+
+SKINNY_API skinny_status skinny_latent_key_weights_bf16(const skinny_latent_key_weights_args *args, void *stream);
+
+/*
+ * Select: which `budget` of request i's n = lens[i] keys stay: the first `sinks`, the last `recent`, and of those
+ * between the ones with the largest weights[i, k] (of equal ones the lowest k; a NaN counts as larger than
+ * any number, -0 as 0); all of them where n <= budget. kept[i] gets them in rising order, -1 behind them, counts[i]
+ * their number. Lengths are clamped to 0 .. columns. SKINNY_EINVAL: sinks + recent > budget.
+ * SKINNY_ENOTSUP: budget, columns or batch above 2^30, 2^30, 2^20.
+ */
+typedef struct skinny_latent_select_args {
+    const float *weights;           /* [batch, columns], rows weights_stride apart */
+    const int32_t *lens;            /* [batch] */
+    int32_t *kept;                  /* [batch, budget] contiguous */
+    int32_t *counts;                /* [batch] */
+    int64_t weights_stride;
+    int64_t batch, columns, budget, sinks, recent;
+} skinny_latent_select_args;
+
+SKINNY_API skinny_status skinny_latent_select(const skinny_latent_select_args *args, void *stream);
+
+/*
+ * Keep: of request i's n = lens[i] rows of the cache only some stay, moved together in place. tokens 0: rows
+ * kept[i, 0 .. counts[i] - 1] of all, to places 0, 1, ... tokens > 0: of its newest `tokens` rows (all earlier ones
+ * stay where they are) those numbers, counted from the first of them, to the places from there on, as after
+ * a verified tree. new_lens[i] is the number of rows left. The numbers must rise; one that is smaller than its place
+ * in the list, or is not a row of the request, leaves the row of its new place as it is. counts are clamped to
+ * 0 .. min(most, rows there are). weights and new_weights (NULL both, or neither): new_weights[i, j] = the weight
+ * of the key that row j holds now, 0 behind the last. The pages that rows move in must be the request's own.
+ * Rows behind the last one kept are left as they are. Lengths and page ids are clamped as in decode.
+ */
+typedef struct skinny_latent_keep_args {
+    void *cache;                    /* [pages, page, 576] */
+    const int32_t *table;           /* [batch, max_pages], rows table_stride apart */
+    const int32_t *lens;            /* [batch] */
+    const int32_t *kept;            /* [batch, most], rows kept_stride apart */
+    const int32_t *counts;          /* [batch] */
+    int32_t *new_lens;              /* [batch], not lens */
+    const float *weights;           /* [batch, columns], rows weights_stride apart, or NULL */
+    float *new_weights;             /* [batch, columns], rows new_weights_stride apart, or NULL */
+    int64_t cache_page_stride, cache_row_stride, table_stride, kept_stride, weights_stride, new_weights_stride;
+    int64_t batch, tokens, most, pages, page, max_pages, columns, latent, rope;
+} skinny_latent_keep_args;
+
+SKINNY_API skinny_status skinny_latent_keep_bf16(const skinny_latent_keep_args *args, void *stream);
+
 /* Number of configurations built into the library, and the i-th of them (0-based). */
 SKINNY_API int32_t skinny_num_configs(void);
 SKINNY_API skinny_status skinny_get_config(int32_t index, skinny_config *out);
