@@ -142,6 +142,17 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// v's sum over the lanes up to this one: within rows of 16 lanes, then over the rows.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);      // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);      // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);      // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);      // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);      // row_bcast:15 to rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);      // row_bcast:31 to rows 2 and 3
+    return v;
+}
+
 // Hold accumulators where they belong at this point: output sums in accumulation registers (a
 // branch that rescales them would otherwise move all of them to ordinary ones and back in every
 // iteration), scores in ordinary ones.

@@ -57,7 +57,7 @@ struct DecodeArgs {
     int2 *cuts;                              // a unit (request and row group): its first partial, its last workgroup
     int batch, tokens, heads, pages, page, max_pages;
     int rows, groups, grid;                  // rows a request, row groups a request, workgroups
-    uint32_t page_mul;                       // see page_of
+    uint32_t page_mul;                       // see quotient
     int page_shift;
     float c;                                 // scale * log2(e)
 };
@@ -844,7 +844,7 @@ static DecodeArgs decode_args(const skinny_latent_decode_args &p, int cus) {
     a.page = (int)p.page;
     a.max_pages = (int)p.max_pages;
     a.rows = a.tokens * a.heads;
-    page_reciprocal(a.page, a.page_mul, a.page_shift);
+    reciprocal(a.page, a.page_mul, a.page_shift);
     const int mb = block_rows(a.rows);
     a.groups = (a.rows + mb - 1) / mb;
     a.c = p.scale * kLog2e;

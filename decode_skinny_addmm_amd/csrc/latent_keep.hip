@@ -58,15 +58,18 @@ __global__ __launch_bounds__(MOST_TOKENS) void latent_tree_mask_kernel(const int
 }
 
 // ---- select -------------------------------------------------------------------------------
-// One workgroup a request. The weights' bits, turned into whole numbers of the same order, are searched from the
-// top for the smallest one that stays: three rounds of counts by 11, 11 and 10 bits. Then each wave
-// takes a piece of the keys, counts those above that number and equal to it, and writes its own behind the
-// waves' before it, so that the list rises and of equal ones the first stay. The weights (4 bytes a key) are
-// read once where they fit LDS, and from L2 five times where not. Chains of dependent steps
-// bound it.
+// One workgroup a request. The weights' bits are turned into whole numbers of the same order and counted by
+// their upper 13 bits, which names the bin of the smallest one that stays: all above it stay, none below. Of its
+// numbers, a few dozen of thousands where weights are spread like sums of softmax weights, each is ranked
+// against each, equal ones by their places; the last one to stay is the border. Where they are too many, two more
+// rounds of counts, by 10 and 9 bits, find it. Then each wave, whose keys are a piece of the
+// request's, writes its own behind the waves' before it: the list rises. Up to 65536 keys are held in
+// registers between the passes; more are read again each time. Chains of dependent steps bound it.
 constexpr int SELECT_THREADS = 1024, SELECT_WAVES = SELECT_THREADS / 64;
-constexpr int BINS = 2048, PER_BIN = BINS / SELECT_THREADS;
-constexpr int CACHED = 36864;                // keys in LDS, 144 KB
+constexpr int ROUND_BITS[3] = {13, 10, 9};
+constexpr int BINS = 1 << ROUND_BITS[0], PER_BIN = BINS / SELECT_THREADS;
+constexpr int RANKED = 256;                  // most numbers that are ranked one by one
+constexpr int HELD = 64, BATCH = 8;          // keys a lane holds; loads that go out together
 
 struct SelectArgs {
     const float *weights;
@@ -84,11 +87,63 @@ __device__ __forceinline__ uint32_t order_of(float w) {
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
+// A wave's keys: w[0 .. count), 64 at a time. each(f) calls f(i, number) for whole waves, in rising
+// order, with key i + lane's number, or 0, which is no weight's, where there is none.
+struct HeldKeys {
+    uint32_t x[HELD];
+    int count;
+    __device__ __forceinline__ HeldKeys(const float *w, int n) : count(n) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int u = 0; u < HELD; u += BATCH)
+            if (u * 64 < count) {
+#pragma unroll
+                for (int b = u; b < u + BATCH; ++b) x[b] = __float_as_uint(w[min(b * 64 + lane, count - 1)]);
+            }
+#pragma unroll
+        for (int u = 0; u < HELD; u += BATCH)
+            if (u * 64 < count) {
+#pragma unroll
+                for (int b = u; b < u + BATCH; ++b) x[b] = b * 64 + lane < count ? order_of(__uint_as_float(x[b])) : 0u;
+            }
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+        for (int u = 0; u < HELD; u += BATCH)
+            if (u * 64 < count) {
+#pragma unroll
+                for (int b = u; b < u + BATCH; ++b) {
+                    uint32_t y = x[b];
+                    asm volatile("" : "+v"(y));          // what a pass makes of it is not kept for the next
+                    f(b * 64, y);
+                }
+            }
+    }
+};
+struct ReadKeys {
+    const float *w;
+    int count;
+    __device__ __forceinline__ ReadKeys(const float *p, int n) : w(p), count(n) {}
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+        const int lane = threadIdx.x & 63;
+        for (int u = 0; u < count; u += 64 * BATCH) {
+            float v[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) v[b] = w[min(u + b * 64 + lane, count - 1)];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) f(u + b * 64, u + b * 64 + lane < count ? order_of(v[b]) : 0u);
+        }
+    }
+};
+
+template <typename Keys>
 __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArgs a) {
-    __shared__ uint32_t cache[CACHED];
-    __shared__ int bins[BINS];
-    __shared__ int sh[2 * SELECT_WAVES], found[2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, req = blockIdx.x;
+    __shared__ __attribute__((aligned(16))) int bins[BINS];
+    __shared__ int sh[SELECT_WAVES], waves_kept[SELECT_WAVES], found[3], ranked;
+    __shared__ uint2 near_border[RANKED];                // number, place
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), req = blockIdx.x;
     const int n = min(max(a.lens[req], 0), a.columns);
     int32_t *kept = a.kept + (int64_t)req * a.budget;
     const int count = min(n, a.budget);
@@ -98,111 +153,147 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
         for (int i = tid; i < n; i += SELECT_THREADS) kept[i] = i;
         return;
     }
-    for (int i = tid; i < a.sinks; i += SELECT_THREADS) kept[i] = i;
-    for (int i = tid; i < a.recent; i += SELECT_THREADS) kept[a.budget - a.recent + i] = n - a.recent + i;
     // of m keys between, want stay: 0 <= want < m
     const int m = n - a.recent - a.sinks, want = a.budget - a.recent - a.sinks;
+    const int piece = (m + SELECT_THREADS - 1) / SELECT_THREADS * 64, i0 = min(m, wave * piece);
+    const Keys keys(a.weights + req * a.w_row + a.sinks + i0, min(m, i0 + piece) - i0);
+    auto clear = [&]() {
+        for (int i = tid; i < BINS / 4; i += SELECT_THREADS) reinterpret_cast<int4 *>(bins)[i] = make_int4(0, 0, 0, 0);
+    };
+    clear();
+    if (tid == 0) ranked = 0;
+    if (tid < SELECT_WAVES) waves_kept[tid] = 0;
+    for (int i = tid; i < a.sinks; i += SELECT_THREADS) kept[i] = i;
+    for (int i = tid; i < a.recent; i += SELECT_THREADS) kept[a.budget - a.recent + i] = n - a.recent + i;
     if (want == 0) return;
-    const float *w = a.weights + req * a.w_row + a.sinks;
-    const bool cached = m <= CACHED;
-    if (cached) {
-        constexpr int U = 8;
-        for (int i0 = tid; i0 < m; i0 += U * SELECT_THREADS) {
-            float x[U];
+    // what the waves before this one counted
+    auto before = [&](const int (&of)[SELECT_WAVES]) {
+        int s = 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) x[u] = i0 + u * SELECT_THREADS < m ? w[i0 + u * SELECT_THREADS] : 0.0f;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * SELECT_THREADS < m) cache[i0 + u * SELECT_THREADS] = order_of(x[u]);
-        }
-    }
-    auto number = [&](int i) { return cached ? cache[i] : order_of(w[i]); };
+        for (int v = 0; v < SELECT_WAVES; ++v) s += v < wave ? of[v] : 0;
+        return s;
+    };
+    __syncthreads();
 
     uint32_t border = 0, known = 0;                      // the border's upper bits, which bits those are
-    int still = want;                                    // to be found among those with these upper bits
-    for (int round = 0; round < 3; ++round) {
-        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, mine = PER_BIN * (SELECT_THREADS - 1 - tid);
-        const uint32_t low = round == 2 ? BINS / 2 - 1 : BINS - 1;
-        for (int i = tid; i < BINS; i += SELECT_THREADS) bins[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < m; i += SELECT_THREADS) {
-            const uint32_t x = number(i);
-            if ((x & known) == border) atomicAdd(&bins[x >> shift & low], 1);
-        }
+    int still = want, same = 0;                          // to be found among the numbers with these bits; those
+    // One more round of counts: of the numbers with the known bits, by the next ones.
+    auto round = [&](int shift, int bits, bool first) __attribute__((always_inline)) {
+        keys.each([&](int, uint32_t x) {
+            if (first ? x != 0 : x - border <= ~known) atomicAdd(&bins[x >> shift & ((1u << bits) - 1)], 1);
+        });
         __syncthreads();
         // numbers in the bins above this thread's (threads count down from the topmost)
-        int own = 0;
+        int own[PER_BIN], sum = 0;
 #pragma unroll
-        for (int b = 0; b < PER_BIN; ++b) own += bins[mine + b];
-        int sum = own;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        if (lane == 63) sh[wave] = sum;
+        for (int b = 0; b < PER_BIN; ++b) sum += own[b] = bins[PER_BIN * (SELECT_THREADS - 1 - tid) + b];
+        int above = wave_scan(sum);
+        if (lane == 63) sh[wave] = above;
         __syncthreads();
-        int above = sum - own;
-        for (int v = 0; v < wave; ++v) above += sh[v];
+        above += before(sh) - sum;
 #pragma unroll
         for (int b = PER_BIN - 1; b >= 0; --b) {
-            const int here = bins[mine + b];
-            if (above < still && still <= above + here) {
-                found[0] = mine + b;
+            if (above < still && still <= above + own[b]) {
+                found[0] = PER_BIN * (SELECT_THREADS - 1 - tid) + b;
                 found[1] = still - above;
+                found[2] = own[b];
             }
-            above += here;
+            above += own[b];
         }
         __syncthreads();
         border |= (uint32_t)found[0] << shift;
-        known |= low << shift;
+        known |= ((1u << bits) - 1) << shift;
         still = found[1];
-    }
+        same = found[2];
+    };
+    round(32 - ROUND_BITS[0], ROUND_BITS[0], true);
 
-    // above the border all, of those equal to it the first `still`
-    const int piece = (m + SELECT_THREADS - 1) / SELECT_THREADS * 64, i0 = min(m, wave * piece), i1 = min(m, i0 + piece);
-    int more = 0, equal = 0;
-    for (int i = i0 + lane; i < i1; i += 64) {
-        const uint32_t x = number(i);
-        more += x > border;
-        equal += x == border;
-    }
+    // The border: numbers above it stay, and of those equal to it the ones up to place `last`.
+    int last = 0, mine = 0;                              // mine: the wave's that stay
+    if (same <= RANKED) {
+        keys.each([&](int i, uint32_t x) {
+            const uint32_t over = x - border;            // numbers with these bits: 0 .. ~known
+            mine += x > border && over > ~known;
+            const uint64_t near = __ballot(over <= ~known);
+            if (near) {                                  // the same in all lanes
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&ranked, __popcll(near));
+                at = uniform(at) + __popcll(near & ((1ull << lane) - 1));
+                if (near >> lane & 1) near_border[at] = make_uint2(x, i0 + i + lane);
+            }
+        });
+        mine = wave_scan(mine);                          // in lane 63
+        __syncthreads();
+        // a wave ranks every 16th, against four in a lane
+        uint2 other[RANKED / 64];
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        more += __shfl_xor(more, d);
-        equal += __shfl_xor(equal, d);
+        for (int u = 0; u < RANKED / 64; ++u) other[u] = u * 64 + lane < same ? near_border[u * 64 + lane] : make_uint2(0, 0);
+        for (int c = wave; c < same; c += SELECT_WAVES) {
+            const uint2 own = near_border[c];
+            int rank = 0;
+#pragma unroll
+            for (int u = 0; u < RANKED / 64; ++u)
+                rank += __popcll(__ballot(other[u].x > own.x || (other[u].x == own.x && other[u].y < own.y)));
+            if (rank < still && lane == 0) atomicAdd(&waves_kept[own.y / (uint32_t)piece], 1);
+            if (rank == still - 1 && lane == 0) {
+                found[0] = (int)own.x;
+                found[1] = (int)own.y;
+            }
+        }
+        __syncthreads();
+        border = (uint32_t)found[0];
+        last = found[1];
+        if (lane == 63) sh[wave] = mine + waves_kept[wave];
+    } else {
+        clear();
+        __syncthreads();
+        round(32 - ROUND_BITS[0] - ROUND_BITS[1], ROUND_BITS[1], false);
+        clear();
+        __syncthreads();
+        round(0, ROUND_BITS[2], false);
+        int equal = 0;
+        keys.each([&](int, uint32_t x) {
+            mine += __popcll(__ballot(x > border));
+            equal += __popcll(__ballot(x == border));
+        });
+        if (lane == 0) waves_kept[wave] = equal;
+        __syncthreads();
+        const int first = before(waves_kept);            // of the equal ones, those of waves before
+        if (first < still && still <= first + equal) {   // the last that stays is one of this wave's
+            int left = still - first;
+            keys.each([&](int i, uint32_t x) {
+                const uint64_t here = __ballot(x == border);
+                if (left > 0 && left <= __popcll(here)) {
+                    if ((here >> lane & 1) && __popcll(here & ((1ull << lane) - 1)) == left - 1) found[1] = i0 + i + lane;
+                }
+                left -= __popcll(here);
+            });
+        }
+        if (lane == 0) sh[wave] = mine + max(0, min(equal, still - first));
+        __syncthreads();
+        last = found[1];
     }
     __syncthreads();
-    if (lane == 0) {
-        sh[wave] = more;
-        sh[SELECT_WAVES + wave] = equal;
-    }
-    __syncthreads();
-    more = equal = 0;
-    for (int v = 0; v < wave; ++v) {
-        more += sh[v];
-        equal += sh[SELECT_WAVES + v];
-    }
-    for (int i = i0; i < i1; i += 64) {                  // whole waves
-        const uint32_t x = i + lane < i1 ? number(i + lane) : 0u;
-        const uint64_t up = __ballot(i + lane < i1 && x > border), same = __ballot(i + lane < i1 && x == border);
-        const uint64_t before = (1ull << lane) - 1;
-        const int g = more + __popcll(up & before), e = equal + __popcll(same & before);
-        if ((up >> lane & 1) || ((same >> lane & 1) && e < still)) kept[a.sinks + g + min(e, still)] = a.sinks + i + lane;
-        more += __popcll(up);
-        equal += __popcll(same);
-    }
+    int at = a.sinks + before(sh);
+    keys.each([&](int i, uint32_t x) {
+        const bool stays = x > border || (x == border && i0 + i + lane <= last);
+        const uint64_t all = __ballot(stays);
+        if (stays) kept[at + __popcll(all & ((1ull << lane) - 1))] = a.sinks + i0 + i + lane;
+        at += __popcll(all);
+    });
 }
 
 // ---- keep ---------------------------------------------------------------------------------
 // Rows move to places that are not behind their own, in place. Columns of a row do not touch each other: a workgroup
-// takes one 128-byte piece of all of a request's rows, in chunks in the order of their places, of which it
-// reads all rows before it writes one. Places rise and no row lies before its place, so what a chunk writes
-// no later one reads. A chunk is 1024 rows, 128 KB on its way a workgroup, since a request has
-// only 9 of them.
-constexpr int DIM = 576, SEGS = DIM * 2 / 128;
-constexpr int KEEP_THREADS = 512, KEEP_TURNS = 16, KEEP_ROWS = KEEP_THREADS / 8 * KEEP_TURNS;
-constexpr int KEEP_WEIGHTS = 4 * KEEP_THREADS;           // weights a workgroup
+// takes one piece of all of a request's rows, in chunks in the order of their places, of which it reads
+// all rows before it writes one. Places rise and no row lies before its place, so what a chunk writes no
+// later one reads. Pieces of 384 bytes, and 512 rows a chunk (196 KB on its way a workgroup), where there are
+// requests enough to fill the chip with them; otherwise 128 bytes and 1024 rows (64 requests of 4096 rows 90 and
+// 100 us, 4 of 2048 rows 23 and 12). The bytes bound it, which are not read again soon (past the caches: 94 us
+// where it was 100).
+constexpr int DIM = 576;
+constexpr int KEEP_TURNS = 16;               // rows that a lane has on their way
+constexpr int KEEP_WEIGHTS = 2048;           // weights a workgroup
 
 struct KeepArgs {
     uint16_t *cache;
@@ -216,7 +307,7 @@ struct KeepArgs {
     float *new_weights;
     int64_t w_row, nw_row;
     int tokens, most, pages, page, max_pages, columns;
-    uint32_t page_mul;                       // see page_of
+    uint32_t page_mul;                       // see quotient
     int page_shift;
 };
 
@@ -236,12 +327,15 @@ struct Kept {
     }
 };
 
-__global__ __launch_bounds__(KEEP_THREADS) void latent_keep_kernel(KeepArgs a) {
+// LANES: of 16 bytes that a workgroup takes of a row.
+template <int LANES, int THREADS>
+__global__ __launch_bounds__(THREADS) void latent_keep_kernel(KeepArgs a) {
+    constexpr int KEEP_ROWS = THREADS / LANES * KEEP_TURNS, SEGS = DIM / 8 / LANES;
     __shared__ int64_t from[KEEP_ROWS], to[KEEP_ROWS];   // elements of the cache; to -1: the row stays
     const int tid = threadIdx.x, seg = blockIdx.x, req = blockIdx.y;
     const Kept k(a, req);
     if (seg >= SEGS) {                                   // weights, which go to an array of their own
-        for (int u = 0; u < KEEP_WEIGHTS; u += KEEP_THREADS) {
+        for (int u = 0; u < KEEP_WEIGHTS; u += THREADS) {
             const int place = (seg - SEGS) * KEEP_WEIGHTS + u + tid;
             if (place >= a.columns) return;
             float w = 0.0f;
@@ -258,10 +352,10 @@ __global__ __launch_bounds__(KEEP_THREADS) void latent_keep_kernel(KeepArgs a) {
         const int page = page_of(a, row), id = min(max(a.table[req * a.t_row + page], 0), a.pages - 1);
         return id * a.c_page + (row - page * a.page) * a.c_row;
     };
-    uint16_t *piece = a.cache + seg * 64 + (tid & 7) * 8;
+    uint16_t *piece = a.cache + (seg * LANES + tid % LANES) * 8;
     for (int j0 = 0; j0 < k.count; j0 += KEEP_ROWS) {
         int moves = 0;
-        for (int j = j0 + tid; j < min(k.count, j0 + KEEP_ROWS); j += KEEP_THREADS) {
+        for (int j = j0 + tid; j < min(k.count, j0 + KEEP_ROWS); j += THREADS) {
             const int row = k.source(a, req, j);
             const bool move = row != k.base + j;
             if (move) from[j - j0] = place(row);
@@ -272,16 +366,18 @@ __global__ __launch_bounds__(KEEP_THREADS) void latent_keep_kernel(KeepArgs a) {
         u32x4_t x[KEEP_TURNS];
 #pragma unroll
         for (int u = 0; u < KEEP_TURNS; ++u) {
-            const int j = u * (KEEP_THREADS / 8) + (tid >> 3);
+            const int j = u * (THREADS / LANES) + tid / LANES;
             x[u] = u32x4_t{0, 0, 0, 0};
-            if (j0 + j < k.count && to[j] >= 0) x[u] = *reinterpret_cast<const u32x4_t *>(piece + from[j]);
+            if (j0 + j < k.count && to[j] >= 0) 
+                x[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(piece + from[j]));
         }
         in_vgpr(x);                                      // all are there
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < KEEP_TURNS; ++u) {
-            const int j = u * (KEEP_THREADS / 8) + (tid >> 3);
-            if (j0 + j < k.count && to[j] >= 0) *reinterpret_cast<u32x4_t *>(piece + to[j]) = x[u];
+            const int j = u * (THREADS / LANES) + tid / LANES;
+            if (j0 + j < k.count && to[j] >= 0) 
+                __builtin_nontemporal_store(x[u], reinterpret_cast<u32x4_t *>(piece + to[j]));
         }
         __syncthreads();                                 // from and to are read
     }
@@ -308,7 +404,10 @@ hipError_t launch_latent_select(const skinny_latent_select_args &p, hipStream_t 
     a.budget = (int)p.budget;
     a.sinks = (int)p.sinks;
     a.recent = (int)p.recent;
-    hipLaunchKernelGGL(latent_select_kernel, dim3((unsigned)p.batch), dim3(SELECT_THREADS), 0, stream, a);
+    if (a.columns <= HELD * SELECT_THREADS)
+        hipLaunchKernelGGL(latent_select_kernel<HeldKeys>, dim3((unsigned)p.batch), dim3(SELECT_THREADS), 0, stream, a);
+    else
+        hipLaunchKernelGGL(latent_select_kernel<ReadKeys>, dim3((unsigned)p.batch), dim3(SELECT_THREADS), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -334,10 +433,15 @@ hipError_t launch_latent_keep(const skinny_latent_keep_args &p, hipStream_t stre
     a.page = (int)p.page;
     a.max_pages = (int)p.max_pages;
     a.columns = (int)p.columns;
-    page_reciprocal(a.page, a.page_mul, a.page_shift);
+    reciprocal(a.page, a.page_mul, a.page_shift);
     const int64_t wblocks = a.new_weights ? (p.columns + KEEP_WEIGHTS - 1) / KEEP_WEIGHTS : 0;
-    hipLaunchKernelGGL(latent_keep_kernel, dim3((unsigned)(SEGS + wblocks), (unsigned)p.batch), dim3(KEEP_THREADS), 0, stream,
-                       a);
+    // few rows a request, as of a tree's path: few workgroups (64 requests of 5 rows 5.1 and 3.9 us)
+    if (p.batch >= 64 || p.most <= 64)
+        hipLaunchKernelGGL((latent_keep_kernel<24, 768>), dim3((unsigned)(DIM / 8 / 24 + wblocks), (unsigned)p.batch), dim3(768), 0,
+                           stream, a);
+    else
+        hipLaunchKernelGGL((latent_keep_kernel<8, 512>), dim3((unsigned)(DIM / 8 / 8 + wblocks), (unsigned)p.batch), dim3(512), 0,
+                           stream, a);
     return hipGetLastError();
 }
 

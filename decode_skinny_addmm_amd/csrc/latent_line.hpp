@@ -69,19 +69,20 @@ __device__ __forceinline__ int64_t run_start(int64_t total, int grid, int b) { r
 // the workgroup whose run holds place x (no run is empty: grid <= total)
 __device__ __forceinline__ int run_of(int64_t total, int grid, int64_t x) { return (int)(((x + 1) * grid - 1) / total); }
 
-// k / page for 0 <= k < 2^30: (k * page_mul) >> (32 + page_shift), page_mul 0 for a page of 1.
-// 2^bits >= page > 2^(bits - 1): the reciprocal 2^(31 + bits) / page, rounded up, fits 32 bits, and
-// for k < 2^30 its rounding adds less than 2^-(1 + bits) < 1 / page to the quotient: exact
-inline void page_reciprocal(int page, uint32_t &mul, int &shift) {
+// k / d for 0 <= k < 2^30: (k * mul) >> (32 + shift), mul 0 for a d of 1.
+// 2^bits >= d > 2^(bits - 1): the reciprocal 2^(31 + bits) / d, rounded up, fits 32 bits, and
+// for k < 2^30 its rounding adds less than 2^-(1 + bits) < 1 / d to the quotient: exact
+inline void reciprocal(int d, uint32_t &mul, int &shift) {
     int bits = 1;
-    while ((1 << bits) < page) ++bits;
-    mul = page == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + bits)) + page - 1) / page);
+    while ((1 << bits) < d) ++bits;
+    mul = d == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + bits)) + d - 1) / d);
     shift = bits - 1;
 }
-template <typename A>
-__device__ __forceinline__ int page_of(const A &a, int k) {
-    return a.page_mul ? (int)(__umulhi((uint32_t)k, a.page_mul) >> a.page_shift) : k;
+__device__ __forceinline__ int quotient(int k, uint32_t mul, int shift) {
+    return mul ? (int)(__umulhi((uint32_t)k, mul) >> shift) : k;
 }
+template <typename A>
+__device__ __forceinline__ int page_of(const A &a, int k) { return quotient(k, a.page_mul, a.page_shift); }
 
 }  // namespace latent
 }  // namespace skinny

@@ -105,17 +105,6 @@ __host__ __device__ inline int64_t split_floats(int64_t nq, int64_t heads) { ret
 // cu[i], never outside 0 .. n
 __device__ __forceinline__ int start(const int32_t *cu, int i, int64_t n) { return (int)min((int64_t)max(cu[i], 0), n); }
 
-// v's sum over the lanes up to this one: within rows of 16 lanes, then over the rows.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);      // row_shr:1
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);      // row_shr:2
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);      // row_shr:4
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);      // row_shr:8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);      // row_bcast:15 to rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);      // row_bcast:31 to rows 2 and 3
-    return v;
-}
-
 // The sequence and its query tile that are number `at` of all: first the tiles that see more keys
 // than sequences have on average, then the others, each sequence's from its last, so that a long
 // prompt among short ones does not start last (4000 tokens before 30 x 200, 16 heads: 162 -> 123 us;
