@@ -1,6 +1,8 @@
 // latent.hpp -- device helpers shared by the latent attention kernels (gfx950 only).
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace skinny {
@@ -44,6 +46,16 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
 }
 
+// f(0), f(1) ... f(N - 1), each number a constant of its own type: arrays that it indexes stay in registers
+// where a loop would be unrolled too late for that.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(const F &f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        static_for<N, I + 1>(f);
+    }
+}
+
 // ---- loads straight into LDS --------------------------------------------------------------
 // lane l's 16 bytes at src (4 with load_lds_word) go to LDS address lds + 16 l (4 l), and of N
 // pieces those at src + 128 i to lds + 1024 i + 16 l. lds is the same in all lanes. Written out
@@ -72,15 +84,24 @@ __device__ __forceinline__ void load_lds_pieces(const void *src, int lds) {
         load_lds_pieces<N, I + 1>(src, lds);
     }
 }
-// the same in no lane unless `on`: the count of loads in flight goes by either way (called with all
-// lanes active)
-template <int I>
-__device__ __forceinline__ void load_lds_piece_if(bool on, const void *src, int lds) {
+// the same in the lanes of `lanes`, all or none of them: the count of loads in flight goes by either way
+// (called with all lanes active)
+__device__ __forceinline__ uint64_t lanes_if(bool on) {
     const uint32_t half = uniform(on ? -1 : 0);
-    const uint64_t lanes = (uint64_t)half << 32 | half;
+    return (uint64_t)half << 32 | half;
+}
+template <int I>
+__device__ __forceinline__ void load_lds_piece_in(uint64_t lanes, const void *src, int lds) {
     asm volatile("s_add_u32 m0, %0, %2\n\ts_mov_b64 exec, %4\n\tglobal_load_lds_dwordx4 %1, off offset:%3\n\t"
                  "s_mov_b64 exec, -1"
                  :: "s"(lds), "v"(src), "i"(896 * I), "i"(128 * I), "s"(lanes) : "memory", "scc");
+}
+// the same from `base`, the same in all lanes, and each lane's own bytes from there
+template <int I>
+__device__ __forceinline__ void load_lds_piece_in(uint64_t lanes, const void *base, uint32_t own, int lds) {
+    asm volatile("s_add_u32 m0, %0, %2\n\ts_mov_b64 exec, %4\n\tglobal_load_lds_dwordx4 %1, %5 offset:%3\n\t"
+                 "s_mov_b64 exec, -1"
+                 :: "s"(lds), "v"(own), "i"(896 * I), "i"(128 * I), "s"(lanes), "s"(base) : "memory", "scc");
 }
 
 // ---- staged key and value rows ----------------------------------------------------------

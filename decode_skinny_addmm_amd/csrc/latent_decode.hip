@@ -39,7 +39,6 @@ constexpr int KT = 32;                       // keys a tile
 constexpr int SEGS = DIM * 2 / 128;          // 128-byte pieces of a row
 constexpr int STAGES = 4;
 constexpr int STAGE_BYTES = KT * DIM * 2;
-constexpr int PW = SEGS + 1;                 // loads a wave issues per stage: a page id and pieces
 constexpr int THREADS = 256;
 
 struct DecodeArgs {
@@ -57,8 +56,8 @@ struct DecodeArgs {
     int2 *cuts;                              // a unit (request and row group): its first partial, its last workgroup
     int batch, tokens, heads, pages, page, max_pages;
     int rows, groups, grid;                  // rows a request, row groups a request, workgroups
-    uint32_t page_mul;                       // see quotient
-    int page_shift;
+    uint32_t page_mul, head_mul;             // see quotient
+    int page_shift, head_shift;
     float c;                                 // scale * log2(e)
 };
 
@@ -139,10 +138,9 @@ struct Shape {
     // softmax of a tile beside the score product of the next: takes registers that 128 rows x 512
     // sums leave no room for
     static constexpr bool FLOW = MB < 128;
-    // fragments read ahead of the matrix instructions (they need about 130 cycles; a 32 x 32
-    // instruction takes 32 of them): of keys, and of dim tiles of values. With 128 rows more of them
-    // cost more than they hide (groups of 6 and 2: 83 -> 86 us for 32 requests x 128 heads x 4000 keys)
-    static constexpr int KG = MB == 128 ? 4 : 6, VG = MB < 128 && ND >= 4 ? 2 : 1;
+    // Fragments read ahead of the matrix instructions (they need about 130 cycles; a 32 x 32 instruction
+    // takes 32 of them, a 16 x 16 one 16): of keys, and of values.
+    static constexpr int KAHEAD = MB == 128 ? 7 : 11, VAHEAD = 3;
 };
 
 // What a workgroup stages, in order: for each unit (request and row group) of its run, the unit's
@@ -167,18 +165,37 @@ struct Due {
     int row, req;
     int kind;                                // 0: none, 1: queries, 2: keys
 };
+// The same where a wave's 8 rows of keys lie in one page: all of it the same in all lanes.
+struct BlockDue {
+    int row, kind;                           // the wave's first row
+    int id;                                  // of its page
+};
+// Where an item's pieces come from (base and each lane's own bytes, or its address) and go to.
+struct Source {
+    const uint16_t *base;
+    uint32_t own;
+    int kind;                                // that `own` is of
+    int to;
+    uint64_t lanes;                          // all if there is an item, else none
+};
 
 // of a row's pieces, those that go out with group `at` of `of` (both known when compiled)
-template <int I = 0>
-__device__ __forceinline__ void pieces_at(int at, int of, bool on, const void *src, int lds) {
+template <bool BLOCKS, int I = 0>
+__device__ __forceinline__ void pieces_at(int at, int of, const Source &p) {
     if constexpr (I < SEGS) {
-        if (I * of / SEGS == at) load_lds_piece_if<I>(on, src, lds);
-        pieces_at<I + 1>(at, of, on, src, lds);
+        if (I * of / SEGS == at) {
+            if constexpr (BLOCKS) load_lds_piece_in<I>(p.lanes, p.base, p.own, p.to);
+            else load_lds_piece_in<I>(p.lanes, p.base, p.to);
+        }
+        pieces_at<BLOCKS, I + 1>(at, of, p);
     }
 }
 
 // MASKED: of the keys before its own, a row sees those of a mask, held a tile as 32 bits.
-template <typename T, int WR, int WD, bool MASKED>
+// BLOCKS: pages are whole groups of 8 rows, so that the 8 keys that a wave stages of a tile lie in one page, whose
+// id and address are worked out once a wave, by the scalar unit. A step's cursor and addresses take the wave
+// some 950 cycles otherwise, and MEASURED with them, of a tile of 128 rows' 5300.
+template <typename T, int WR, int WD, bool MASKED, bool BLOCKS>
 __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional_t<MASKED, MaskedArgs, DecodeArgs> a) {
     typedef Shape<T, WR, WD> S;
     typedef typename T::acc_t acc_t;
@@ -190,6 +207,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
     const int row = T::row(lane), grp = T::grp(lane);
     const int wr = wave % WR, d0 = (wave / WR) * (L / WD);
     constexpr int QT = (S::MB + KT - 1) / KT;            // query tiles a unit
+    constexpr int PW = BLOCKS ? SEGS : SEGS + 1;         // loads a wave issues a stage: pieces, and a word of page ids
 
     Line<decltype(a), THREADS> line;
     line.measure(a, sh);
@@ -220,6 +238,87 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
         c.g = (int)((lo - base) / tiles);
         c.enter(a, (int)((lo - base) % tiles), QT);
     }
+    // past the unit's query tiles, its key tiles, or into the next unit
+    auto advance = [&]() __attribute__((always_inline)) {
+        if (c.t < 0) {
+            if (++c.t == 0) c.t = c.t0;
+        } else if (++c.t == c.end) {
+            c.left -= c.end - c.t0;
+            c.more = c.left > 0;
+            if (c.more) {
+                if (++c.g == a.groups) {
+                    c.g = 0;
+                    ++c.req;
+                }
+                c.enter(a, 0, QT);
+            }
+        }
+    };
+    Source src{a.cache, 0, 0, 0, ~0ull};
+    auto stage_address = [&](int slot) __attribute__((always_inline)) {
+        return lds_address(ring + (uint32_t)slot % STAGES * STAGE_BYTES + wave * (SEGS * 1024));
+    };
+    auto chunk_of = [&](int x) __attribute__((always_inline)) { return ((x & 7) ^ swz(8 * wave + (x >> 3))) * 8; };
+    // Item n is staged after step n, and the pieces of item n + LOOK go out between the matrix instructions that
+    // follow, one at a time (ten loads in a row hold a wave up for 1100 cycles). The stage that they fill is
+    // free: the value product is done with item n - 1, or, where it runs one step behind the score
+    // product, with item n - 2. plan() takes the next item, aim() works out where a due one comes from. With
+    // page ids by lane, step n takes those of item n + 2 LOOK, by way of LDS, and aims at item n + LOOK; by block,
+    // it plans item n + LOOK + 1, whose id is there when the next step aims at it.
+    constexpr int LOOK = S::FLOW ? 2 : 3;
+    static_assert(LOOK <= QT + 1, "the items issued before the first step exist");
+    // Of the unit that is staged: its row of the table, its last block; of the next tile: the wave's first key.
+    typedef const __attribute__((address_space(4))) int32_t *constant_ptr;
+    int64_t ids_row = 0;
+    int last_block = 0, next_key = 0, of_req = 0;
+    auto enter_block = [&]() __attribute__((always_inline)) {
+        ids_row = c.req * a.t_row;
+        last_block = max(0, c.len - 1) & ~7;
+        next_key = c.tiles.at(c.t0) * KT + 8 * wave;
+        of_req = c.req;
+    };
+    auto plan_block = [&]() __attribute__((always_inline)) {
+        BlockDue d{0, 0, 0};
+        int page = 0;
+        if (c.more) {
+            bool same = false;                           // the next item is this unit's next tile of keys
+            if (c.t >= 0) {                              // blocks past the end repeat the last one: masked
+                const int k = min(next_key, last_block);
+                page = page_of(a, k);
+                d.row = k - page * a.page;
+                d.kind = 2;
+                next_key += KT;
+                if (MASKED && c.t + 1 == c.tiles.head) next_key += c.tiles.skip * KT;
+                same = c.t + 1 < c.end;
+            } else {
+                if (c.t == -QT) enter_block();
+                d.row = c.g * S::MB + (c.t + QT) * KT + 8 * wave;
+                d.kind = 1;
+            }
+            if (same) ++c.t;
+            else advance();
+        }
+        // loaded in any case, so that nothing waits for it here
+        d.id = ((constant_ptr)(uintptr_t)(a.table + uniform((int64_t)(ids_row + page))))[0];
+        return d;
+    };
+    auto aim_block = [&](const BlockDue &d, int slot) __attribute__((always_inline)) {
+        if (d.kind == 2) {                               // ids outside the pool are clamped
+            src.base = a.cache + (uint64_t)(uint32_t)min(max(d.id, 0), a.pages - 1) * (uint32_t)a.c_page + (uint32_t)d.row * (uint32_t)a.c_row;
+            if (src.kind != 2) {
+                const int x = own_lane();
+                src.own = ((uint32_t)(x >> 3) * (uint32_t)a.c_row + chunk_of(x)) * 2;
+                src.kind = 2;
+            }
+        } else {                                         // rows past the last repeat it
+            const int x = own_lane();
+            const int r = min(d.row + (x >> 3), a.rows - 1), j = quotient(r, a.head_mul, a.head_shift), h = r - j * a.heads;
+            src.base = a.q + (int64_t)of_req * a.tokens * a.q_row;
+            src.own = ((uint32_t)j * (uint32_t)a.q_row + (uint32_t)h * (uint32_t)a.q_head + chunk_of(x)) * 2;
+            src.kind = 1;
+        }
+        src.to = stage_address(slot);
+    };
     // takes the next item; its page ids go to place `slot` of the ids' ring
     auto plan = [&](int slot) __attribute__((always_inline)) {
         Due d{0, c.req, 0};
@@ -229,82 +328,78 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
             if (c.t < 0) {                               // rows past the last repeat it
                 d.row = min(c.g * S::MB + (c.t + QT) * KT + kl, a.rows - 1);
                 d.kind = 1;
-                if (++c.t == 0) c.t = c.t0;
             } else {                                     // keys past the end repeat the last one: masked
                 const int k = max(0, min(c.tiles.at(c.t) * KT + kl, c.len - 1));
                 const int page = page_of(a, k);
                 id = a.table + c.req * a.t_row + page;
                 d.row = k - page * a.page;
                 d.kind = 2;
-                if (++c.t == c.end) {
-                    c.left -= c.end - c.t0;
-                    c.more = c.left > 0;
-                    if (c.more) {
-                        if (++c.g == a.groups) {
-                            c.g = 0;
-                            ++c.req;
-                        }
-                        c.enter(a, 0, QT);
-                    }
-                }
             }
+            advance();
         }
         load_lds_word(id, lds_address(ids + slot % STAGES * 256));
         return d;
     };
-    // where a due item's pieces come from and go to
-    const uint16_t *from = a.cache;
-    int to = 0;
     auto aim = [&](const Due &d, int slot) __attribute__((always_inline)) {
-        const int x = own_lane();
-        const int chunk = ((x & 7) ^ swz(8 * wave + (x >> 3))) * 8;
+        const int x = own_lane(), chunk = chunk_of(x);
         if (d.kind == 2) {                               // ids outside the pool are clamped
             const int id = *(__attribute__((address_space(3))) const int32_t *)(ids + slot % STAGES * 256 + x * 4);
-            from = a.cache + (int64_t)min(max(id, 0), a.pages - 1) * a.c_page + (int64_t)d.row * a.c_row + chunk;
+            src.base = a.cache + (int64_t)min(max(id, 0), a.pages - 1) * a.c_page + (int64_t)d.row * a.c_row + chunk;
         } else {
-            const int j = d.row / a.heads, h = d.row - j * a.heads;
-            from = a.q + ((int64_t)d.req * a.tokens + j) * a.q_row + h * a.q_head + chunk;
+            const int j = quotient(d.row, a.head_mul, a.head_shift), h = d.row - j * a.heads;
+            src.base = a.q + ((int64_t)d.req * a.tokens + j) * a.q_row + h * a.q_head + chunk;
         }
-        to = lds_address(ring + slot % STAGES * STAGE_BYTES + wave * (SEGS * 1024));
+        src.to = stage_address(slot);
     };
-    // Item n is staged after step n, which takes the ids of item n + 2 LOOK and aims at item n + LOOK;
-    // the pieces of the latter go out between the matrix instructions that follow, one at a time
-    // (ten loads in a row hold a wave up for 1100 cycles). The stage that they fill is free: the
-    // value product is done with item n - 1, or, where it runs one step behind the score product,
-    // with item n - 2.
-    constexpr int LOOK = S::FLOW ? 2 : 3;
-    static_assert(LOOK <= QT + 1, "the items issued before the first step exist");
     int n = -1;
     Due due[LOOK];                                       // the next items to be issued
-    {
+    BlockDue due_block;                                  // the next one
+    if constexpr (BLOCKS) {
+#pragma unroll
+        for (int x = 0; x < LOOK; ++x) {
+            aim_block(plan_block(), x);
+            pieces_at<BLOCKS>(0, 1, src);
+        }
+        due_block = plan_block();
+    } else {
         Due early[LOOK];
 #pragma unroll
         for (int x = 0; x < LOOK; ++x) early[x] = plan(x);
         due[0] = plan(LOOK);
         aim(early[0], 0);                                // queries: their ids are not needed
-        load_lds_pieces<SEGS>(from, to);
+        pieces_at<BLOCKS>(0, 1, src);
         wait_vmcnt<SEGS>();
 #pragma unroll
         for (int x = 1; x < LOOK; ++x) {
             due[x] = plan(LOOK + x);
             aim(early[x], x);
-            load_lds_pieces<SEGS>(from, to);
+            pieces_at<BLOCKS>(0, 1, src);
         }
     }
     lds_u8 *st = ring, *st_before = ring;
-    bool live = false;                                   // there is an item to issue
     auto step = [&]() __attribute__((always_inline)) {
         ++n;
         wait_vmcnt<PW *(LOOK - 1)>();
         lds_barrier();
-        live = due[0].kind != 0;
-        const Due d = plan(n + 2 * LOOK);
-        if (live) aim(due[0], n + LOOK);
+        if constexpr (BLOCKS) {
+            const bool there = due_block.kind != 0;
+            if (there) aim_block(due_block, n + LOOK);
+            due_block = plan_block();
+            src.base = (const uint16_t *)uniform((int64_t)src.base);     // in scalar registers from here on
+            src.to = uniform(src.to);
+            src.lanes = lanes_if(there);
+        } else {
+            const bool there = due[0].kind != 0;
+            const Due d = plan(n + 2 * LOOK);
+            if (there) aim(due[0], n + LOOK);
+            src.to = uniform(src.to);
+            src.lanes = lanes_if(there);
 #pragma unroll
-        for (int x = 0; x + 1 < LOOK; ++x) due[x] = due[x + 1];
-        due[LOOK - 1] = d;
+            for (int x = 0; x + 1 < LOOK; ++x) due[x] = due[x + 1];
+            due[LOOK - 1] = d;
+        }
         st_before = st;
-        st = ring + n % STAGES * STAGE_BYTES;
+        st = ring + (uint32_t)n % STAGES * STAGE_BYTES;
     };
     // ---- fragment places within a stage. Score product: key row `row` of each subtile (subtiles
     // start at multiples of 16 rows: the same swizzle), K step k reads 16-byte chunk
@@ -338,31 +433,31 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
 
     constexpr int NT = KT / T::ROWS;                     // key subtiles: 1 or 2
     constexpr int XS = T::NS / 8;                        // key steps of the value product
-    constexpr int KG = S::KG, NG = S::KS * NT / KG;      // fragments a group, groups of the score product
-    static_assert(KG * NG == S::KS * NT, "whole groups");
+    constexpr int NK = S::KS * NT, NV = S::ND * XS;      // fragments of the score product, of the value product
     // places between matrix instructions where pieces go out: all of a step's, if a value product
     // follows each score product
-    constexpr int ISSUES = S::FLOW ? NG : NG + S::ND / S::VG;
+    constexpr int ISSUES = S::FLOW ? NK : NK + NV;
     u32x4_t qf[S::KS], pf[XS];
     acc_t o[S::ND], s[NT], next[NT];
     float m, l;
 
     // S^T = K Q^T of the staged tile into `sum`, and beside it, in slices between the matrix
-    // instructions, the softmax weights of the tile before from s. Fragments are read a group
-    // ahead; the scheduling barriers keep the groups apart, and the compiler from spilling.
+    // instructions, the softmax weights of the tile before from s. Fragments are read KAHEAD
+    // instructions ahead; the scheduling barriers keep them there, and the compiler from spilling.
     // Weights are rounded to bf16 for the matrix product, whose operands are of one type (by 2^-8 relative
     // at most, independently of each other: an output's error grows from the 0.0017 of its own rounding
     // to 0.0022 at most in the listed cases); their sum l is of the unrounded ones.
     float mu = 0.0f;
-    auto weight_slice = [&](int i0, int i1) __attribute__((always_inline)) {
+    auto weight_pair = [&](int i) __attribute__((always_inline)) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(s[i / T::NO][i % T::NO], a.c, -mu));
+        const float y = __builtin_amdgcn_exp2f(fmaf(s[(i + 1) / T::NO][(i + 1) % T::NO], a.c, -mu));
+        l += x;
+        l += y;
+        pf[i / 8][i % 8 / 2] = pack_bf16(x, y);
+    };
+    auto all_weights = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = i0; i < i1; i += 2) {
-            const float x = __builtin_amdgcn_exp2f(fmaf(s[i / T::NO][i % T::NO], a.c, -mu));
-            const float y = __builtin_amdgcn_exp2f(fmaf(s[(i + 1) / T::NO][(i + 1) % T::NO], a.c, -mu));
-            l += x;
-            l += y;
-            pf[i / 8][i % 8 / 2] = pack_bf16(x, y);
-        }
+        for (int i = 0; i < T::NS; i += 2) weight_pair(i);
     };
     auto scores = [&](acc_t (&sum)[NT], auto with_weights) __attribute__((always_inline)) {
         lds_u8 *at[KA];
@@ -371,25 +466,21 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
             const int k = e / NT, u = e % NT;
             return *(const lds_u32x4 *)(at[k % KA] + (u * T::ROWS / 8) * (SEGS * 1024) + (k / KA) * 1024);
         };
-        u32x4_t kf[2][KG];
+        u32x4_t kf[S::KAHEAD + 1];
 #pragma unroll
-        for (int e = 0; e < KG; ++e) kf[0][e] = key_frag(e);
-#pragma unroll
-        for (int gi = 0; gi < NG; ++gi) {
+        for (int e = 0; e < S::KAHEAD; ++e) kf[e] = key_frag(e);
+        static_for<NK>([&](auto e) __attribute__((always_inline)) {
             __builtin_amdgcn_sched_barrier(0);
-            if (gi + 1 < NG) {
-#pragma unroll
-                for (int e = 0; e < KG; ++e) kf[(gi + 1) & 1][e] = key_frag((gi + 1) * KG + e);
-            }
+            if constexpr (e + S::KAHEAD < NK) kf[(e + S::KAHEAD) % (S::KAHEAD + 1)] = key_frag(e + S::KAHEAD);
             __builtin_amdgcn_sched_barrier(0);
+            sum[e % NT] = T::mfma(kf[e % (S::KAHEAD + 1)], qf[e / NT], e / NT ? sum[e % NT] : acc_t{0.0f});
+            if constexpr (with_weights.value) {
 #pragma unroll
-            for (int e = 0; e < KG; ++e) {
-                const int k_at = gi * KG + e;
-                sum[k_at % NT] = T::mfma(kf[gi & 1][e], qf[k_at / NT], k_at / NT ? sum[k_at % NT] : acc_t{0.0f});
+                for (int i = 0; i < T::NS / 2; ++i)
+                    if (i * NK / (T::NS / 2) == e) weight_pair(2 * i);
             }
-            if constexpr (with_weights.value) weight_slice(T::NS / 2 * gi / NG * 2, T::NS / 2 * (gi + 1) / NG * 2);
-            pieces_at(gi, ISSUES, live, from, to);
-        }
+            pieces_at<BLOCKS>(e, ISSUES, src);
+        });
         in_vgpr(sum);
     };
     // O^T += V^T P^T. An A fragment of V^T is dim tile i, key step x; B register pairs hold keys
@@ -417,29 +508,24 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                     __builtin_amdgcn_sched_barrier(0);
                     o[i] = T::mfma(pick_values(value(i, x), others), pf[x], o[i]);
                 }
-                if constexpr (!S::FLOW)
-                    if (i % S::VG == S::VG - 1) pieces_at(NG + i / S::VG, ISSUES, live && !others, from, to);
+                if constexpr (!S::FLOW) {
+#pragma unroll
+                    for (int x = 0; x < XS; ++x)
+                        if (!others) pieces_at<BLOCKS>(NK + i * XS + x, ISSUES, src);
+                }
             }
             return;
         }
-        constexpr int VG = S::VG;
-        u32x4_t vf[2][VG * XS];
+        u32x4_t vf[S::VAHEAD + 1];
 #pragma unroll
-        for (int e = 0; e < VG * XS; ++e) vf[0][e] = value(e / XS, e % XS);
-#pragma unroll
-        for (int i = 0; i < S::ND; i += VG) {
+        for (int e = 0; e < S::VAHEAD; ++e) vf[e] = value(e / XS, e % XS);
+        static_for<NV>([&](auto e) __attribute__((always_inline)) {
             __builtin_amdgcn_sched_barrier(0);
-            if (i + VG < S::ND) {
-#pragma unroll
-                for (int e = 0; e < VG * XS; ++e) vf[(i / VG + 1) & 1][e] = value(i + VG + e / XS, e % XS);
-            }
+            if constexpr (e + S::VAHEAD < NV) vf[(e + S::VAHEAD) % (S::VAHEAD + 1)] = value((e + S::VAHEAD) / XS, (e + S::VAHEAD) % XS);
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int e = 0; e < VG * XS; ++e) {
-                o[i + e / XS] = T::mfma(vf[i / VG & 1][e], pf[e % XS], o[i + e / XS]);
-            }
-            if constexpr (!S::FLOW) pieces_at(NG + i / VG, ISSUES, live, from, to);
-        }
+            o[e / XS] = T::mfma(vf[e % (S::VAHEAD + 1)], pf[e % XS], o[e / XS]);
+            if constexpr (!S::FLOW) pieces_at<BLOCKS>(NK + e, ISSUES, src);
+        });
     };
     // The same for tile t with scores that are not finite, of which some rows see less than others. A
     // latent that is not finite must not reach rows that do not see it, whose weight 0 times it is NaN;
@@ -509,7 +595,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
 
         for (int qi = 0; qi < QT; ++qi) {
             step();
-            pieces_at(0, 1, live, from, to);
+            pieces_at<BLOCKS>(0, 1, src);
             if (qi == wr * T::ROWS / KT) {
                 lds_u8 *at[KA];
                 find_keys(st + wr * T::ROWS % KT / 8 * (SEGS * 1024), at);
@@ -596,7 +682,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                     rescale();
                     if (!odd && t + 1 < t1) continue;
                 }
-                weight_slice(0, T::NS);
+                all_weights();
                 if (odd) add_values_carefully(st, sees_of(t));     // rare
                 else add_values(st, std::false_type(), false);
                 in_acc(o);
@@ -613,7 +699,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                     }
                     scored = false;
                     if (odd || grow) break;
-                    weight_slice(0, T::NS);
+                    all_weights();
                     add_values(st, std::false_type(), false);
                 } while (++t < t1);
                 if (t >= t1) break;
@@ -622,7 +708,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                     scored = true;
                     continue;
                 }
-                weight_slice(0, T::NS);
+                all_weights();
                 add_values_carefully(st, sees_of(t));      // rare
                 if (++t >= t1) break;
             }
@@ -784,9 +870,13 @@ hipError_t launch_join(const DecodeArgs &a, hipStream_t stream) {
 }
 
 template <typename T, int WR, int WD, typename A>
-hipError_t launch_shape(A a, hipStream_t stream) {
+hipError_t launch_shape(A a, bool blocks, hipStream_t stream) {
+    constexpr bool MASKED = std::is_same_v<A, MaskedArgs>;
     a.cuts = reinterpret_cast<int2 *>(a.work + 2 * a.grid * part_floats<Shape<T, WR, WD>::MB>());
-    hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, std::is_same_v<A, MaskedArgs>>), dim3((unsigned)a.grid), dim3(THREADS), 0, stream, a);
+    if (blocks)
+        hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, true>), dim3((unsigned)a.grid), dim3(THREADS), 0, stream, a);
+    else
+        hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, false>), dim3((unsigned)a.grid), dim3(THREADS), 0, stream, a);
     hipError_t err = hipGetLastError();
     // one workgroup takes every run whole: nothing to join
     if (err != hipSuccess || a.grid == 1) return err;
@@ -845,6 +935,7 @@ static DecodeArgs decode_args(const skinny_latent_decode_args &p, int cus) {
     a.max_pages = (int)p.max_pages;
     a.rows = a.tokens * a.heads;
     reciprocal(a.page, a.page_mul, a.page_shift);
+    reciprocal(a.heads, a.head_mul, a.head_shift);
     const int mb = block_rows(a.rows);
     a.groups = (a.rows + mb - 1) / mb;
     a.c = p.scale * kLog2e;
@@ -856,11 +947,14 @@ static DecodeArgs decode_args(const skinny_latent_decode_args &p, int cus) {
 
 template <typename A>
 static hipError_t launch(const A &a, hipStream_t stream) {
+    // a page's bytes, and a lane's from its request's first query, fit 31 bits
+    const int64_t most = (int64_t)1 << 29;
+    const bool blocks = a.page % 8 == 0 && a.c_row < most / a.page && (a.pages <= 1 || a.c_page < most) && a.q_row < most / a.tokens && a.q_head < most / a.heads;
     switch (block_rows(a.rows)) {
-        case 16: return launch_shape<Tile16, 1, 4>(a, stream);
-        case 32: return launch_shape<Tile16, 2, 2>(a, stream);
-        case 64: return launch_shape<Tile16, 4, 1>(a, stream);
-        default: return launch_shape<Tile32, 4, 1>(a, stream);
+        case 16: return launch_shape<Tile16, 1, 4>(a, blocks, stream);
+        case 32: return launch_shape<Tile16, 2, 2>(a, blocks, stream);
+        case 64: return launch_shape<Tile16, 4, 1>(a, blocks, stream);
+        default: return launch_shape<Tile32, 4, 1>(a, blocks, stream);
     }
 }
 
@@ -870,6 +964,9 @@ hipError_t launch_latent_decode(const skinny_latent_decode_args &p, int cus, hip
 
 hipError_t launch_latent_masked_decode(const skinny_latent_decode_args &p, const skinny_latent_mask &m, int cus,
                                        hipStream_t stream) {
+    // a window as long as a request can be hides nothing
+    const int64_t window = m.window < p.max_pages * p.page ? m.window : 0;
+    if (!m.tree && !window) return launch_latent_decode(p, cus, stream);
     MaskedArgs a;
     static_cast<DecodeArgs &>(a) = decode_args(p, cus);
     a.tree = m.tree;
@@ -877,8 +974,8 @@ hipError_t launch_latent_masked_decode(const skinny_latent_decode_args &p, const
     a.tree_row = m.tree_stride;
     a.depth_row = m.depth_stride;
     a.words = (int)((p.tokens + 31) / 32);
-    a.window = (int)std::min<int64_t>(m.window, INT_MAX / 2);
-    a.sinks = m.window ? (int)std::min<int64_t>(m.sinks, INT_MAX / 2) : 0;
+    a.window = (int)window;                              // fewer than 2^30
+    a.sinks = window ? (int)std::min<int64_t>(m.sinks, INT_MAX / 2) : 0;
     return launch(a, stream);
 }
 

@@ -38,6 +38,7 @@ constexpr int KS = DQ / T::KSTEP;            // K steps of the score product
 constexpr int ND = HD / T::DIMS;             // dim tiles of the output
 constexpr int NT = KT / T::ROWS;             // key subtiles
 constexpr int NP = NT * T::NS;               // weights a lane holds
+constexpr int NARROW_GROUP = 2;              // fragments that the narrow form reads together (4: spills, 5% slower)
 
 // the place in a tile of a lane's weight j, counted from its first
 __host__ __device__ constexpr int place0(int j) { return j / T::NS * T::ROWS + 8 * (j % T::NS >> 2) + (j & 3); }
@@ -82,22 +83,37 @@ __device__ __forceinline__ Tiles tiles_of(const WindowArgs &a, int fewest, int m
     }
     return s;
 }
-// Whether a query that sees `limit` keys without a window sees key k (`left`: limit, window's begin and
-// first keys, all counted from the lane's first key of the tile).
+// Which keys of a tile a query sees that without a window sees `limit`: those before `limit`, with a window
+// those of them from `begin` on or before `sinks`. All counted from the lane's first key of the tile.
 struct Left {
     int limit, begin, sinks;
     template <bool WINDOW>
     __device__ __forceinline__ bool sees(int k) const {
         return WINDOW ? k < limit && (k >= begin || k < sinks) : k < limit;
     }
+    // the same where the tile has none of the first keys: one comparison
+    template <bool WINDOW>
+    __device__ __forceinline__ bool sees_near(int k) const {
+        return WINDOW ? (uint32_t)(k - begin) < (uint32_t)(limit - begin) : k < limit;
+    }
 };
 __device__ __forceinline__ Left left_of(const PrefillArgs &, int limit, int k0) { return {limit - k0, 0, 0}; }
 __device__ __forceinline__ Left left_of(const WindowArgs &a, int limit, int k0) {
     return {limit - k0, limit - a.window - k0, a.sinks - k0};
 }
+// Whether a tile that begins at key k0 has some of the first keys.
+__device__ __forceinline__ bool has_sinks(const PrefillArgs &, int) { return false; }
+__device__ __forceinline__ bool has_sinks(const WindowArgs &a, int k0) { return k0 < a.sinks; }
 // The first tile from which on a query of a workgroup that sees `most` keys sees its tiles to their begin.
 __device__ __forceinline__ int first_whole(const PrefillArgs &, int) { return 0; }
 __device__ __forceinline__ int first_whole(const WindowArgs &a, int most) { return (max(0, most - a.window) + KT - 1) / KT; }
+
+// Whether no query sees a key of the tile that begins at k0, of queries the first of which sees `first` keys
+// without a window and the last `most`.
+__device__ __forceinline__ bool hidden(const PrefillArgs &, int k0, int, int most) { return k0 >= most; }
+__device__ __forceinline__ bool hidden(const WindowArgs &a, int k0, int first, int most) {
+    return k0 >= most || (k0 >= a.sinks && k0 + KT <= first - a.window);
+}
 
 // One row's partial: 128 sums; maxima and totals follow all rows' sums.
 __host__ __device__ inline int64_t split_floats(int64_t nq, int64_t heads) { return nq * heads * (HD + 2); }
@@ -140,7 +156,7 @@ __device__ __forceinline__ int find_tile(const PrefillArgs &a, int at, int &tile
 }
 
 // One pass over key tiles [t0, t1) of `span`. limit: keys that the lane's row sees (without a window);
-// first, most: the fewest and the most that any row of the workgroup sees. safe: non-finite values in tiles that some row sees in part
+// first, most: the fewest and the most that any row of the wave sees. safe: non-finite values in tiles that some row sees in part
 // reach only the rows that see them (see split_value).
 template <typename A>
 __device__ __forceinline__ void run_tiles(const A &a, uint8_t *lds, const u32x4_t (&qf)[KS], int head, int64_t k0row,
@@ -193,30 +209,57 @@ __device__ __forceinline__ void run_tiles(const A &a, uint8_t *lds, const u32x4_
         wait_vmcnt<0>();
         lds_barrier();                       // tile t is staged, the other stage is free
         if (t + 1 < t1) issue(t + 1);
+        const int at = span.at(t), k0 = at * KT;
+        if (hidden(a, k0, first, most)) continue;        // of all rows of the wave
         lds_u8 *st = ring + (t & 1) * STAGE_BYTES;
-        f32x16_t s[NT];
+        // Fragments are read from LDS a group ahead of the matrix instructions that take them, the first of the
+        // values before the softmax; the scheduling barriers keep the groups apart.
+        auto value = [&](int i, int x) __attribute__((always_inline)) {     // dim tile i, 16 keys x
+            u32x4_t f;
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-            for (int j = 0; j < T::NO; ++j) s[u][j] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                const u32x4_t kf = *(const lds_u32x4 *)(st + koff[k % 4] + u * (T::ROWS / 8) * (KSEG * 1024) +
-                                                        (k / 4) * 1024);
-                s[u] = T::mfma(kf, qf[k], s[u]);
+            for (int hh = 0; hh < 2; ++hh) {
+                lds_u8 *at = st + voff[i % 2][hh] + (i / 2) * 1024 + 2 * x * (VSEG * 1024);
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
+                f[2 * hh] = v[0];
+                f[2 * hh + 1] = v[1];
             }
+            return f;
+        };
+        constexpr int G = NARROW_GROUP, NK = KS * NT, NV = NP / 8 * ND;
+        static_assert(NK % G == 0 && NV % G == 0, "whole groups");
+        u32x4_t f[2][G];
+        auto key_group = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = g * G; e < g * G + G; ++e)
+                f[g & 1][e % G] = *(const lds_u32x4 *)(st + koff[e / NT % 4] + e % NT * (T::ROWS / 8) * (KSEG * 1024) + e / NT / 4 * 1024);
+        };
+        auto value_group = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = g * G; e < g * G + G; ++e) f[g & 1][e % G] = value(e % ND, e / ND);
+        };
+        f32x16_t s[NT];
+        key_group(0);
+#pragma unroll
+        for (int g = 0; g < NK / G; ++g) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (g + 1 < NK / G) key_group(g + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = g * G; e < g * G + G; ++e)
+                s[e % NT] = T::mfma(f[g & 1][e % G], qf[e / NT], e / NT ? s[e % NT] : f32x16_t{0.0f});
         }
+        value_group(0);
         float p[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) p[i] = s[i / T::NS][i % T::NS];
-        const int at = span.at(t), k0 = at * KT;
         const bool mixed = k0 + KT > first || (WINDOW && at < first_whole(a, most));
         const Left left = left_of(a, limit, k0 + T::place(0, grp));
-        if (mixed) {
+        if (mixed && has_sinks(a, k0)) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) p[i] = left.sees<WINDOW>(place0(i)) ? p[i] : -INFINITY;
+        } else if (mixed) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) p[i] = left.sees_near<WINDOW>(place0(i)) ? p[i] : -INFINITY;
         }
         float top = p[0];
 #pragma unroll
@@ -244,22 +287,15 @@ __device__ __forceinline__ void run_tiles(const A &a, uint8_t *lds, const u32x4_
         u32x4_t pf[NP / 8];
 #pragma unroll
         for (int i = 0; i < NP / 2; ++i) pf[i / 4][i % 4] = pack_bf16(p[2 * i], p[2 * i + 1]);
-        auto value = [&](int i, int x) {     // dim tile i, 16 keys x
-            u32x4_t f;
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                lds_u8 *at = st + voff[i % 2][hh] + (i / 2) * 1024 + 2 * x * (VSEG * 1024);
-                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
-                f[2 * hh] = v[0];
-                f[2 * hh + 1] = v[1];
-            }
-            return f;
-        };
         if (!(mixed && safe)) {
 #pragma unroll
-            for (int x = 0; x < NP / 8; ++x)
+            for (int g = 0; g < NV / G; ++g) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (g + 1 < NV / G) value_group(g + 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < ND; ++i) o[i] = T::mfma(value(i, x), pf[x], o[i]);
+                for (int e = g * G; e < g * G + G; ++e) o[e % ND] = T::mfma(f[g & 1][e % G], pf[e / ND], o[e % ND]);
+            }
         } else {
             u32x4_t see[NP / 8];
 #pragma unroll
@@ -388,8 +424,11 @@ __global__ __launch_bounds__(THREADS, 2) void latent_prefill_kernel(A a) {
     f32x16_t o[ND];
     float m, l;
     bool safe = false;
+    // the same of the wave's rows
+    const int r0 = tile * BM + uniform(wave) * T::ROWS;
+    const int wave_first = uniform(sees(min(r0, lq - 1))), wave_most = r0 < lq ? uniform(sees(min(r0 + T::ROWS, lq) - 1)) : 0;
     for (;;) {
-        run_tiles(a, lds, qf, head, k0, lk, span, t0, t1, limit, first, last, safe, o, m, l);
+        run_tiles(a, lds, qf, head, k0, lk, span, t0, t1, limit, wave_first, wave_most, safe, o, m, l);
         // a non-finite result where some rows see fewer keys than others: once more, key by key
         const bool some = std::is_same_v<A, WindowArgs> || t1 * KT > first;
         if (safe || !any_wave<WAVES>(not_finite(o) && some, lds)) break;
@@ -698,10 +737,13 @@ struct Plan {
     int64_t tiles;                           // most query tiles that nq rows in batch sequences can need
     int splits;
 };
-// keys: those that a workgroup takes, on average.
-Plan plan(int64_t nq, int64_t keys, int64_t batch, int64_t heads, int cus) {
+// With a window a wide workgroup takes 128 more keys that only half of its rows see, and the narrow form leaves
+// out a wave's tiles that none of its rows sees, so that longer windows are needed (16384 tokens x 16 heads, wide
+// and narrow in us: windows of 1024 265 and 228, of 2048 424 and 432, of 4096 738 and 801; 2 x 6000 tokens x 5
+// heads, window 2500 115 and 117). keys: those that a workgroup takes, on average.
+Plan plan(int64_t nq, int64_t keys, int64_t batch, int64_t heads, bool window, int cus) {
     Plan p;
-    p.wide = nq / batch >= 192 && keys >= 1024;
+    p.wide = nq / batch >= 192 && keys >= (window ? 2560 : 1024);
     const int bm = p.wide ? WIDE_BM : BM;
     p.tiles = std::min(nq, (nq + batch * (bm - 1)) / bm);
     // Splits of the keys: as many as fill the CUs (one wide workgroup each, or two narrow ones),
@@ -712,6 +754,9 @@ Plan plan(int64_t nq, int64_t keys, int64_t batch, int64_t heads, int cus) {
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({room, most, 32}));
     return p;
 }
+
+// A window as long as all keys hides none.
+int64_t window_of(int64_t nk, int64_t window) { return window >= nk ? 0 : window; }
 
 // Keys that a workgroup takes, on average; with a window what its rows see between them.
 int64_t keys_taken(int64_t nk, int64_t batch, int64_t window, int64_t sinks) {
@@ -724,12 +769,14 @@ int64_t keys_taken(int64_t nk, int64_t batch, int64_t window, int64_t sinks) {
 int64_t latent_prefill_workspace_bytes(int64_t nq, int64_t nk, int64_t batch, int64_t heads, int64_t window, int64_t sinks,
                                        int cus) {
     if (nq == 0 || batch == 0 || heads == 0) return 0;
-    const int s = plan(nq, keys_taken(nk, batch, window, sinks), batch, heads, cus).splits;
+    window = window_of(nk, window);
+    const int s = plan(nq, keys_taken(nk, batch, window, sinks), batch, heads, window > 0, cus).splits;
     return s == 1 ? 0 : s * split_floats(nq, heads) * (int64_t)sizeof(float);
 }
 
 hipError_t launch_latent_prefill(const skinny_latent_prefill_args &p, int64_t window, int64_t sinks, int cus,
                                  hipStream_t stream) {
+    window = window_of(p.nk, window);
     WindowArgs a;
     a.q = static_cast<const uint16_t *>(p.q);
     a.k = static_cast<const uint16_t *>(p.k);
@@ -753,7 +800,7 @@ hipError_t launch_latent_prefill(const skinny_latent_prefill_args &p, int64_t wi
     a.nk = p.nk;
     a.batch = (int)p.batch;
     a.heads = (int)p.heads;
-    const Plan how = plan(p.nq, keys_taken(p.nk, p.batch, window, sinks), p.batch, p.heads, cus);
+    const Plan how = plan(p.nq, keys_taken(p.nk, p.batch, window, sinks), p.batch, p.heads, window > 0, cus);
     a.tiles = (int)how.tiles;
     a.average = (int)(p.nk / p.batch);
     a.splits = how.splits;

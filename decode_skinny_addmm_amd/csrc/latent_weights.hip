@@ -161,7 +161,7 @@ __global__ __launch_bounds__(THREADS) void latent_key_weights_kernel(WeightArgs 
     };
     const uint16_t *from = a.cache;
     int to = 0;
-    bool live = false;                                   // there is an item to stage
+    uint64_t live = 0;                                   // there is an item to stage: all lanes, or none
     auto aim = [&](const Due &d, int slot) __attribute__((always_inline)) {
         if (d.kind == 2) {                               // ids outside the pool are clamped
             const int id = *(__attribute__((address_space(3))) const int32_t *)(words + slot % SLOTS * SLOT_BYTES + (lane >> 3) * 4);
@@ -172,15 +172,15 @@ __global__ __launch_bounds__(THREADS) void latent_key_weights_kernel(WeightArgs 
             from = a.q + ((int64_t)d.req * a.tokens + j) * a.q_row + h * a.q_head + chunk;
         }
         to = lds_address(ring + slot % STAGES * STAGE_BYTES + (wave >> 1) * (SEGS * 1024) + (wave & 1) * (PIECES * 1024));
-        live = d.kind != 0;
+        live = lanes_if(d.kind != 0);
     };
     // the item's pieces that go out with group `at` of `of` (both known when compiled)
     auto pieces_at = [&](int at, int of) __attribute__((always_inline)) {
-        if (0 * of / PIECES == at) load_lds_piece_if<0>(live, from, to);
-        if (1 * of / PIECES == at) load_lds_piece_if<1>(live, from, to);
-        if (2 * of / PIECES == at) load_lds_piece_if<2>(live, from, to);
-        if (3 * of / PIECES == at) load_lds_piece_if<3>(live, from, to);
-        if (4 * of / PIECES == at) load_lds_piece_if<4>(live && !(wave & 1), from, to);
+        if (0 * of / PIECES == at) load_lds_piece_in<0>(live, from, to);
+        if (1 * of / PIECES == at) load_lds_piece_in<1>(live, from, to);
+        if (2 * of / PIECES == at) load_lds_piece_in<2>(live, from, to);
+        if (3 * of / PIECES == at) load_lds_piece_in<3>(live, from, to);
+        if (4 * of / PIECES == at) load_lds_piece_in<4>(wave & 1 ? 0 : live, from, to);
     };
     static_assert(PIECES == 5, "five pieces");
     static_assert(2 * LOOK < SLOTS, "an item's word stays until it has been worked on");
