@@ -210,7 +210,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
     constexpr int PW = BLOCKS ? SEGS : SEGS + 1;         // loads a wave issues a stage: pieces, and a word of page ids
 
     Line<decltype(a), THREADS> line;
-    line.measure(a, sh);
+    line.measure(a, (int64_t)a.batch * a.groups * max(1, (a.max_pages * a.page + KT - 1) / KT), sh);
     const int grid = uniform(runs<S::MB>(a.grid, line.total));
     if ((int)blockIdx.x >= grid) return;
     int64_t lo = run_start(line.total, grid, blockIdx.x);
@@ -639,13 +639,14 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
             mu = m == -INFINITY ? 0.0f : m;
         };
         // moves the row's reference maximum to what the scores need
-        auto rescale = [&]() __attribute__((always_inline)) {
+        auto rescale = [&](bool first) __attribute__((always_inline)) {
             const float up = fmaxf(m, top);
             const float alpha = up == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - up);
             m = up;
             mu = m == -INFINITY ? 0.0f : m;
             l *= alpha;
             grow = false;
+            if (first) return;                           // the sums are 0 yet
 #pragma unroll
             for (int i = 0; i < S::ND; ++i) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -679,7 +680,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                     inspect(++t);
                 }
                 if (grow) {
-                    rescale();
+                    rescale(t == t0);
                     if (!odd && t + 1 < t1) continue;
                 }
                 all_weights();
@@ -703,7 +704,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                     add_values(st, std::false_type(), false);
                 } while (++t < t1);
                 if (t >= t1) break;
-                if (grow) rescale();
+                if (grow) rescale(t == t0);
                 if (!odd) {
                     scored = true;
                     continue;

@@ -5,6 +5,8 @@
 // An argument struct A names batch and groups, and request_tiles(a, i) the tiles of request i.
 #pragma once
 
+#include <climits>
+
 #include "latent.hpp"
 
 namespace skinny {
@@ -34,20 +36,49 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &t
 }
 
 // Where the line of tiles lies: its length, and for place x the request it belongs to and the place
-// of that request's first tile. Thread i counts requests i * per .. i * per + per - 1.
+// of that request's first tile. Up to 512 requests each wave works it out by itself, 32 bits allowing: lane i
+// counts requests i * per .. i * per + per - 1 (MEASURED). With more, thread i of the workgroup does.
 template <typename A, int THREADS>
 struct Line {
     static constexpr int WAVES = THREADS / 64;           // sh holds WAVES + 2 numbers
+    static constexpr int MOST_PER_LANE = 8;
     int64_t total, before;                   // of this thread's requests
-    int per;
-    __device__ __forceinline__ void measure(const A &a, int64_t *sh) {
-        per = (a.batch + THREADS - 1) / THREADS;
+    int per, own;
+    bool alone;
+    __device__ __forceinline__ int64_t count(const A &a, int first) const {
         int64_t v = 0;
-        for (int i = threadIdx.x * per; i < min(a.batch, (int)(threadIdx.x + 1) * per); ++i) v += request_tiles(a, i);
-        before = block_scan<THREADS>(v * a.groups, sh, total);
+        for (int i = first; i < min(a.batch, first + per); ++i) v += request_tiles(a, i);
+        return v * a.groups;
+    }
+    // most: an upper bound of total
+    __device__ __forceinline__ void measure(const A &a, int64_t most, int64_t *sh) {
+        alone = a.batch <= 64 * MOST_PER_LANE && most <= INT_MAX;
+        if (alone) {
+            const int lane = threadIdx.x & 63;
+            per = (a.batch + 63) / 64;
+            own = (int)count(a, lane * per);
+            const int sum = wave_scan(own);
+            before = sum - own;
+            total = __builtin_amdgcn_readlane(sum, 63);
+            return;
+        }
+        per = (a.batch + THREADS - 1) / THREADS;
+        before = block_scan<THREADS>(count(a, threadIdx.x * per), sh, total);
         total = uniform(total);
     }
     __device__ __forceinline__ void find(const A &a, int64_t x, int64_t *sh, int &req, int64_t &base) const {
+        if (alone) {
+            const int w = __builtin_ctzll(__ballot(before <= x && x < before + own));
+            base = __builtin_amdgcn_readlane((int)before, w);
+            req = w * per;
+            if (per == 1) return;
+            for (;;) {
+                const int64_t n = (int64_t)uniform(request_tiles(a, req)) * a.groups;
+                if (x < base + n || req + 1 == a.batch) return;
+                base += n;
+                ++req;
+            }
+        }
         int64_t at = before;
         for (int i = threadIdx.x * per; i < min(a.batch, (int)(threadIdx.x + 1) * per); ++i) {
             const int64_t n = (int64_t)request_tiles(a, i) * a.groups;

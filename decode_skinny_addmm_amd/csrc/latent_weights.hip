@@ -120,7 +120,7 @@ __global__ __launch_bounds__(THREADS) void latent_key_weights_kernel(WeightArgs 
     const int row = T::row(lane), grp = T::grp(lane);
 
     Line<WeightArgs, THREADS> line;
-    line.measure(a, sh);
+    line.measure(a, (int64_t)a.batch * ((a.columns + KT - 1) / KT + a.lead), sh);
     const int grid = (int)min((int64_t)a.grid, line.total);
     if ((int)blockIdx.x >= grid) return;
     const int64_t lo = run_start(line.total, grid, blockIdx.x), hi = run_start(line.total, grid, blockIdx.x + 1);
