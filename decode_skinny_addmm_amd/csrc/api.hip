@@ -501,7 +501,8 @@ skinny_status run_latent_keep(const skinny_latent_keep_args *a, void *stream) {
                          a->kept_stride > kMaxStride))
         return SKINNY_EINVAL;
     if (!a->lens || !a->counts || !a->new_lens || a->new_lens == a->lens || (!a->kept && a->most) ||
-        (a->max_pages > 0 && (!a->cache || !a->table)) || (!a->weights != !a->new_weights && a->columns))
+        (a->max_pages > 0 && (!a->cache || !a->table)) || (!a->weights != !a->new_weights && a->columns) ||
+        (a->weights && a->weights == a->new_weights))
         return SKINNY_EINVAL;
     if (a->weights && a->batch > 1 && (a->weights_stride < a->columns || a->weights_stride > kMaxStride ||
                                        a->new_weights_stride < a->columns || a->new_weights_stride > kMaxStride))

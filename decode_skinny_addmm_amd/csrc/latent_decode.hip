@@ -950,7 +950,8 @@ template <typename A>
 static hipError_t launch(const A &a, hipStream_t stream) {
     // a page's bytes, and a lane's from its request's first query, fit 31 bits
     const int64_t most = (int64_t)1 << 29;
-    const bool blocks = a.page % 8 == 0 && a.c_row < most / a.page && (a.pages <= 1 || a.c_page < most) && a.q_row < most / a.tokens && a.q_head < most / a.heads;
+    const bool blocks = a.page % 8 == 0 && a.c_row < most / a.page && (a.pages <= 1 || a.c_page < most) &&
+                        a.q_row < most / a.tokens && a.q_head < most / a.heads;
     switch (block_rows(a.rows)) {
         case 16: return launch_shape<Tile16, 1, 4>(a, blocks, stream);
         case 32: return launch_shape<Tile16, 2, 2>(a, blocks, stream);

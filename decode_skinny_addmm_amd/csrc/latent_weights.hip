@@ -32,7 +32,7 @@ constexpr int STAGE_BYTES = KT * DIM * 2;
 constexpr int WAVES = 8, THREADS = WAVES * 64;
 constexpr int PIECES = (SEGS + 1) / 2;       // two waves share 8 rows of a stage: 5 pieces and 4 (and one that loads nothing)
 constexpr int PW = PIECES + 1;               // loads a wave issues a stage: a word and pieces
-constexpr int SLOTS = 8, SLOT_BYTES = 128;    // 32 words each of so many stages: page ids of 8 rows, or 32 rows' log sums
+constexpr int SLOTS = 8, SLOT_BYTES = 128;   // 32 words each of so many stages: page ids of 8 rows, or 32 rows' log sums
 constexpr int KS = DIM / T::KSTEP;           // K steps
 constexpr float LEAD = 0.42f;                // what a query tile takes, in times of a tile of keys
 constexpr int AHEAD = 3;                     // fragments read ahead
@@ -185,8 +185,8 @@ __global__ __launch_bounds__(THREADS) void latent_key_weights_kernel(WeightArgs 
     static_assert(PIECES == 5, "five pieces");
     static_assert(2 * LOOK < SLOTS, "an item's word stays until it has been worked on");
     // Item n is worked on after step n, which takes the word of item n + 2 LOOK and aims at item n + LOOK, whose
-    // pieces go out between the matrix instructions that follow, to where item n - 1 was. Of the loads issued later than item n's there are those of LOOK - 1 items, each with a
-    // word.
+    // pieces go out between the matrix instructions that follow, to where item n - 2 was. Of the loads issued later
+    // than item n's there are those of LOOK - 1 items, each with a word.
     Due due[LOOK];
     {
         Due early[LOOK];

@@ -498,6 +498,11 @@ def latent_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, causal: bool = True
     return out, lse
 
 
+def _whole(name, value, least):
+    if not hasattr(value, "__index__") or value < least:
+        raise ValueError("%s must be a whole number of at least %d, got %s" % (name, least, value))
+
+
 def latent_tree_mask(parents, mask=None, depth=None, stream=None):
     """Rows of trees of drafted tokens (skinny_latent_tree_mask), for latent_tree_decode.
 
@@ -561,9 +566,8 @@ def latent_window_prefill(q, k, v, k_rot, cu_q, cu_k, scale: float, window: int,
     """Causal latent_prefill with a sliding window (skinny_latent_window_prefill_bf16): a query at position p of
     its sequence sees keys k <= p with k > p - window or k < sinks. The rest as in latent_prefill;
     workspace: latent_window_prefill_workspace(nq, nk, batch, heads, window, sinks). Returns (out, lse)."""
-    for name, value, least in (("window", window, 1), ("sinks", sinks, 0)):
-        if not hasattr(value, "__index__") or value < least:
-            raise ValueError("%s must be a whole number of at least %d, got %s" % (name, least, value))
+    _whole("window", window, 1)
+    _whole("sinks", sinks, 0)
     gpu, out, lse, workspace = _prefill_outputs(q, k, cu_q, out, lse, workspace, stream,
                                                 lib().skinny_latent_window_prefill_workspace,
                                                 "skinny_latent_window_prefill_workspace", window, sinks)
@@ -596,8 +600,7 @@ def latent_select(weights, lens, budget: int, sinks: int = 0, recent: int = 0, k
     gpu = _gpu_of("weights", weights)
     if weights.dim() != 2:
         raise ValueError("weights must be a tensor [batch, columns]")
-    if budget < 0:
-        raise ValueError("budget must not be negative, got %d" % budget)
+    _whole("budget", budget, 0)
     if kept is None:
         kept = _new((weights.shape[0], budget), torch.int32, weights.device, stream)
     if counts is None:

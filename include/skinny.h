@@ -494,7 +494,7 @@ SKINNY_API skinny_status skinny_latent_select(const skinny_latent_select_args *a
  * stay where they are) those numbers, counted from the first of them, to the places from there on, as after
  * a verified tree. new_lens[i] is the number of rows left. The numbers must rise; one that is smaller than its place
  * in the list, or is not a row of the request, leaves the row of its new place as it is. counts are clamped to
- * 0 .. min(most, rows there are). weights and new_weights (NULL both, or neither): new_weights[i, j] = the weight
+ * 0 .. min(most, rows there are). weights and new_weights (NULL both, or two arrays): new_weights[i, j] = the weight
  * of the key that row j holds now, 0 behind the last. The pages that rows move in must be the request's own.
  * Rows behind the last one kept are left as they are. Lengths and page ids are clamped as in decode.
  */

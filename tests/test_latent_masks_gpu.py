@@ -74,6 +74,57 @@ def test_tree_decode_cut_requests(sk):
     tree_case(sk, [9000], 4, 4, 64, seed=4)
 
 
+@pytest.mark.parametrize("page", [4, 12, 20])
+@pytest.mark.parametrize("heads,tokens", [(2, 3), (8, 4), (16, 4), (16, 8), (5, 30)])
+def test_tree_decode_pages_of_no_whole_groups(sk, heads, tokens, page):
+    """8 rows in a row lie in up to three pages; row shapes of 16, 32, 64 and 128, and groups of them."""
+    tree_case(sk, [700, tokens, 97, 0], heads, tokens, page, seed=page)
+    tree_case(sk, [700, tokens, 97, 301], heads, tokens, page, window=90, sinks=21, seed=page + 1, deep=True)
+
+
+@pytest.mark.parametrize("heads,tokens", [(2, 3), (16, 2), (16, 4), (16, 8)])
+def test_tree_decode_of_strided_rows(sk, heads, tokens):
+    """A cache whose rows and pages lie apart, queries that are a slice; then pages, rows and queries that lie so
+    far apart that their offsets pass 31 and 32 bits."""
+    g = gen(heads)
+    lens, rows = [333, tokens, 90], 3 * tokens
+    cache, table, n = paged(g, lens, 16)
+    q = normal(g, rows, heads, DIM)
+    parents = [random_parents(g, tokens) for _ in lens]
+    mask, _ = sk.latent_tree_mask(torch.tensor(parents, dtype=torch.int32, device="cuda"))
+    paths = [mref.ancestors(p) for p in parents]
+    apart = torch.full((cache.shape[0], 17, DIM + 16), math.nan, dtype=BF, device="cuda")[:, :16, :DIM]
+    apart.copy_(cache)
+    queries = torch.full((rows, heads + 1, DIM + 8), math.nan, dtype=BF, device="cuda")[:, 1:, :DIM]
+    queries.copy_(q)
+    out, lse = sk.latent_tree_decode(queries, apart, table.cuda(), n.cuda(), mask, SCALE)
+    seen = lambda i, m: mref.seen_of(m, tokens, above=paths[i][0])
+    mref.check_decode(out, lse, q, cache, table, n, SCALE, tokens, seen, "strided")
+    few, order = normal(g, 3, 16, DIM), torch.tensor([[2, 0, 1]] * 3, dtype=torch.int32)
+    short = torch.tensor([48, tokens, 20 + tokens], dtype=torch.int32)
+    queries = q.cuda()
+    for step, row in (((1 << 29) - 8, DIM), ((1 << 29) + 8, DIM), ((1 << 31) + 64, DIM + 8), (DIM + 8, (1 << 25) + 8)):
+        far = torch.empty(2 * step + 15 * row + DIM, dtype=BF, device="cuda").as_strided((3, 16, DIM), (step, row, 1))
+        far.copy_(few)
+        out, lse = sk.latent_tree_decode(queries, far, order.cuda(), short.cuda(), mask, SCALE)
+        mref.check_decode(out, lse, q, few, order, short, SCALE, tokens, seen, "far")
+        del far
+    step = (1 << 29) // tokens + 8 - (1 << 29) // tokens % 8
+    far = torch.empty((rows - 1) * step + heads * DIM, dtype=BF, device="cuda").as_strided((rows, heads, DIM), (step, DIM, 1))
+    far.copy_(q)
+    out, lse = sk.latent_tree_decode(far, apart, table.cuda(), n.cuda(), mask, SCALE)
+    mref.check_decode(out, lse, q, cache, table, n, SCALE, tokens, seen, "far queries")
+
+
+@pytest.mark.parametrize("batch", [511, 512, 513, 700])
+def test_masked_decode_of_many_requests(sk, batch):
+    """Around what each wave counts by itself, with empty requests and such shorter than their new tokens."""
+    rng = random.Random(batch)
+    lens = [rng.choice((0, 1, 2, 3, 31, 33, 70, 150)) for _ in range(batch)]
+    window_case(sk, lens, 4, 2, 16, 20, 5, seed=batch)
+    tree_case(sk, lens, 4, 3, 16, seed=batch)
+
+
 @pytest.mark.parametrize("heads,tokens,window,sinks", [(8, 5, 5, 0), (8, 5, 40, 3), (2, 17, 100, 64), (16, 8, 33, 1),
                                                        (1, 64, 64, 32), (8, 24, 500, 4), (4, 3, 10 ** 9, 5)])
 def test_tree_decode_windows(sk, heads, tokens, window, sinks):
@@ -194,6 +245,20 @@ def test_window_prefill(sk, lq, lk, heads, window, sinks):
 def test_window_prefill_long(sk, lq, lk, heads, window, sinks):
     """Both forms, tiles left out between the first keys and the window, split keys."""
     window_prefill_case(sk, lq, lk, heads, window, sinks, seed=window)
+
+
+@pytest.mark.parametrize("window,sinks", [(2560, 0), (2700, 4), (3000, 130), (2561, 600)])
+@pytest.mark.parametrize("lq,lk,heads", [([700], [4000], 2), ([3900], [3900], 1), ([200, 900, 300], [6100, 3600, 2700], 2),
+                                         ([257, 511], [7001, 5000], 3)])
+def test_window_prefill_of_long_windows(sk, lq, lk, heads, window, sinks):
+    """Windows long enough for the wide form."""
+    window_prefill_case(sk, lq, lk, heads, window, sinks, seed=window)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("lq,lk,heads,window", [([700], [4000], 2, 2700), ([3700], [3700], 1, 2600)])
+def test_long_windows_hide_anything(sk, lq, lk, heads, window, bad):
+    test_window_prefill_hidden_values_may_be_anything(sk, lq, lk, heads, window, bad)
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
@@ -338,6 +403,14 @@ def test_select_many_keys(sk, n):
     select_case(sk, [[round(x, 1) for x in r] for r in rows], n // 3, 0, 0)
 
 
+@pytest.mark.parametrize("n", [65535, 65536, 65537, 66000])
+def test_select_around_what_registers_hold(sk, n):
+    g = gen(n)
+    rows = [torch.exp(2 * torch.randn(m, generator=g)).tolist() for m in (n, 9)]
+    select_case(sk, rows, 3000 + n % 7, 4, 64)
+    select_case(sk, [[float(int(x)) for x in r] for r in rows], n - 5, 0, 0)
+
+
 def keep_case(sk, lens, kept, page, tokens=0, columns=None, seed=0, counts=None, most=None):
     """kept: a rising list a request."""
     print("keep", dict(lens=lens[:8], page=page, tokens=tokens, columns=columns), flush=True)
@@ -373,6 +446,26 @@ def test_keep(sk, page):
     keep_case(sk, lens, [list(range(n)) for n in lens], page, seed=2)                     # nothing moves
     keep_case(sk, lens, [list(range(n // 2, n)) for n in lens], page, columns=70, seed=3)  # everything by the same way
     keep_case(sk, lens, [[] for n in lens], page, columns=1, seed=4)
+
+
+@pytest.mark.parametrize("batch", [63, 64, 70])
+def test_keep_of_many_requests(sk, batch):
+    """Lists longer than what a workgroup moves at once, in requests of every length."""
+    g = gen(batch)
+    lens = [int(x) for x in torch.randint(0, 1900, (batch,), generator=g)]
+    lens[:4] = 1900, 0, 1, 64
+    some = lambda n, m: sorted(torch.randperm(n, generator=g)[:m].tolist())
+    keep_case(sk, lens, [some(n, n * 3 // 4) for n in lens], 16, columns=1900, seed=1)
+    keep_case(sk, lens, [list(range(n // 3, n)) for n in lens], 48, columns=1000, seed=2)
+    keep_case(sk, lens, [list(range(n)) for n in lens], 16, seed=3)
+
+
+@pytest.mark.parametrize("most", [63, 64, 65])
+def test_keep_around_short_lists(sk, most):
+    g = gen(most)
+    lens = [700, 64, 65, 66, 63, 0]
+    some = lambda n, m: sorted(torch.randperm(n, generator=g)[:min(n, m)].tolist())
+    keep_case(sk, lens, [some(n, most) for n in lens], 16, columns=700, most=most)
 
 
 def test_keep_after_a_tree(sk):
@@ -534,7 +627,7 @@ def test_binding_refuses(sk):
             ("rows", lambda: sk.latent_key_weights(q, cache, table, n, lse, w, SCALE, tokens=2)),
             ("scale", lambda: sk.latent_key_weights(q, cache, table, n, lse, w, 0.0, tokens=3)),
             ("overlap", lambda: sk.latent_key_weights(q, cache, table, n, w.flatten()[:24].view(6, 4), w, SCALE, tokens=3)),
-            ("budget", lambda: sk.latent_select(w, n, -1)), ("budget", lambda: sk.latent_select(w, n, 5, sinks=3, recent=3)),
+            ("budget", lambda: sk.latent_select(w, n, -1)), ("budget", lambda: sk.latent_select(w, n, 2.5)), ("budget", lambda: sk.latent_select(w, n, 5, sinks=3, recent=3)),
             ("recent", lambda: sk.latent_select(w, n, 5, recent=-1)), ("lens", lambda: sk.latent_select(w, n.long(), 5)),
             ("overlap", lambda: sk.latent_select(w, n, 10, counts=n)),
             ("overlap", lambda: sk.latent_keep(cache, table, n, kept, counts, new_lens=n)),

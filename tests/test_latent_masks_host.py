@@ -39,7 +39,7 @@ def select_args(**over):
 
 
 def keep_args(**over):
-    d = dict(cache=P, table=P, lens=P, kept=P, counts=P, new_lens=P + 64, weights=P, new_weights=P, cache_page_stride=576 * 16,
+    d = dict(cache=P, table=P, lens=P, kept=P, counts=P, new_lens=P + 64, weights=P, new_weights=P + 64, cache_page_stride=576 * 16,
              cache_row_stride=576, table_stride=9, kept_stride=5, weights_stride=100, new_weights_stride=100, batch=2,
              tokens=0, most=5, pages=20, page=16, max_pages=9, columns=100, latent=512, rope=64)
     d.update(over)
@@ -100,7 +100,8 @@ def test_select_refuses(L, want, over):
     (EINVAL, dict(batch=-1)), (EINVAL, dict(tokens=-1)), (EINVAL, dict(most=-1)), (EINVAL, dict(page=0)), (EINVAL, dict(pages=0)),
     (EINVAL, dict(columns=-1)), (ENOTSUP, dict(latent=256)), (ENOTSUP, dict(rope=0)), (EINVAL, dict(cache=None)),
     (EINVAL, dict(table=None)), (EINVAL, dict(lens=None)), (EINVAL, dict(kept=None)), (EINVAL, dict(counts=None)),
-    (EINVAL, dict(new_lens=None)), (EINVAL, dict(new_lens=P)), (EINVAL, dict(weights=None)), (EINVAL, dict(new_weights=None)),
+    (EINVAL, dict(new_lens=None)), (EINVAL, dict(new_lens=P)), (EINVAL, dict(new_weights=P)),
+    (EINVAL, dict(weights=None)), (EINVAL, dict(new_weights=None)),
     (EALIGN, dict(cache=P + 8)), (EALIGN, dict(kept=P + 2)), (EALIGN, dict(cache_page_stride=576 * 16 + 4)),
     (EINVAL, dict(cache_row_stride=568)), (EINVAL, dict(cache_page_stride=576)), (EINVAL, dict(table_stride=8)),
     (EINVAL, dict(kept_stride=4)), (EINVAL, dict(weights_stride=99)), (EINVAL, dict(new_weights_stride=99)),
