@@ -288,9 +288,11 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
 // takes one piece of all of a request's rows, in chunks in the order of their places, of which it reads
 // all rows before it writes one. Places rise and no row lies before its place, so what a chunk writes no
 // later one reads. Pieces of 384 bytes, and 512 rows a chunk (196 KB on its way a workgroup), where there are
-// requests enough to fill the chip with them; otherwise 128 bytes and 1024 rows (64 requests of 4096 rows 90 and
-// 100 us, 4 of 2048 rows 23 and 12). The bytes bound it, which are not read again soon (past the caches: 94 us
-// where it was 100).
+// requests enough to fill the chip with them; otherwise 128 bytes and 2048 rows, 262 KB, half of a CU's registers
+// (64 requests, of 4096 kept rows each 123 and 127 us, of 500 12.2 and 14.9; 16 requests 63 and 31, 6.8 and 5.5;
+// with 1024 rows a chunk 4 requests of 2048 10.8 us where it is 9.0). Many requests the bytes bound, which are not
+// read again soon (past the caches: 94 us where it was 100; 64 requests of which most drop some 110 of 4200 rows 86
+// us, 390 MB read and written, 4.5 TB/s), few of them the chain of a chunk's loads: list, page ids, rows, stores.
 constexpr int DIM = 576;
 constexpr int KEEP_TURNS = 16;               // rows that a lane has on their way
 constexpr int KEEP_WEIGHTS = 2048;           // weights a workgroup
@@ -440,7 +442,7 @@ hipError_t launch_latent_keep(const skinny_latent_keep_args &p, hipStream_t stre
         hipLaunchKernelGGL((latent_keep_kernel<24, 768>), dim3((unsigned)(DIM / 8 / 24 + wblocks), (unsigned)p.batch), dim3(768), 0,
                            stream, a);
     else
-        hipLaunchKernelGGL((latent_keep_kernel<8, 512>), dim3((unsigned)(DIM / 8 / 8 + wblocks), (unsigned)p.batch), dim3(512), 0,
+        hipLaunchKernelGGL((latent_keep_kernel<8, 1024>), dim3((unsigned)(DIM / 8 / 8 + wblocks), (unsigned)p.batch), dim3(1024), 0,
                            stream, a);
     return hipGetLastError();
 }
