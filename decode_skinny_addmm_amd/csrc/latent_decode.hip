@@ -16,10 +16,14 @@
 //   * 4 waves as WR row groups x WD groups of latent dims: each wave computes the whole scores
 //     of its rows (repeated by the WD waves: matrix time is spare, and no scores cross waves)
 //     and its dims of the output, so the only barrier is the ring's.
-// Measured: one request of 131071 keys x 32 heads 32 us (151 MB, 4.8 TB/s; its inner loop 6 TB/s) and 7
-// for the join; 96 requests of about 4000 keys x 128 heads 132 us (485 MB read, 92 MB of partials
+// With a window the line holds only the tiles that a request's rows see between them; with a tree of new tokens
+// the tiles that hold them are masked by the tokens' words, which lie in LDS (see seen_keys).
+// Measured: one request of 131071 keys x 32 heads 34 us (151 MB, 4.4 TB/s; its inner loop 6 TB/s) and 7
+// for the join; 96 requests of about 4000 keys x 128 heads 125 us (485 MB read, 92 MB of partials
 // written) and 22 for the join; 64 requests of 3000 keys x 64 heads 55 us (240 MB read) and 7.6 for the
-// join. With 128 rows the matrix instructions take 40% of a wave's time (33% of the kernel's, with its
+// join; windows of 4096 of 64 requests x 16 heads 61 us (311 MB read, 5.1 TB/s) and 4.8; trees of 24 tokens x 8
+// heads over 32 requests of 4096 keys 92 and 14, of 64 x 16 over 8 of 8000 146 and 19; a tree of 7 x 8 over 500
+// keys 10 and 4. With 128 rows the matrix instructions take 40% of a wave's time (35% of the kernel's, with its
 // start and its uneven end), and neither they nor memory bound it alone: in this layout of one wave a
 // SIMD, registers full of sums and queries leave no room to run a tile's softmax beside the next one's
 // products.
@@ -194,7 +198,8 @@ __device__ __forceinline__ void pieces_at(int at, int of, const Source &p) {
 // MASKED: of the keys before its own, a row sees those of a mask, held a tile as 32 bits.
 // BLOCKS: pages are whole groups of 8 rows, so that the 8 keys that a wave stages of a tile lie in one page, whose
 // id and address are worked out once a wave, by the scalar unit. A step's cursor and addresses take the wave
-// some 950 cycles otherwise, and MEASURED with them, of a tile of 128 rows' 5300.
+// some 970 cycles otherwise, and 775 so, of a tile of 128 rows' 4300 (8 requests of 8000 keys x 1024 rows: 157 and 148
+// us).
 template <typename T, int WR, int WD, bool MASKED, bool BLOCKS>
 __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional_t<MASKED, MaskedArgs, DecodeArgs> a) {
     typedef Shape<T, WR, WD> S;
@@ -304,7 +309,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
     };
     auto aim_block = [&](const BlockDue &d, int slot) __attribute__((always_inline)) {
         if (d.kind == 2) {                               // ids outside the pool are clamped
-            src.base = a.cache + (uint64_t)(uint32_t)min(max(d.id, 0), a.pages - 1) * (uint32_t)a.c_page + (uint32_t)d.row * (uint32_t)a.c_row;
+            src.base = a.cache + (uint64_t)(uint32_t)min(max(d.id, 0), a.pages - 1) * (uint32_t)a.c_page +
+                       (uint32_t)d.row * (uint32_t)a.c_row;
             if (src.kind != 2) {
                 const int x = own_lane();
                 src.own = ((uint32_t)(x >> 3) * (uint32_t)a.c_row + chunk_of(x)) * 2;
@@ -428,7 +434,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
         for (int j = 0; j < VA; ++j)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
-                at[j][hh] = place_of(from, (vbase ^ (j * T::DIMS * 2) ^ (HALF == 8 ? hh * 16 : 0)) + hh * (HALF / 8) * (SEGS * 1024));
+                at[j][hh] = place_of(from, (vbase ^ (j * T::DIMS * 2) ^ (HALF == 8 ? hh * 16 : 0)) +
+                                               hh * (HALF / 8) * (SEGS * 1024));
     };
 
     constexpr int NT = KT / T::ROWS;                     // key subtiles: 1 or 2
@@ -521,7 +528,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
         for (int e = 0; e < S::VAHEAD; ++e) vf[e] = value(e / XS, e % XS);
         static_for<NV>([&](auto e) __attribute__((always_inline)) {
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (e + S::VAHEAD < NV) vf[(e + S::VAHEAD) % (S::VAHEAD + 1)] = value((e + S::VAHEAD) / XS, (e + S::VAHEAD) % XS);
+            constexpr int then = e + S::VAHEAD;
+            if constexpr (then < NV) vf[then % (S::VAHEAD + 1)] = value(then / XS, then % XS);
             __builtin_amdgcn_sched_barrier(0);
             o[e / XS] = T::mfma(vf[e % (S::VAHEAD + 1)], pf[e % XS], o[e / XS]);
             if constexpr (!S::FLOW) pieces_at<BLOCKS>(NK + e, ISSUES, src);
@@ -625,8 +633,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
 #pragma unroll
                 for (int i = 0; i < T::NS; ++i) {
                     const float x = s[i / T::NO][i % T::NO];
-                    const bool seen = MASKED ? keys >> T::place(i, 0) & 1 : t * KT + T::place(i, grp) < limit, fin = finite_f32(x);
-                    odd |= !fin;                         // so is the key's row, or a query
+                    const bool seen = MASKED ? keys >> T::place(i, 0) & 1 : t * KT + T::place(i, grp) < limit;
+                    odd |= !finite_f32(x);               // so is the key's row, or a query
                     s[i / T::NO][i % T::NO] = seen ? x : -INFINITY;
                 }
                 odd = __any(odd);
@@ -750,7 +758,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                     }
                 }
             }
-        } else {
+        } else if (r < a.rows) {                         // no partials of rows that repeat the last
             float *part = a.work + (2 * (int64_t)blockIdx.x + (leading ? 0 : 1)) * part_floats<S::MB>();
             f32x4_t *ps = reinterpret_cast<f32x4_t *>(part) + wave * (S::ND * S::NO4 * 64) + lane;
 #pragma unroll
@@ -781,7 +789,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
 // unit's partials further and meet in LDS; each lane asks for 4 partials at once. With few units the
 // latency of these loads bounds it (256 partials of 32 rows, 17 MB: 7.0 us, of which the launch and the
 // look-up of the cuts are most; 8.5 with whole waves on a partial), with many their bytes
-// (350 partials of 128 rows, 92 MB: 22 us, 4.7 TB/s).
+// (350 partials of 128 rows, 92 MB: 22 us, 4.7 TB/s; 8 of them at once gain nothing there and cost small joins 1
+// us).
 template <typename T, int WR, int WD, int WP, int PL>
 __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(DecodeArgs a) {
     typedef Shape<T, WR, WD> S;
@@ -818,12 +827,14 @@ __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(Dec
     auto partial = [&](int j) {
         return a.work + (j == 0 ? (int64_t)cut.x : 2 * (int64_t)(b0 + j)) * part_floats<S::MB>();
     };
-    for (int j = turn; j < pieces; j += 4 * TURNS) {
+    const int r = g * S::MB + row;
+    for (int j = r < a.rows ? turn : pieces; j < pieces; j += 4 * TURNS) {
         float pm[4], pl[4];
         f32x4_t po[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const float *part = partial(min(j + u * TURNS, pieces - 1));
+            if (j + u * TURNS >= pieces) break;
+            const float *part = partial(j + u * TURNS);
             pm[u] = part[(int64_t)S::MB * L + row];
             pl[u] = part[(int64_t)S::MB * (L + 1) + row];
             po[u] = reinterpret_cast<const f32x4_t *>(part)[at];
@@ -850,7 +861,6 @@ __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(Dec
     } else if (turn) {
         return;
     }
-    const int r = g * S::MB + row;
     if (r >= a.rows) return;
     const int64_t qr = (int64_t)req * a.tokens + r / a.heads;
     const int h = r % a.heads;

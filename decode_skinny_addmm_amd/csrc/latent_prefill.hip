@@ -11,10 +11,14 @@
 // workgroups share a CU, so that one's softmax runs beside the other's matrix instructions.
 // Where the queries are too few to fill the chip, a row's keys are split over several
 // workgroups and their partial sums joined by a second kernel. Long sequences go to the wide form
-// below. Measured: 6 prompts of 217 .. 1294 tokens x 32 heads 72 us (144 MB at least: 2 TB/s, 480
-// TFLOP/s; not causal 103 us, 670 TFLOP/s), 16 prompts of about 256 42 us (3.6 TB/s), one prompt of 129 x
-// 8 heads 9.5 us. Beside its matrix instructions (27% of the cycles with the 6 prompts) a tile waits for
-// all its loads, and each matrix instruction for its fragment from LDS, which is not read ahead as in the wide form.
+// below. With a window the tiles are those of the first keys and those from the first row's window on, and a
+// wave leaves out the ones that none of its 32 rows sees.
+// Measured: 6 prompts of 217 .. 1294 tokens x 32 heads 70 us (144 MB at least: 2 TB/s, 490 TFLOP/s), one prompt
+// of 129 x 8 heads 9.2 us; windows of 500 of 6 prompts of about 1500 x 32 heads 98 us (218 MB at least, 470
+// TFLOP/s), of 1024 of one of 16384 x 16 heads 222 us (752 TFLOP/s; matrix cores busy 38% of the cycles at 2.1
+// GHz). Four rounds of workgroups begin with queries and a first tile that nothing hides (10 us of a workgroup's
+// 55 there) and end with 4 us of stores; a tile's matrix instructions and its softmax take about as long, and two
+// waves a SIMD overlap them in part. Tiles of 32 keys lose 5%; three workgroups a CU of them spill (222 -> 550 us).
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -38,7 +42,8 @@ constexpr int KS = DQ / T::KSTEP;            // K steps of the score product
 constexpr int ND = HD / T::DIMS;             // dim tiles of the output
 constexpr int NT = KT / T::ROWS;             // key subtiles
 constexpr int NP = NT * T::NS;               // weights a lane holds
-constexpr int NARROW_GROUP = 2;              // fragments that the narrow form reads together (4: spills, 5% slower)
+// fragments that the narrow form reads together (6 windowed prompts: 106 us, 111 with 4, 175 with 8, which spills)
+constexpr int NARROW_GROUP = 2;
 
 // the place in a tile of a lane's weight j, counted from its first
 __host__ __device__ constexpr int place0(int j) { return j / T::NS * T::ROWS + 8 * (j % T::NS >> 2) + (j & 3); }

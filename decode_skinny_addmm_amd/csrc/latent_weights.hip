@@ -13,6 +13,12 @@
 //     run goes by chunks of up to 8 tiles of one request.
 //   * Everything comes through one ring of LDS stages of 36 KB: a chunk's key tiles, each taken
 //     out by its wave, then the query tiles, which all waves compute on. Two stages are in flight.
+// Measured: 64 requests of 4000 .. 12000 keys x 16 rows 107 us (614 MB read, 5.8 TB/s), 2 of about 16000 x
+// 1024 rows 47 us in a row of calls (34.6 GFLOP at least, 735 TFLOP/s; 55 alone, matrix cores busy 25% of the
+// cycles): 1000 tiles of keys over 256 workgroups are runs of 4, each with the 32 query tiles behind it, and a
+// step's barrier and addresses are not hidden by two waves a SIMD that a barrier keeps in step. Addresses of
+// whole blocks by the scalar unit, as in latent_decode.hip, are slower here (137 and 56 us), and so are 16 x 16
+// matrix instructions (58).
 #include <algorithm>
 #include <type_traits>
 
@@ -34,8 +40,9 @@ constexpr int PIECES = (SEGS + 1) / 2;       // two waves share 8 rows of a stag
 constexpr int PW = PIECES + 1;               // loads a wave issues a stage: a word and pieces
 constexpr int SLOTS = 8, SLOT_BYTES = 128;   // 32 words each of so many stages: page ids of 8 rows, or 32 rows' log sums
 constexpr int KS = DIM / T::KSTEP;           // K steps
-constexpr float LEAD = 0.42f;                // what a query tile takes, in times of a tile of keys
-constexpr int AHEAD = 3;                     // fragments read ahead
+constexpr float LEAD = 0.42f;                // what a query tile takes, in times of a tile of keys (30 requests of 2000 ..
+                                             // 4000 keys x 512 rows 72 us, 90 with none, 82 with twice as much)
+constexpr int AHEAD = 3;                     // fragments read ahead (2 and 4 take as long)
 
 struct WeightArgs {
     const uint16_t *q;
@@ -138,7 +145,8 @@ __global__ __launch_bounds__(THREADS) void latent_key_weights_kernel(WeightArgs 
     lds_u8 *words = ring + STAGES * STAGE_BYTES + wave * (SLOTS * SLOT_BYTES);
     // staging: waves 2b and 2b + 1 take rows 8b .. 8b + 7 of a tile, lane l row l / 8; the first of them
     // the row's pieces 0 .. 4, the second 5 .. 8
-    const int first_own = 8 * (wave >> 1), own = first_own + (lane >> 3), chunk = ((lane & 7) ^ swz(own)) * 8 + (wave & 1) * (PIECES * 64);
+    const int first_own = 8 * (wave >> 1), own = first_own + (lane >> 3);
+    const int chunk = ((lane & 7) ^ swz(own)) * 8 + (wave & 1) * (PIECES * 64);
     auto plan = [&](int slot) __attribute__((always_inline)) {
         Due d{0, c.req, 0};
         const void *word = a.table;
@@ -164,7 +172,8 @@ __global__ __launch_bounds__(THREADS) void latent_key_weights_kernel(WeightArgs 
     uint64_t live = 0;                                   // there is an item to stage: all lanes, or none
     auto aim = [&](const Due &d, int slot) __attribute__((always_inline)) {
         if (d.kind == 2) {                               // ids outside the pool are clamped
-            const int id = *(__attribute__((address_space(3))) const int32_t *)(words + slot % SLOTS * SLOT_BYTES + (lane >> 3) * 4);
+            typedef __attribute__((address_space(3))) const int32_t lds_i32;
+            const int id = *(lds_i32 *)(words + slot % SLOTS * SLOT_BYTES + (lane >> 3) * 4);
             const int place = d.row - page_of(a, d.row) * a.page;
             from = a.cache + (int64_t)min(max(id, 0), a.pages - 1) * a.c_page + (int64_t)place * a.c_row + chunk;
         } else if (d.kind == 1) {
@@ -183,7 +192,9 @@ __global__ __launch_bounds__(THREADS) void latent_key_weights_kernel(WeightArgs 
         if (4 * of / PIECES == at) load_lds_piece_in<4>(wave & 1 ? 0 : live, from, to);
     };
     static_assert(PIECES == 5, "five pieces");
-    static_assert(2 * LOOK < SLOTS, "an item's word stays until it has been worked on");
+    // two waves that share a tile work at step n on item n - 1, and on the weights of item n - 3
+    static_assert(LOOK + 2 <= STAGES, "a stage is not filled while it is worked on");
+    static_assert(2 * LOOK + 4 <= SLOTS, "an item's word stays until it has been worked on");
     // Item n is worked on after step n, which takes the word of item n + 2 LOOK and aims at item n + LOOK, whose
     // pieces go out between the matrix instructions that follow, to where item n - 2 was. Of the loads issued later
     // than item n's there are those of LOOK - 1 items, each with a word.
@@ -230,7 +241,7 @@ __global__ __launch_bounds__(THREADS) void latent_key_weights_kernel(WeightArgs 
     u32x4_t kf[KS];
     while (todo.more()) {
         // A chunk of half as many tiles as waves or fewer: two waves of a SIMD share a tile, and of the query
-        // tiles, which then come two a turn, each takes one
+        // tiles, which then come two a turn, each takes one (2 requests of 16000 keys x 1024 rows 62 -> 55 us)
         const int share = todo.keys <= WAVES / 2 ? 2 : 1;
         const int mine = share == 2 ? wave % (WAVES / 2) : wave, turn = share == 2 ? wave / (WAVES / 2) : 0;
         for (int x = 0; x < todo.keys; ++x) {

@@ -497,6 +497,7 @@ SKINNY_API skinny_status skinny_latent_select(const skinny_latent_select_args *a
  * 0 .. min(most, rows there are). weights and new_weights (NULL both, or two arrays): new_weights[i, j] = the weight
  * of the key that row j holds now, 0 behind the last. The pages that rows move in must be the request's own.
  * Rows behind the last one kept are left as they are. Lengths and page ids are clamped as in decode.
+ * SKINNY_ENOTSUP: other latents or rotated numbers than 512 and 64, a batch above 65535, counts as in decode.
  */
 typedef struct skinny_latent_keep_args {
     void *cache;                    /* [pages, page, 576] */
