@@ -19,10 +19,10 @@
 // With a window the line holds only the tiles that a request's rows see between them; with a tree of new tokens
 // the tiles that hold them are masked by the tokens' words, which lie in LDS (see seen_keys).
 // Measured: one request of 131071 keys x 32 heads 34 us (151 MB, 4.4 TB/s; its inner loop 6 TB/s) and 7
-// for the join; 96 requests of about 4000 keys x 128 heads 125 us (485 MB read, 92 MB of partials
+// for the join; 96 requests of about 4000 keys x 128 heads 119 us (485 MB read, 92 MB of partials
 // written) and 22 for the join; 64 requests of 3000 keys x 64 heads 55 us (240 MB read) and 7.6 for the
 // join; windows of 4096 of 64 requests x 16 heads 61 us (311 MB read, 5.1 TB/s) and 4.8; trees of 24 tokens x 8
-// heads over 32 requests of 4096 keys 92 and 14, of 64 x 16 over 8 of 8000 146 and 19; a tree of 7 x 8 over 500
+// heads over 32 requests of 4096 keys 84 and 14, of 64 x 16 over 8 of 8000 138 and 16; a tree of 7 x 8 over 500
 // keys 10 and 4. With 128 rows the matrix instructions take 40% of a wave's time (35% of the kernel's, with its
 // start and its uneven end), and neither they nor memory bound it alone: in this layout of one wave a
 // SIMD, registers full of sums and queries leave no room to run a tile's softmax beside the next one's
@@ -59,7 +59,9 @@ struct DecodeArgs {
     float *work;                             // partial sums: see part_floats
     int2 *cuts;                              // a unit (request and row group): its first partial, its last workgroup
     int batch, tokens, heads, pages, page, max_pages;
-    int rows, groups, grid;                  // rows a request, row groups a request, workgroups
+    int rows, all_groups, grid;              // rows a request, row groups a request, workgroups
+    int groups, side;                        // row groups of a request in the line, and side by side: see shared_run
+    int lead;                                // see request_tiles
     uint32_t page_mul, head_mul;             // see quotient
     int page_shift, head_shift;
     float c;                                 // scale * log2(e)
@@ -109,8 +111,12 @@ __device__ __forceinline__ Tiles tiles_of(const MaskedArgs &a, int len) {
     }
     return s;
 }
+// What a unit (request and row group) takes of the line: its tiles, and ahead of them `lead` places of no work, so
+// that a run that ends one unit and begins the next, which loads queries and leaves partials twice, is given
+// fewer tiles. (8 requests x 1024 rows x 8000 keys: runs of 57 tiles in one unit took 121 to 129 us, in two 132
+// to 141.)
 template <typename A>
-__device__ __forceinline__ int request_tiles(const A &a, int i) { return tiles_of(a, request_len(a, i)).count; }
+__device__ __forceinline__ int request_tiles(const A &a, int i) { return tiles_of(a, request_len(a, i)).count + a.lead; }
 
 // Bits b of a tile of keys that starts at k0 with k0 + b < x.
 __device__ __forceinline__ uint32_t keys_below(int x, int k0) {
@@ -133,6 +139,21 @@ __device__ __forceinline__ int runs(int most, int64_t total) {
     return min(grid, max(1, (int)(FACTOR * sqrtf((float)total))));
 }
 
+// Row groups of a request read the same keys. Where they divide the chip well they are not behind each other in
+// the line but side by side: the line holds a request's tiles once, and each of its runs is taken by `side`
+// workgroups, one a group, at the same time and on one XCD, whose L2 serves all but the first. (Workgroups go to
+// the XCDs in turn.) 8 groups read 90 MB where it was 575, 2 groups 162 where it was 330, which takes them from 91 to
+// 88 us; 8 groups as long as before.
+struct SharedRun {
+    int run, own;                            // the run, the row group (of those side by side); run -1: none
+};
+__device__ __forceinline__ SharedRun shared_run(int block, int grid, int side) {
+    if (side == 1) return {block < grid ? block : -1, 0};
+    const int all = grid * side, per = (all + 7) / 8, p = (block & 7) * per + (block >> 3);
+    if (block >> 3 >= per || p >= all) return {-1, 0};
+    return {p / side, p % side};
+}
+
 template <typename T, int WR, int WD>
 struct Shape {
     static constexpr int MB = T::ROWS * WR;              // rows a workgroup
@@ -153,15 +174,19 @@ struct Shape {
 struct Cursor {
     int req, g, len, t, t0, end;             // unit; next item: query tile t + QT if t < 0, else key tile t
     Tiles tiles;
-    int64_t left;                            // key tiles of the run from this unit on
+    int taken;                               // places of the run in this unit
+    int64_t left;                            // places of the run from this unit on
     bool more;
+    // from place `first` of the unit on
     template <typename A>
     __device__ __forceinline__ void enter(const A &a, int first, int qt) {
         len = uniform_len(a, req);
         tiles = tiles_of(a, len);
         t = -qt;
-        t0 = first;
-        end = (int)min((int64_t)tiles.count, first + left);
+        taken = (int)min((int64_t)(tiles.count + a.lead - first), left);
+        t0 = max(0, first - a.lead);
+        end = first + taken - a.lead;
+        more = end > 0;                      // a run may end with places of no work
     }
 };
 // An item whose load is due: this lane's row (of the request's queries, or of its cache page).
@@ -215,11 +240,14 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
     constexpr int PW = BLOCKS ? SEGS : SEGS + 1;         // loads a wave issues a stage: pieces, and a word of page ids
 
     Line<decltype(a), THREADS> line;
-    line.measure(a, (int64_t)a.batch * a.groups * max(1, (a.max_pages * a.page + KT - 1) / KT), sh);
-    const int grid = uniform(runs<S::MB>(a.grid, line.total));
-    if ((int)blockIdx.x >= grid) return;
-    int64_t lo = run_start(line.total, grid, blockIdx.x);
-    const int64_t hi = run_start(line.total, grid, blockIdx.x + 1);
+    line.measure(a, (int64_t)a.batch * a.groups * (max(1, (a.max_pages * a.page + KT - 1) / KT) + a.lead), sh);
+    const int grid = uniform(max(1, runs<S::MB>(a.grid, line.total * a.side) / a.side));      // runs
+    const SharedRun mine = shared_run(blockIdx.x, grid, a.side);
+    if (mine.run < 0) return;
+    // me: the number of its partials
+    const int own_group = uniform(mine.own), run0 = own_group * grid, me = uniform(run0 + mine.run);
+    int64_t lo = run_start(line.total, grid, mine.run);
+    const int64_t hi = run_start(line.total, grid, mine.run + 1);
     int req;
     int64_t base;
     line.find(a, lo, sh, req, base);
@@ -237,18 +265,18 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
     Cursor c;
     c.req = req;
     c.left = hi - lo;
-    c.more = true;
     {
-        const int tiles = tiles_of(a, uniform_len(a, req)).count;
-        c.g = (int)((lo - base) / tiles);
-        c.enter(a, (int)((lo - base) % tiles), QT);
+        const int places = tiles_of(a, uniform_len(a, req)).count + a.lead;
+        c.g = (int)((lo - base) / places);
+        c.enter(a, (int)((lo - base) % places), QT);
     }
+    if (!c.more) return;
     // past the unit's query tiles, its key tiles, or into the next unit
     auto advance = [&]() __attribute__((always_inline)) {
         if (c.t < 0) {
             if (++c.t == 0) c.t = c.t0;
         } else if (++c.t == c.end) {
-            c.left -= c.end - c.t0;
+            c.left -= c.taken;
             c.more = c.left > 0;
             if (c.more) {
                 if (++c.g == a.groups) {
@@ -297,7 +325,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                 same = c.t + 1 < c.end;
             } else {
                 if (c.t == -QT) enter_block();
-                d.row = c.g * S::MB + (c.t + QT) * KT + 8 * wave;
+                d.row = (own_group + c.g) * S::MB + (c.t + QT) * KT + 8 * wave;
                 d.kind = 1;
             }
             if (same) ++c.t;
@@ -332,7 +360,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
         if (c.more) {
             const int kl = 8 * wave + (own_lane() >> 3);
             if (c.t < 0) {                               // rows past the last repeat it
-                d.row = min(c.g * S::MB + (c.t + QT) * KT + kl, a.rows - 1);
+                d.row = min((own_group + c.g) * S::MB + (c.t + QT) * KT + kl, a.rows - 1);
                 d.kind = 1;
             } else {                                     // keys past the end repeat the last one: masked
                 const int k = max(0, min(c.tiles.at(c.t) * KT + kl, c.len - 1));
@@ -558,8 +586,10 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
         const int len = uniform_len(a, req);
         const Tiles span = tiles_of(a, len);
         const int tiles = span.count;
-        const int g = (int)((lo - base) / tiles), t0 = (int)((lo - base) % tiles);
-        const int t1 = (int)min((int64_t)tiles, t0 + (hi - lo));
+        const int places = tiles + a.lead, first = (int)((lo - base) % places);
+        const int g = own_group + (int)((lo - base) / places), taken = (int)min((int64_t)(places - first), hi - lo);
+        const int t0 = max(0, first - a.lead), t1 = first + taken - a.lead;
+        if (t1 <= 0) break;                                      // see Cursor
         // keys this lane's row sees: it is row (token, head) of the request; rows past the last repeat it
         const int limit = max(0, len - a.tokens + 1 + min(g * S::MB + wr * T::ROWS + row, a.rows - 1) / a.heads);
         int whole = max(0, len - a.tokens + 1) / KT;             // tiles before this: all rows see all of them
@@ -729,8 +759,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
         const int64_t qr = (int64_t)req * a.tokens + j;
         const bool uncut = t0 == 0 && t1 == tiles;
         if (t0 == 0 && tid == 0)
-            a.cuts[(int64_t)req * a.groups + g] = make_int2(
-                2 * blockIdx.x + (leading ? 0 : 1), uncut ? (int)blockIdx.x : run_of(line.total, grid, lo + tiles - 1));
+            a.cuts[(int64_t)req * a.all_groups + g] = make_int2(
+                2 * me + (leading ? 0 : 1), uncut ? me : run0 + run_of(line.total, grid, lo - first + places - 1));
         if (uncut) {
             if (r < a.rows) {                            // the lanes of a row are in this together
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // no key: zeros
@@ -759,7 +789,7 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
                 }
             }
         } else if (r < a.rows) {                         // no partials of rows that repeat the last
-            float *part = a.work + (2 * (int64_t)blockIdx.x + (leading ? 0 : 1)) * part_floats<S::MB>();
+            float *part = a.work + (2 * (int64_t)me + (leading ? 0 : 1)) * part_floats<S::MB>();
             f32x4_t *ps = reinterpret_cast<f32x4_t *>(part) + wave * (S::ND * S::NO4 * 64) + lane;
 #pragma unroll
             for (int i = 0; i < S::ND; ++i) {
@@ -776,8 +806,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
             }
         }
         leading = false;
-        lo += t1 - t0;
-        if (lo == base + (int64_t)tiles * a.groups) {
+        lo += taken;
+        if (lo == base + (int64_t)places * a.groups) {
             base = lo;
             ++req;
         }
@@ -807,7 +837,7 @@ __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(Dec
     const int2 cut = a.cuts[unit];
     const int b0 = cut.x >> 1, pieces = cut.y - b0 + 1;
     if (pieces <= 1) return;
-    const int req = unit / a.groups, g = unit % a.groups;
+    const int req = unit / a.all_groups, g = unit % a.all_groups;
 
     // at = (wave of the writer, 4-register group, its lane) in the partial's order; see the writer
     constexpr int PERW = S::ND * S::NO4;
@@ -875,7 +905,7 @@ __global__ __launch_bounds__(WP > 4 ? WP * 64 : 256) void latent_join_kernel(Dec
 template <typename T, int WR, int WD, int WP, int PL>
 hipError_t launch_join(const DecodeArgs &a, hipStream_t stream) {
     constexpr int PER = Shape<T, WR, WD>::MB * L / 4 / (64 / PL), QUADS = WP > 4 ? 1 : 4 / WP;
-    const unsigned blocks = (unsigned)((int64_t)a.batch * a.groups * (PER / QUADS));
+    const unsigned blocks = (unsigned)((int64_t)a.batch * a.all_groups * (PER / QUADS));
     hipLaunchKernelGGL((latent_join_kernel<T, WR, WD, WP, PL>), dim3(blocks), dim3(WP > 4 ? WP * 64 : 256), 0, stream, a);
     return hipGetLastError();
 }
@@ -883,17 +913,19 @@ hipError_t launch_join(const DecodeArgs &a, hipStream_t stream) {
 template <typename T, int WR, int WD, typename A>
 hipError_t launch_shape(A a, bool blocks, hipStream_t stream) {
     constexpr bool MASKED = std::is_same_v<A, MaskedArgs>;
+    // see shared_run: as many on each XCD
+    const unsigned workgroups = a.side > 1 ? (unsigned)((a.grid + 7) / 8 * 8) : (unsigned)a.grid;
     a.cuts = reinterpret_cast<int2 *>(a.work + 2 * a.grid * part_floats<Shape<T, WR, WD>::MB>());
     if (blocks)
-        hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, true>), dim3((unsigned)a.grid), dim3(THREADS), 0, stream, a);
+        hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, true>), dim3(workgroups), dim3(THREADS), 0, stream, a);
     else
-        hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, false>), dim3((unsigned)a.grid), dim3(THREADS), 0, stream, a);
+        hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, false>), dim3(workgroups), dim3(THREADS), 0, stream, a);
     hipError_t err = hipGetLastError();
     // one workgroup takes every run whole: nothing to join
     if (err != hipSuccess || a.grid == 1) return err;
     // takers of a unit's partials: about as many as it has on average, unless that makes more waves
     // than the chip holds at once (8 requests x 4000 keys x 128 heads 47 us with 16, 44 with 4)
-    const int64_t units = (int64_t)a.batch * a.groups, waves = units * (Shape<T, WR, WD>::MB * L / 4 / 64), room = 16384;
+    const int64_t units = (int64_t)a.batch * a.all_groups, waves = units * (Shape<T, WR, WD>::MB * L / 4 / 64), room = 16384;
     if (a.grid > 64 * units && waves * 64 <= room) return launch_join<T, WR, WD, 16, 4>(a, stream);
     if (a.grid > 16 * units && waves * 16 <= room) return launch_join<T, WR, WD, 16, 1>(a, stream);
     if (a.grid > 4 * units) return launch_join<T, WR, WD, 4, 1>(a, stream);
@@ -948,11 +980,18 @@ static DecodeArgs decode_args(const skinny_latent_decode_args &p, int cus) {
     reciprocal(a.page, a.page_mul, a.page_shift);
     reciprocal(a.heads, a.head_mul, a.head_shift);
     const int mb = block_rows(a.rows);
-    a.groups = (a.rows + mb - 1) / mb;
+    a.all_groups = (a.rows + mb - 1) / mb;
     a.c = p.scale * kLog2e;
     // no more workgroups than the line can have tiles
-    const int64_t most = (int64_t)a.batch * a.groups * std::max<int64_t>(1, (p.max_pages * p.page + KT - 1) / KT);
+    const int64_t most = (int64_t)a.batch * a.all_groups * std::max<int64_t>(1, (p.max_pages * p.page + KT - 1) / KT);
     a.grid = (int)std::min<int64_t>(cus, most);
+    // side by side where that leaves few CUs idle: at most an eighth
+    const bool shared = a.all_groups <= a.grid && a.grid % a.all_groups * 8 <= a.grid;
+    a.side = shared ? a.all_groups : 1;
+    a.groups = a.all_groups / a.side;
+    // with 0, 3, 6 and 8 places in us: 32 requests x 192 rows x 4096 keys 87, 84, 84, 84, 8 x 1024 x 8000 145, 142, 138,
+    // 138, 96 x 128 x 4000 126, 122, 119, 120; with 64 rows and 0, 2, 4, 6: 4 windows of 1000 15.2, 13.6, 13.1, 13.8
+    a.lead = p.batch * a.groups > 1 ? (mb == 128 ? 6 : mb == 64 ? 4 : 2) : 0;
     return a;
 }
 

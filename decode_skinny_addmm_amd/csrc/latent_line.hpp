@@ -2,7 +2,7 @@
 //
 // The key tiles of all requests, one request after the other (times `groups` for kernels that take a
 // request's rows in groups), form a line. Workgroups take equal runs of it, whatever the lengths.
-// An argument struct A names batch and groups, and request_tiles(a, i) the tiles of request i.
+// An argument struct A names batch and groups, and request_tiles(a, i) what request i takes of the line.
 #pragma once
 
 #include <climits>

@@ -116,6 +116,28 @@ def test_tree_decode_of_strided_rows(sk, heads, tokens):
     mref.check_decode(out, lse, q, cache, table, n, SCALE, tokens, seen, "far queries")
 
 
+@pytest.mark.parametrize("page", [16, 20])
+@pytest.mark.parametrize("heads,tokens", [(8, 17), (128, 3), (64, 9), (128, 7), (32, 44), (128, 13), (128, 20)])
+def test_decode_of_many_row_groups(sk, heads, tokens, page):
+    """2 to 20 groups of 128 rows, side by side where they divide the chip well and else behind each other, in few and
+    in many runs, with requests shorter than a tile and empty ones between."""
+    lens = [40, 0, tokens, 700, 3, 0, 0, 129]
+    print("groups", heads, tokens, page, flush=True)
+    g = gen(heads + tokens)
+    cache, table, n = paged(g, lens, page)
+    q = normal(g, len(lens) * tokens, heads, DIM)
+    out, lse = sk.latent_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), SCALE, tokens=tokens)
+    mref.check_decode(out, lse, q, cache, table, n, SCALE, tokens, lambda i, m: mref.seen_of(m, tokens), "groups")
+    window_case(sk, lens, heads, tokens, page, 90, 35, seed=1)
+
+
+@pytest.mark.parametrize("lens", [[1], [5000], [31, 4000, 32], [1] * 40, [0] * 9, [2000] * 20, [64, 0] * 60])
+@pytest.mark.parametrize("heads", [8, 24, 64, 100, 200])
+def test_decode_lines(sk, lens, heads):
+    """Runs that end and begin in the places ahead of a request, hold many requests, or a part of one."""
+    window_case(sk, lens, heads, 1, 16, 3000, 10, seed=heads)
+
+
 @pytest.mark.parametrize("batch", [511, 512, 513, 700])
 def test_masked_decode_of_many_requests(sk, batch):
     """Around what each wave counts by itself, with empty requests and such shorter than their new tokens."""
