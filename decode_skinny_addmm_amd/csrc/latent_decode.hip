@@ -19,12 +19,12 @@
 // With a window the line holds only the tiles that a request's rows see between them; with a tree of new tokens
 // the tiles that hold them are masked by the tokens' words, which lie in LDS (see seen_keys).
 // Measured: one request of 131071 keys x 32 heads 34 us (151 MB, 4.4 TB/s; its inner loop 6 TB/s) and 7
-// for the join; 96 requests of about 4000 keys x 128 heads 119 us (485 MB read, 92 MB of partials
+// for the join; 96 requests of about 4000 keys x 128 heads 119 us (484 MB read, 89 MB of partials
 // written) and 22 for the join; 64 requests of 3000 keys x 64 heads 55 us (240 MB read) and 7.6 for the
 // join; windows of 4096 of 64 requests x 16 heads 61 us (311 MB read, 5.1 TB/s) and 4.8; trees of 24 tokens x 8
 // heads over 32 requests of 4096 keys 84 and 14, of 64 x 16 over 8 of 8000 138 and 16; a tree of 7 x 8 over 500
-// keys 10 and 4. With 128 rows the matrix instructions take 40% of a wave's time (35% of the kernel's, with its
-// start and its uneven end), and neither they nor memory bound it alone: in this layout of one wave a
+// keys 10 and 4. With 128 rows the matrix instructions take 40% of a wave's time (36% of the kernel's, with its
+// start and end), and neither they nor memory bound it alone: in this layout of one wave a
 // SIMD, registers full of sums and queries leave no room to run a tile's softmax beside the next one's
 // products.
 #include <algorithm>
