@@ -117,10 +117,11 @@ def test_tree_decode_of_strided_rows(sk, heads, tokens):
 
 
 @pytest.mark.parametrize("page", [16, 20])
-@pytest.mark.parametrize("heads,tokens", [(8, 17), (128, 3), (64, 9), (128, 7), (32, 44), (128, 13), (128, 20)])
+@pytest.mark.parametrize("heads,tokens", [(8, 17), (128, 3), (64, 9), (128, 7), (32, 44), (128, 13), (128, 20),
+                                          (128, 37), (256, 22)])
 def test_decode_of_many_row_groups(sk, heads, tokens, page):
-    """2 to 20 groups of 128 rows, side by side where they divide the chip well and else behind each other, in few and
-    in many runs, with requests shorter than a tile and empty ones between."""
+    """2 to 44 groups of 128 rows, side by side where they divide the chip well and else (37 and 44 over 256 CUs) behind
+    each other, in few and in many runs, with requests shorter than a tile and empty ones between."""
     lens = [40, 0, tokens, 700, 3, 0, 0, 129]
     print("groups", heads, tokens, page, flush=True)
     g = gen(heads + tokens)
