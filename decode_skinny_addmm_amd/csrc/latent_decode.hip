@@ -196,7 +196,8 @@ struct Due {
 };
 // The same where a wave's 8 rows of keys lie in one page: all of it the same in all lanes.
 struct BlockDue {
-    int row, kind;                           // the wave's first row
+    int row;                                 // the wave's first row
+    int kind;                                // 0: none, 1: queries, 2 + r: keys, of which rows up to r are the request's
     int id;                                  // of its page
 };
 // Where an item's pieces come from (base and each lane's own bytes, or its address) and go to.
@@ -300,13 +301,13 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
     // it plans item n + LOOK + 1, whose id is there when the next step aims at it.
     constexpr int LOOK = S::FLOW ? 2 : 3;
     static_assert(LOOK <= QT + 1, "the items issued before the first step exist");
-    // Of the unit that is staged: its row of the table, its last block; of the next tile: the wave's first key.
+    // Of the unit that is staged: its row of the table, its last key; of the next tile: the wave's first key.
     typedef const __attribute__((address_space(4))) int32_t *constant_ptr;
     int64_t ids_row = 0;
-    int last_block = 0, next_key = 0, of_req = 0;
+    int last_key = 0, next_key = 0, of_req = 0;
     auto enter_block = [&]() __attribute__((always_inline)) {
         ids_row = c.req * a.t_row;
-        last_block = max(0, c.len - 1) & ~7;
+        last_key = max(0, c.len - 1);
         next_key = c.tiles.at(c.t0) * KT + 8 * wave;
         of_req = c.req;
     };
@@ -316,10 +317,10 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
         if (c.more) {
             bool same = false;                           // the next item is this unit's next tile of keys
             if (c.t >= 0) {                              // blocks past the end repeat the last one: masked
-                const int k = min(next_key, last_block);
+                const int k = min(next_key, last_key & ~7);
                 page = page_of(a, k);
                 d.row = k - page * a.page;
-                d.kind = 2;
+                d.kind = 2 + min(last_key - k, 7);
                 next_key += KT;
                 if (MASKED && c.t + 1 == c.tiles.head) next_key += c.tiles.skip * KT;
                 same = c.t + 1 < c.end;
@@ -336,13 +337,16 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
         return d;
     };
     auto aim_block = [&](const BlockDue &d, int slot) __attribute__((always_inline)) {
-        if (d.kind == 2) {                               // ids outside the pool are clamped
+        if (d.kind >= 2) {                               // ids outside the pool are clamped
             src.base = a.cache + (uint64_t)(uint32_t)min(max(d.id, 0), a.pages - 1) * (uint32_t)a.c_page +
                        (uint32_t)d.row * (uint32_t)a.c_row;
-            if (src.kind != 2) {
+            // Rows past the request's last repeat it: what the pool holds behind it, which may not be finite, would
+            // make the last tile go the way of add_values_carefully (64 requests x 33 keys x 64 heads: 16 us, and 28 with
+            // NaN there).
+            if (src.kind != d.kind) {
                 const int x = own_lane();
-                src.own = ((uint32_t)(x >> 3) * (uint32_t)a.c_row + chunk_of(x)) * 2;
-                src.kind = 2;
+                src.own = ((uint32_t)min(x >> 3, d.kind - 2) * (uint32_t)a.c_row + chunk_of(x)) * 2;
+                src.kind = d.kind;
             }
         } else {                                         // rows past the last repeat it
             const int x = own_lane();
