@@ -131,11 +131,15 @@ __device__ __forceinline__ uint32_t keys_below(int x, int k0) {
 // of 3000, 6000 and 12000 keys give 1.8 to 1.9 and 2.2 to 2.6, which moves the factors by 6% at most)
 // and w = 4.5 TB/s (128 heads: 32 requests x 1000 keys 57 -> 50 us, one of 10000 37 -> 34; 64 heads:
 // 2 x 3000 26 -> 25; of 16 and 32 rows the partials are too small to matter).
+// A line of so few tiles that this gives each a run of its own gives them with the places of no work, too, which are
+// `total`'s others (in us where pairs of tiles shared runs, and so: 8 requests x 40 keys x 64 heads 13.9 and 11.0, 3 x 80 x 128
+// heads 17.3 and 14.2).
 template <int MB>
-__device__ __forceinline__ int runs(int most, int64_t total) {
+__device__ __forceinline__ int runs(int most, int64_t total, int64_t tiles) {
     const int grid = (int)min((int64_t)most, total);
     if constexpr (MB < 64) return grid;
     constexpr float FACTOR = MB == 64 ? 5.4f : 4.5f;
+    if (tiles <= (int)(FACTOR * FACTOR)) return grid;
     return min(grid, max(1, (int)(FACTOR * sqrtf((float)total))));
 }
 
@@ -242,7 +246,8 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
 
     Line<decltype(a), THREADS> line;
     line.measure(a, (int64_t)a.batch * a.groups * (max(1, (a.max_pages * a.page + KT - 1) / KT) + a.lead), sh);
-    const int grid = uniform(max(1, runs<S::MB>(a.grid, line.total * a.side) / a.side));      // runs
+    const int grid = uniform(max(1, runs<S::MB>(a.grid, line.total * a.side,
+                                                (line.total - (int64_t)a.batch * a.groups * a.lead) * a.side) / a.side));
     const SharedRun mine = shared_run(blockIdx.x, grid, a.side);
     if (mine.run < 0) return;
     // me: the number of its partials
@@ -818,6 +823,13 @@ __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional
     }
 }
 
+// Workgroups that can have tiles: at most one a CU, and no more than the line can have of them (the places of no work
+// are not counted).
+int takers(const DecodeArgs &a, int most) {
+    const int64_t tiles = std::max<int64_t>(1, ((int64_t)a.max_pages * a.page + KT - 1) / KT);
+    return (int)std::min<int64_t>(most, (int64_t)a.batch * a.all_groups * tiles);
+}
+
 // Joins the partial sums of the units that were cut between workgroups. A wave's lanes are PL groups:
 // each takes the same 64 / PL float4 of a unit's sums, of every PL-th partial. WP waves share a
 // unit's partials further and meet in LDS; each lane asks for 4 partials at once. With few units the
@@ -930,9 +942,10 @@ hipError_t launch_shape(A a, bool blocks, hipStream_t stream) {
     // takers of a unit's partials: about as many as it has on average, unless that makes more waves
     // than the chip holds at once (8 requests x 4000 keys x 128 heads 47 us with 16, 44 with 4)
     const int64_t units = (int64_t)a.batch * a.all_groups, waves = units * (Shape<T, WR, WD>::MB * L / 4 / 64), room = 16384;
-    if (a.grid > 64 * units && waves * 64 <= room) return launch_join<T, WR, WD, 16, 4>(a, stream);
-    if (a.grid > 16 * units && waves * 16 <= room) return launch_join<T, WR, WD, 16, 1>(a, stream);
-    if (a.grid > 4 * units) return launch_join<T, WR, WD, 4, 1>(a, stream);
+    const int pieces = takers(a, a.grid);
+    if (pieces > 64 * units && waves * 64 <= room) return launch_join<T, WR, WD, 16, 4>(a, stream);
+    if (pieces > 16 * units && waves * 16 <= room) return launch_join<T, WR, WD, 16, 1>(a, stream);
+    if (pieces > 4 * units) return launch_join<T, WR, WD, 4, 1>(a, stream);
     return launch_join<T, WR, WD, 1, 1>(a, stream);
 }
 
@@ -986,16 +999,18 @@ static DecodeArgs decode_args(const skinny_latent_decode_args &p, int cus) {
     const int mb = block_rows(a.rows);
     a.all_groups = (a.rows + mb - 1) / mb;
     a.c = p.scale * kLog2e;
-    // no more workgroups than the line can have tiles
-    const int64_t most = (int64_t)a.batch * a.all_groups * std::max<int64_t>(1, (p.max_pages * p.page + KT - 1) / KT);
-    a.grid = (int)std::min<int64_t>(cus, most);
     // side by side where that leaves few CUs idle: at most an eighth
-    const bool shared = a.all_groups <= a.grid && a.grid % a.all_groups * 8 <= a.grid;
+    const int most = takers(a, cus);
+    const bool shared = a.all_groups <= most && most % a.all_groups * 8 <= most;
     a.side = shared ? a.all_groups : 1;
     a.groups = a.all_groups / a.side;
     // with 0, 3, 6 and 8 places in us: 32 requests x 192 rows x 4096 keys 87, 84, 84, 84, 8 x 1024 x 8000 145, 142, 138,
     // 138, 96 x 128 x 4000 126, 122, 119, 120; with 64 rows and 0, 2, 4, 6: 4 windows of 1000 15.2, 13.6, 13.1, 13.8
     a.lead = p.batch * a.groups > 1 ? (mb == 128 ? 6 : mb == 64 ? 4 : 2) : 0;
+    // No more workgroups than the line can have places, those of no work among them: with one for each tile alone, short
+    // lines left some workgroups with nothing and others with two tiles (2 requests x 40 keys x 64 heads 12.9 us, 10.2 so;
+    // 3 x 87 x 32 heads 9.9, 8.9).
+    a.grid = (int)std::min<int64_t>(cus, most + (int64_t)a.batch * a.all_groups * a.lead);
     return a;
 }
 

@@ -59,3 +59,19 @@ def test_rows_behind_the_end_cost_nothing(sk, heads):
     print("heads", heads, "finite", finite, "NaN behind the end", odd, flush=True)
     assert torch.equal(out, out_again) and torch.equal(lse, lse_again)
     assert odd < 1.15 * finite
+
+
+@pytest.mark.parametrize("heads,keys,batch,most", [(32, 40, 3, 1.1), (64, 40, 3, 1.1), (64, 40, 8, 1.2), (128, 80, 3, 1.15)])
+def test_a_few_short_requests_take_as_long_as_one(sk, heads, keys, batch, most):
+    """Each of their tiles has a workgroup of its own, as one request's have. (One request and these, in us: 8.8 and 8.9, 10.0 and
+    10.2, 10.0 and 11.0, 13.6 and 14.2; where tiles of a request shared one: 10.3, 12.9, 13.9 and 17.3.)"""
+    g = gen(heads)
+    cache, table, n = (t.cuda() for t in paged(g, [keys] * batch, 64))
+    q = normal(g, batch, heads, DIM).cuda()
+    one, out_one, lse_one = decode_call(sk, q[:1], cache, table[:1], n[:1])
+    all_, out, lse = decode_call(sk, q, cache, table, n)
+    alone, together = shortest(one, all_)
+    print("heads", heads, "alone", alone, "together", together, flush=True)
+    assert torch.equal(out[:1], out_one) and torch.equal(lse[:1], lse_one)
+    ref.check_decode(out, lse, q, cache, table, n, SCALE, 1, "short")
+    assert together < most * alone
