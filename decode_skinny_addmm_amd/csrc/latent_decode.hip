@@ -229,7 +229,9 @@ __device__ __forceinline__ void pieces_at(int at, int of, const Source &p) {
 // BLOCKS: pages are whole groups of 8 rows, so that the 8 keys that a wave stages of a tile lie in one page, whose
 // id and address are worked out once a wave, by the scalar unit. A step's cursor and addresses take the wave
 // some 970 cycles otherwise, and 775 so, of a tile of 128 rows' 4300 (8 requests of 8000 keys x 1024 rows: 157 and 148
-// us).
+// us). Not with 16 rows: their short tiles gain nothing, and where the caches hold the rows they lose, as reads of LDS then
+// wait for the page id's scalar load (64 requests of 2100 keys x 16 heads: 32 us by lanes, 34 by blocks; of 3000 40.5 and
+// 43.5; 32 heads the same either way).
 template <typename T, int WR, int WD, bool MASKED, bool BLOCKS>
 __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional_t<MASKED, MaskedArgs, DecodeArgs> a) {
     typedef Shape<T, WR, WD> S;
@@ -932,9 +934,14 @@ hipError_t launch_shape(A a, bool blocks, hipStream_t stream) {
     // see shared_run: as many on each XCD
     const unsigned workgroups = a.side > 1 ? (unsigned)((a.grid + 7) / 8 * 8) : (unsigned)a.grid;
     a.cuts = reinterpret_cast<int2 *>(a.work + 2 * a.grid * part_floats<Shape<T, WR, WD>::MB>());
-    if (blocks)
-        hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, true>), dim3(workgroups), dim3(THREADS), 0, stream, a);
-    else
+    bool launched = false;
+    if constexpr (Shape<T, WR, WD>::MB > 16) {
+        if (blocks) {
+            hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, true>), dim3(workgroups), dim3(THREADS), 0, stream, a);
+            launched = true;
+        }
+    }
+    if (!launched)
         hipLaunchKernelGGL((latent_decode_kernel<T, WR, WD, MASKED, false>), dim3(workgroups), dim3(THREADS), 0, stream, a);
     hipError_t err = hipGetLastError();
     // one workgroup takes every run whole: nothing to join
