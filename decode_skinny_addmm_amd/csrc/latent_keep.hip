@@ -82,10 +82,11 @@ struct SelectArgs {
 };
 
 // whole numbers that order as the weights do: a NaN above all, both zeros the same
+constexpr uint32_t ZERO = 0x80000000u;
 __device__ __forceinline__ uint32_t order_of(float w) {
     const uint32_t u = __float_as_uint(w);
     if (w != w) return ~0u;
-    if (w == 0.0f) return 0x80000000u;
+    if (w == 0.0f) return ZERO;
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
     __shared__ int sh[SELECT_WAVES], waves_kept[SELECT_WAVES], found[3], ranked;
     __shared__ uint2 near_border[RANKED];                // number, place
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), req = blockIdx.x;
-    const int n = min(max(a.lens[req], 0), a.columns);
+    const int n = min(max(a.lens[req], 0), 1 << 30);
     int32_t *kept = a.kept + (int64_t)req * a.budget;
     const int count = min(n, a.budget);
     if (tid == 0) a.counts[req] = count;
@@ -155,8 +156,10 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
         for (int i = tid; i < n; i += SELECT_THREADS) kept[i] = i;
         return;
     }
-    // of m keys between, want stay: 0 <= want < m
-    const int m = n - a.recent - a.sinks, want = a.budget - a.recent - a.sinks;
+    // Of m + bare keys between, want stay: 0 <= want < m + bare. The last `bare` have no column, and so the weight 0: they are
+    // counted, not read
+    const int between = n - a.recent - a.sinks, want = a.budget - a.recent - a.sinks;
+    const int m = max(0, min(between, a.columns - a.sinks)), bare = between - m;
     const int piece = (m + SELECT_THREADS - 1) / SELECT_THREADS * 64, i0 = min(m, wave * piece);
     const Keys keys(a.weights + req * a.w_row + a.sinks + i0, min(m, i0 + piece) - i0);
     auto clear = [&]() {
@@ -184,6 +187,7 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
         keys.each([&](int, uint32_t x) {
             if (first ? x != 0 : x - border <= ~known) atomicAdd(&bins[x >> shift & ((1u << bits) - 1)], 1);
         });
+        if (bare && tid == 0 && (first || ZERO - border <= ~known)) atomicAdd(&bins[ZERO >> shift & ((1u << bits) - 1)], bare);
         __syncthreads();
         // numbers in the bins above this thread's (threads count down from the topmost)
         int own[PER_BIN], sum = 0;
@@ -212,7 +216,9 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
 
     // The border: numbers above it stay, and of those equal to it the ones up to place `last`.
     int last = 0, mine = 0;                              // mine: the wave's that stay
-    if (same <= RANKED) {
+    int rest = 0;                                        // of the keys without a column, those that stay: the first ones
+    if (same <= RANKED && !(bare && ZERO - border <= ~known)) {
+        if (ZERO > border) rest = bare;
         keys.each([&](int i, uint32_t x) {
             const uint32_t over = x - border;            // numbers with these bits: 0 .. ~known
             mine += x > border && over > ~known;
@@ -261,6 +267,10 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
         if (lane == 0) waves_kept[wave] = equal;
         __syncthreads();
         const int first = before(waves_kept);            // of the equal ones, those of waves before
+        int columned = 0;                                // all of them that have a column
+#pragma unroll
+        for (int v = 0; v < SELECT_WAVES; ++v) columned += waves_kept[v];
+        if (ZERO >= border) rest = ZERO > border ? bare : max(0, still - columned);
         if (first < still && still <= first + equal) {   // the last that stays is one of this wave's
             int left = still - first;
             keys.each([&](int i, uint32_t x) {
@@ -273,9 +283,10 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
         }
         if (lane == 0) sh[wave] = mine + max(0, min(equal, still - first));
         __syncthreads();
-        last = found[1];
+        last = still > columned ? INT_MAX : found[1];
     }
     __syncthreads();
+    for (int i = tid; i < rest; i += SELECT_THREADS) kept[a.budget - a.recent - rest + i] = a.sinks + m + i;
     int at = a.sinks + before(sh);
     keys.each([&](int i, uint32_t x) {
         const bool stays = x > border || (x == border && i0 + i + lane <= last);

@@ -595,7 +595,7 @@ def latent_select(weights, lens, budget: int, sinks: int = 0, recent: int = 0, k
 
     weights float32 [batch, columns], lens int32 [batch]. Of more than `budget` keys the first `sinks`, the last
     `recent` and the largest weights between them stay (of equal ones the first; a NaN is larger than any
-    number); of fewer, all. Returns kept int32 [batch, budget], rising, -1 behind the last, and counts int32
+    number; a key without a column, as latent_key_weights leaves out, has the weight 0); of fewer, all. Returns kept int32 [batch, budget], rising, -1 behind the last, and counts int32
     [batch], for latent_keep."""
     gpu = _gpu_of("weights", weights)
     if weights.dim() != 2:

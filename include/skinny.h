@@ -473,8 +473,9 @@ SKINNY_API skinny_status skinny_latent_key_weights_bf16(const skinny_latent_key_
 /*
  * Select: which `budget` of request i's n = lens[i] keys stay: the first `sinks`, the last `recent`, and of those
  * between the ones with the largest weights[i, k] (of equal ones the lowest k; a NaN counts as larger than
- * any number, -0 as 0); all of them where n <= budget. kept[i] gets them in rising order, -1 behind them, counts[i]
- * their number. Lengths are clamped to 0 .. columns. SKINNY_EINVAL: sinks + recent > budget.
+ * any number, -0 as 0; a key without a column has the weight 0); all of them where n <= budget. kept[i] gets them in
+ * rising order, -1 behind them, counts[i] their number. Lengths are clamped to 0 .. 2^30. SKINNY_EINVAL: sinks + recent >
+ * budget.
  * SKINNY_ENOTSUP: budget, columns or batch above 2^30, 2^30, 2^20.
  */
 typedef struct skinny_latent_select_args {

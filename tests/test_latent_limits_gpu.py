@@ -75,3 +75,70 @@ def test_a_few_short_requests_take_as_long_as_one(sk, heads, keys, batch, most):
     assert torch.equal(out[:1], out_one) and torch.equal(lse[:1], lse_one)
     ref.check_decode(out, lse, q, cache, table, n, SCALE, 1, "short")
     assert together < most * alone
+
+
+# ---------------------------------------------------------------------------- fewer columns than keys
+
+def draws(g, n, kind):
+    """Weights: spread like sums of softmax weights, many zeros, or some negative."""
+    w = torch.exp(2 * torch.randn(n, generator=g))
+    if kind == "zeros":
+        w[torch.rand(n, generator=g) < 0.7] = 0.0
+    if kind == "signed":
+        w *= torch.where(torch.rand(n, generator=g) < 0.5, -1.0, 1.0)
+    return w
+
+
+@pytest.mark.parametrize("kind", ["spread", "zeros", "signed"])
+@pytest.mark.parametrize("columns,budget,sinks,recent", [(100, 40, 4, 8), (100, 150, 0, 0), (100, 99, 99, 0), (100, 120, 110, 10),
+                                                         (300, 290, 3, 280), (300, 299, 0, 0), (1, 10, 0, 0), (0, 7, 2, 3),
+                                                         (2000, 1900, 16, 64), (2000, 700, 0, 1)])
+def test_select_of_keys_without_a_column(sk, columns, budget, sinks, recent, kind):
+    """`recent` and the budget count from a request's true end, and keys without a column have the weight 0."""
+    g = gen(columns + budget)
+    lens = [0, 1, columns, columns + 1, columns + 37, budget, budget + 1, columns + budget, 5000, max(0, columns - 1)]
+    w = torch.stack([draws(g, columns, kind) for _ in lens]) if columns else torch.empty(len(lens), 0)
+    kept, counts = sk.latent_select(w.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), budget, sinks=sinks, recent=recent)
+    for i, n in enumerate(lens):
+        full = w[i].tolist()[:n] + [0.0] * (n - columns)
+        want = mref.select(full, n, budget, sinks, recent)
+        assert int(counts[i]) == len(want), (i, n)
+        assert kept[i].tolist() == want + [-1] * (budget - len(want)), (i, n)
+
+
+def test_select_of_keys_far_past_the_columns(sk):
+    """More columns than registers hold, and lengths that are cut to 2^30."""
+    g = gen(7)
+    w = torch.stack([draws(g, 70000, k) for k in ("spread", "zeros", "signed")])
+    lens = torch.tensor([70001, 2 ** 31 - 1, 200000], dtype=torch.int32)
+    kept, counts = sk.latent_select(w.cuda(), lens.cuda(), 60000, sinks=4, recent=100)
+    assert counts.tolist() == [60000] * 3
+    for i, n in enumerate((70001, 2 ** 30, 200000)):
+        near = min(n - 100, 140000)                              # keys behind it have the weight 0, and earlier ones too
+        full = w[i].tolist()[:near] + [0.0] * (near - 70000)
+        want = mref.select(full, near, 59900, 4, 0) + list(range(n - 100, n))
+        assert kept[i].tolist() == want, (i, n)
+
+
+def test_select_and_keep_with_fewer_columns_than_keys(sk):
+    """The newest rows stay, whatever the columns, and take the weight 0 along."""
+    g = gen(8)
+    lens, columns, budget, recent = [300, 90, 130, 0], 100, 64, 24
+    cache, table, n = paged(g, lens, 16)
+    q = normal(g, len(lens), 4, DIM)
+    got = cache.cuda()
+    _, lse = sk.latent_decode(q.cuda(), got, table.cuda(), n.cuda(), SCALE)
+    weights = sk.latent_key_weights(q.cuda(), got, table.cuda(), n.cuda(), lse, torch.zeros(len(lens), columns, device="cuda"), SCALE)
+    kept, counts = sk.latent_select(weights, n.cuda(), budget, sinks=4, recent=recent)
+    left, fewer = sk.latent_keep(got, table.cuda(), n.cuda(), kept, counts, weights=weights)
+    want = cache.clone()
+    for i, m in enumerate(lens):
+        full = weights[i].tolist()[:m] + [0.0] * (m - columns)
+        numbers = mref.select(full, m, budget, 4, recent)
+        mref.keep(want, table[i], m, numbers, 0)
+        assert int(left[i]) == len(numbers)
+        assert fewer[i].tolist() == [full[k] for k in numbers] + [0.0] * (columns - len(numbers)), i
+        rows = mref.keys_of(got.cpu(), table, left.cpu(), i)
+        newest = mref.keys_of(cache, table, n, i)[-recent:]
+        assert torch.equal(rows[-len(newest):], newest), i
+    assert torch.equal(got.cpu(), want)
