@@ -320,6 +320,40 @@ skinny_status hip_status(hipError_t err) {
     return SKINNY_EHIP;
 }
 
+// Lists of 4-byte numbers that a call is given: rows of `width` of them, `stride` apart.
+struct List {
+    const void *p;
+    int64_t rows, width, stride;
+    uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
+    bool empty() const { return !p || rows <= 0 || width <= 0; }
+    uintptr_t end() const { return begin() + ((uintptr_t)(rows - 1) * stride + width) * 4; }
+    // whether bytes lo .. hi - 1 touch a row
+    bool touched(uintptr_t lo, uintptr_t hi) const {
+        const uintptr_t wide = (uintptr_t)width * 4, step = (uintptr_t)stride * 4;
+        const uintptr_t i = lo < begin() + wide ? 0 : rows == 1 ? 1 : (lo - begin() - wide) / step + 1;
+        return i < (uintptr_t)rows && begin() + i * step < hi;
+    }
+};
+List list(const void *p, int64_t rows, int64_t width, int64_t stride) {
+    return rows > 1 && stride == width ? List{p, 1, rows * width, 0} : List{p, rows, width, rows > 1 ? stride : 0};
+}
+// Whether two of them share a number (rows that lie between each other's do not).
+bool share(const List &a, const List &b) {
+    if (a.empty() || b.empty() || a.end() <= b.begin() || b.end() <= a.begin()) return false;
+    const List &few = a.rows <= b.rows ? a : b, &many = a.rows <= b.rows ? b : a;
+    for (int64_t i = 0; i < few.rows; ++i) {
+        const uintptr_t lo = few.begin() + (uintptr_t)i * few.stride * 4;
+        if (many.touched(lo, lo + (uintptr_t)few.width * 4)) return true;
+    }
+    return false;
+}
+// A list that a call writes shares no number with the others: workgroups read those again behind its writes.
+bool apart(const List &written, std::initializer_list<List> others) {
+    for (const List &o : others)
+        if (share(written, o)) return false;
+    return true;
+}
+
 skinny_status run_latent_append(const skinny_latent_append_args *a, void *stream) {
     if (!a || a->n < 0 || a->heads < 0 || a->pages < 0 || a->page < 1 || !(a->eps >= 0.0f)) return SKINNY_EINVAL;
     if (a->latent != 512 || a->rope != 64) return SKINNY_ENOTSUP;
@@ -511,6 +545,13 @@ skinny_status run_latent_keep(const skinny_latent_keep_args *a, void *stream) {
     const void *words[] = {a->table, a->lens, a->kept, a->counts, a->new_lens, a->weights, a->new_weights};
     for (const void *p : words)
         if (!aligned(p, 4)) return SKINNY_EALIGN;
+    const List table = list(a->table, a->batch, a->max_pages, a->table_stride), lens = list(a->lens, a->batch, 1, 1),
+               kept = list(a->kept, a->batch, a->most, a->kept_stride), counts = list(a->counts, a->batch, 1, 1),
+               weights = list(a->weights, a->batch, a->columns, a->weights_stride),
+               fresh = list(a->new_weights, a->batch, a->columns, a->new_weights_stride);
+    if (!apart(list(a->new_lens, a->batch, 1, 1), {table, lens, kept, counts, weights, fresh}) ||
+        !apart(fresh, {table, lens, kept, counts, weights}))
+        return SKINNY_EINVAL;
     return hip_status(launch_latent_keep(*a, static_cast<hipStream_t>(stream)));
 }
 

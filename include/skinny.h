@@ -497,7 +497,9 @@ SKINNY_API skinny_status skinny_latent_select(const skinny_latent_select_args *a
  * in the list, or is not a row of the request, leaves the row of its new place as it is. counts are clamped to
  * 0 .. min(most, rows there are). weights and new_weights (NULL both, or two arrays): new_weights[i, j] = the weight
  * of the key that row j holds now, 0 behind the last. The pages that rows move in must be the request's own.
- * Rows behind the last one kept are left as they are. Lengths and page ids are clamped as in decode.
+ * Rows behind the last one kept are left as they are. Lengths and page ids are clamped as in decode. new_lens and
+ * new_weights share no number with each other or with what is read (else SKINNY_EINVAL), and the cache none with any
+ * of the lists (not checked).
  * SKINNY_ENOTSUP: other latents or rotated numbers than 512 and 64, a batch above 65535, counts as in decode.
  */
 typedef struct skinny_latent_keep_args {
@@ -506,7 +508,7 @@ typedef struct skinny_latent_keep_args {
     const int32_t *lens;            /* [batch] */
     const int32_t *kept;            /* [batch, most], rows kept_stride apart */
     const int32_t *counts;          /* [batch] */
-    int32_t *new_lens;              /* [batch], not lens */
+    int32_t *new_lens;              /* [batch] */
     const float *weights;           /* [batch, columns], rows weights_stride apart, or NULL */
     float *new_weights;             /* [batch, columns], rows new_weights_stride apart, or NULL */
     int64_t cache_page_stride, cache_row_stride, table_stride, kept_stride, weights_stride, new_weights_stride;

@@ -1,5 +1,6 @@
 """Latent attention at the limits of what its operands may hold, on the GPU: rows behind a request's end, few short
 requests, weights with fewer columns than keys, lengths and page ids that are clamped, strided operands."""
+import ctypes
 import math
 
 import pytest
@@ -141,4 +142,40 @@ def test_select_and_keep_with_fewer_columns_than_keys(sk):
         rows = mref.keys_of(got.cpu(), table, left.cpu(), i)
         newest = mref.keys_of(cache, table, n, i)[-recent:]
         assert torch.equal(rows[-len(newest):], newest), i
+    assert torch.equal(got.cpu(), want)
+
+
+# -------------------------------------------------------------------------------- lists that interleave
+
+def test_keep_takes_lists_between_each_other(sk):
+    """By the C entry: rows of weights and new weights, and the other lists, side by side in one array share no number."""
+    from decode_skinny_addmm_amd import _lib
+    g = gen(9)
+    lens, columns = [90, 40, 64], 90
+    cache, table, n = paged(g, lens, 16)
+    kept = [sorted(torch.randperm(m, generator=g)[:m * 2 // 3].tolist()) for m in lens]
+    most, pages = 60, table.shape[1]
+    wide = torch.zeros(3, 2 * columns + most + pages + 3, dtype=torch.int32)
+    w = torch.rand(3, columns, generator=g)
+    wide[:, :columns] = w.view(torch.int32)
+    for i, k in enumerate(kept):
+        wide[i, 2 * columns:2 * columns + len(k)] = torch.tensor(k, dtype=torch.int32)
+    wide[:, 2 * columns + most:2 * columns + most + pages] = table
+    wide[1, -3:] = n                                              # behind a row's lists, before the next row's
+    wide[0, -3:] = torch.tensor([len(k) for k in kept])
+    got, lists = cache.cuda(), wide.cuda()
+    at = lambda row, column: lists.data_ptr() + 4 * (row * wide.shape[1] + column)
+    end = wide.shape[1] - 3
+    args = _lib.SkinnyLatentKeepArgs(
+        cache=got.data_ptr(), table=at(0, 2 * columns + most), lens=at(1, end), kept=at(0, 2 * columns), counts=at(0, end),
+        new_lens=at(2, end), weights=at(0, 0), new_weights=at(0, columns), cache_page_stride=16 * DIM, cache_row_stride=DIM,
+        table_stride=wide.shape[1], kept_stride=wide.shape[1], weights_stride=wide.shape[1], new_weights_stride=wide.shape[1],
+        batch=3, tokens=0, most=most, pages=cache.shape[0], page=16, max_pages=pages, columns=columns, latent=512, rope=64)
+    assert _lib.lib().skinny_latent_keep_bf16(ctypes.byref(args), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    want, lists = cache.clone(), lists.cpu()
+    for i, m in enumerate(lens):
+        left, moved = mref.keep(want, table[i], m, kept[i], 0, w[i])
+        assert int(lists[2, end + i]) == left
+        assert torch.equal(lists[i, columns:2 * columns], moved.view(torch.int32)), i
     assert torch.equal(got.cpu(), want)
