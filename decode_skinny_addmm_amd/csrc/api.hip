@@ -502,6 +502,10 @@ skinny_status run_latent_key_weights(const skinny_latent_key_weights_args *a, vo
     if (!aligned(a->q, 16) || !aligned(a->cache, 16) || !aligned(a->table, 4) || !aligned(a->lens, 4) || !aligned(a->lse, 4) ||
         !aligned(a->weights, 4))
         return SKINNY_EALIGN;
+    if (!apart(list(a->weights, a->batch, a->columns, a->weights_stride),
+               {list(a->table, a->batch, a->max_pages, a->table_stride), list(a->lens, a->batch, 1, 1),
+                list(a->lse, rows, a->heads, a->heads)}))
+        return SKINNY_EINVAL;
     const int cus = device_cus();
     if (!cus) return SKINNY_EHIP;
     return hip_status(launch_latent_key_weights(*a, cus, static_cast<hipStream_t>(stream)));
@@ -515,6 +519,10 @@ skinny_status run_latent_select(const skinny_latent_select_args *a, void *stream
     if (a->batch > 1 && (a->weights_stride < a->columns || a->weights_stride > kMaxStride)) return SKINNY_EINVAL;
     if (!a->lens || !a->counts || (!a->weights && a->columns) || (!a->kept && a->budget)) return SKINNY_EINVAL;
     if (!aligned(a->weights, 4) || !aligned(a->lens, 4) || !aligned(a->kept, 4) || !aligned(a->counts, 4)) return SKINNY_EALIGN;
+    const List weights = list(a->weights, a->batch, a->columns, a->weights_stride), lens = list(a->lens, a->batch, 1, 1),
+               counts = list(a->counts, a->batch, 1, 1);
+    if (!apart(list(a->kept, a->batch, a->budget, a->budget), {weights, lens, counts}) || !apart(counts, {weights, lens}))
+        return SKINNY_EINVAL;
     return hip_status(launch_latent_select(*a, static_cast<hipStream_t>(stream)));
 }
 
@@ -562,6 +570,9 @@ skinny_status run_latent_tree_mask(const int32_t *parents, int32_t *mask, int32_
     if (batch == 0 || tokens == 0) return SKINNY_OK;
     if (!parents || !mask || !depth) return SKINNY_EINVAL;
     if (!aligned(parents, 4) || !aligned(mask, 4) || !aligned(depth, 4)) return SKINNY_EALIGN;
+    const List from = list(parents, batch, tokens, tokens), to = list(depth, batch, tokens, tokens);
+    if (!apart(list(mask, batch * tokens, (tokens + 31) / 32, (tokens + 31) / 32), {from, to}) || !apart(to, {from}))
+        return SKINNY_EINVAL;
     return hip_status(launch_latent_tree_mask(parents, mask, depth, batch, tokens, static_cast<hipStream_t>(stream)));
 }
 

@@ -436,7 +436,8 @@ SKINNY_API skinny_status skinny_latent_masked_decode_bf16(const skinny_latent_de
 
 /* The rows of trees given by their parents: parents [batch, tokens], each an earlier token of the same request
  * (any other number: the token follows the context); mask [batch, tokens, (tokens + 31) / 32] gets each token's
- * own bit and those of the tokens above it, depth [batch, tokens] their number. All contiguous. */
+ * own bit and those of the tokens above it, depth [batch, tokens] their number. All contiguous; none overlaps
+ * another (else SKINNY_EINVAL). */
 SKINNY_API skinny_status skinny_latent_tree_mask(const int32_t *parents, int32_t *mask, int32_t *depth, int64_t batch,
                                                  int64_t tokens, void *stream);
 
@@ -454,7 +455,8 @@ SKINNY_API skinny_status skinny_latent_window_prefill_workspace(int64_t nq, int6
  * Key weights: weights[i, k] += sum over the rows (token j, head h) of request i that see key k
  * (k <= lens[i] - tokens + j) of exp(scale * q . cache_k - lse[row]), for the keys k < lens[i] that have a column:
  * what a decode call with the same arguments gave each key, added up. Keys and requests as in decode. The order of
- * the sums is fixed. Other places of weights are left as they are. Refusals as in decode.
+ * the sums is fixed. Other places of weights are left as they are. weights share no number with table, lens or lse (else
+ * SKINNY_EINVAL), nor with q or the cache (not checked). Other refusals as in decode.
  */
 typedef struct skinny_latent_key_weights_args {
     const void *q;                  /* [batch * tokens, heads, 576] */
@@ -475,7 +477,7 @@ SKINNY_API skinny_status skinny_latent_key_weights_bf16(const skinny_latent_key_
  * between the ones with the largest weights[i, k] (of equal ones the lowest k; a NaN counts as larger than
  * any number, -0 as 0; a key without a column has the weight 0); all of them where n <= budget. kept[i] gets them in
  * rising order, -1 behind them, counts[i] their number. Lengths are clamped to 0 .. 2^30. SKINNY_EINVAL: sinks + recent >
- * budget.
+ * budget, or kept or counts that share a number with another list.
  * SKINNY_ENOTSUP: budget, columns or batch above 2^30, 2^30, 2^20.
  */
 typedef struct skinny_latent_select_args {
