@@ -179,3 +179,94 @@ def test_keep_takes_lists_between_each_other(sk):
         assert int(lists[2, end + i]) == left
         assert torch.equal(lists[i, columns:2 * columns], moved.view(torch.int32)), i
     assert torch.equal(got.cpu(), want)
+
+
+# ---------------------------------------------------------------------- what is clamped, and strides
+
+def clamped(g):
+    """Lengths outside of 0 .. 48 and page ids outside of the pool of 10, of requests whose pages are their own."""
+    lens = torch.tensor([41, 49, 2 ** 31 - 1, -5, -2 ** 31, 48], dtype=torch.int32)
+    table = torch.tensor([[-3, 1, 2], [3, 4, 2 ** 30], [5, 6, 7], [8, 8, 8], [-1, -1, -1], [-2 ** 31, 1, 2 ** 31 - 1]], dtype=torch.int32)
+    return normal(g, 10, 16, DIM), table, lens
+
+
+@pytest.mark.parametrize("heads,tokens", [(2, 3), (8, 4), (16, 4), (32, 5)])
+def test_masked_decode_clamps(sk, heads, tokens):
+    g = gen(heads)
+    cache, table, n = clamped(g)
+    q = normal(g, len(n) * tokens, heads, DIM)
+    parents = [[j - 1 if j % 3 else -1 for j in range(tokens)]] * len(n)
+    above, depth = mref.ancestors(parents[0])
+    mask, _ = sk.latent_tree_mask(torch.tensor(parents, dtype=torch.int32, device="cuda"))
+    out, lse = sk.latent_tree_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), mask, SCALE)
+    mref.check_decode(out, lse, q, cache, table, n, SCALE, tokens, lambda i, m: mref.seen_of(m, tokens, above=above), "tree")
+    # depths are clamped to 0 .. tokens - 1 (those that the words do not speak of stand where they are told)
+    far = torch.tensor([[-7 if j % 2 else 2 ** 31 - 1 for j in range(tokens)]] * len(n), dtype=torch.int32)
+    out, lse = sk.latent_tree_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), mask, SCALE, window=11, sinks=2, depth=far.cuda())
+    near = far[0].clamp(0, tokens - 1)
+    mref.check_decode(out, lse, q, cache, table, n, SCALE, tokens, lambda i, m: mref.seen_of(m, tokens, 11, 2, above, near), "window")
+    out, lse = sk.latent_window_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), SCALE, 9, sinks=1, tokens=tokens)
+    mref.check_decode(out, lse, q, cache, table, n, SCALE, tokens, lambda i, m: mref.seen_of(m, tokens, 9, 1), "chain")
+
+
+@pytest.mark.parametrize("heads,tokens", [(2, 1), (16, 3), (64, 4)])
+def test_key_weights_clamp(sk, heads, tokens):
+    g = gen(heads)
+    cache, table, n = clamped(g)
+    q = normal(g, len(n) * tokens, heads, DIM)
+    _, lse = sk.latent_decode(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), SCALE, tokens=tokens)
+    before = torch.rand(len(n), 60, generator=g)
+    got = sk.latent_key_weights(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), lse, before.cuda(), SCALE, tokens=tokens)
+    mref.check_weights(got, before, q, cache, table, n, lse, SCALE, tokens, "clamped")
+
+
+@pytest.mark.parametrize("tokens", [0, 20])
+def test_keep_clamps(sk, tokens):
+    g = gen(10)
+    cache, table, n = clamped(g)
+    table, n = table[:5], n[:5]                                  # the last request shares pages with others
+    kept = torch.tensor([sorted(torch.randperm(tokens or 48, generator=g)[:12].tolist()) for _ in n], dtype=torch.int32)
+    counts = torch.tensor([2 ** 31 - 1, 12, 5, 7, -2 ** 31], dtype=torch.int32)
+    weights = torch.rand(5, 60, generator=g)
+    got = cache.cuda()
+    left, fresh = sk.latent_keep(got, table.cuda(), n.cuda(), kept.cuda(), counts.cuda(), tokens=tokens, weights=weights.cuda())
+    want = cache.clone()
+    for i in range(5):
+        m = max(0, min(int(n[i]), 48))
+        length, moved = mref.keep(want, table[i], m, kept[i, :max(0, min(int(counts[i]), 12))].tolist(), tokens, weights[i])
+        assert int(left[i]) == length, i
+        assert torch.equal(fresh[i].cpu(), moved), i
+    assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("heads,tokens", [(2, 3), (16, 2), (40, 4)])
+def test_key_weights_of_strided_rows(sk, heads, tokens):
+    """A cache whose rows and pages lie apart, queries that are a slice; then pages, rows and queries that lie so far apart that
+    their offsets pass 31 and 32 bits."""
+    g = gen(heads)
+    lens, rows = [333, tokens, 90], 3 * tokens
+    cache, table, n = paged(g, lens, 16)
+    q = normal(g, rows, heads, DIM)
+    before = torch.rand(3, 340, generator=g)
+
+    def check(queries, pool, order, n, small, what):
+        _, lse = sk.latent_decode(q.cuda(), small.cuda(), order.cuda(), n.cuda(), SCALE, tokens=tokens)
+        got = sk.latent_key_weights(queries, pool, order.cuda(), n.cuda(), lse, before.cuda(), SCALE, tokens=tokens)
+        mref.check_weights(got, before, q, small, order, n, lse, SCALE, tokens, what)
+
+    apart = torch.full((cache.shape[0], 17, DIM + 16), math.nan, dtype=BF, device="cuda")[:, :16, :DIM]
+    apart.copy_(cache)
+    queries = torch.full((rows, heads + 1, DIM + 8), math.nan, dtype=BF, device="cuda")[:, 1:, :DIM]
+    queries.copy_(q)
+    check(queries, apart, table, n, cache, "strided")
+    few, order = normal(g, 3, 16, DIM), torch.tensor([[2, 0, 1]] * 3, dtype=torch.int32)
+    short = torch.tensor([48, tokens, 20 + tokens], dtype=torch.int32)
+    for step, row in (((1 << 29) + 8, DIM), ((1 << 31) + 64, DIM + 8), (DIM + 8, (1 << 25) + 8)):
+        far = torch.empty(2 * step + 15 * row + DIM, dtype=BF, device="cuda").as_strided((3, 16, DIM), (step, row, 1))
+        far.copy_(few)
+        check(queries, far, order, short, few, "far")
+        del far
+    step = (1 << 31) // (rows - 1) + 8 - (1 << 31) // (rows - 1) % 8
+    far = torch.empty((rows - 1) * step + heads * DIM, dtype=BF, device="cuda").as_strided((rows, heads, DIM), (step, DIM, 1))
+    far.copy_(q)
+    check(far, apart, table, n, cache, "far queries")
