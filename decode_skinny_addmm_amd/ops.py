@@ -582,7 +582,9 @@ def latent_key_weights(q, cache, table, lens, lse, weights, scale: float, tokens
 
     q, cache, table, lens, scale, tokens as in latent_decode, lse float32 [batch * tokens, heads] as it returned:
     weights float32 [batch, columns] (rows may lie apart) gets at [i, k] the sum over request i's rows
-    that see key k of exp(scale * q . key - lse). Keys without a column are left out. With `tokens` the last ones
+    that see key k of exp(scale * q . key - lse). Keys without a column are left out. The rows are a chain that sees all
+    keys up to its own, `tokens` of every request: lse of latent_tree_decode or latent_window_decode gives no softmax
+    weights here (take that of a latent_decode call of the rows that were accepted). With `tokens` the last ones
     of a prompt it tells which of the prompt's keys they look at. Returns weights."""
     gpu = _gpu_of("q", q)
     _call(_latent().key_weights, "skinny_latent_key_weights_bf16", gpu, stream, q, cache, table, lens, lse, weights, scale,

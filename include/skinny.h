@@ -454,8 +454,10 @@ SKINNY_API skinny_status skinny_latent_window_prefill_workspace(int64_t nq, int6
 /*
  * Key weights: weights[i, k] += sum over the rows (token j, head h) of request i that see key k
  * (k <= lens[i] - tokens + j) of exp(scale * q . cache_k - lse[row]), for the keys k < lens[i] that have a column:
- * what a decode call with the same arguments gave each key, added up. Keys and requests as in decode. The order of
- * the sums is fixed. Other places of weights are left as they are. weights share no number with table, lens or lse (else
+ * what a decode call with the same arguments gave each key, added up. Keys and requests as in decode. Every request has
+ * `tokens` rows, a chain that sees all keys up to its own: with the log sums of a masked call (of a tree, of a window) the
+ * terms are no softmax weights, since keys that those rows did not see are counted all the same, and a row's may add up to more
+ * than 1. The order of the sums is fixed. Other places of weights are left as they are. weights share no number with table, lens or lse (else
  * SKINNY_EINVAL), nor with q or the cache (not checked). Other refusals as in decode.
  */
 typedef struct skinny_latent_key_weights_args {
