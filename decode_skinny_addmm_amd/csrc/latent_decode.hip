@@ -147,7 +147,10 @@ __device__ __forceinline__ int runs(int most, int64_t total, int64_t tiles) {
 // the line but side by side: the line holds a request's tiles once, and each of its runs is taken by `side`
 // workgroups, one a group, at the same time and on one XCD, whose L2 serves all but the first. (Workgroups go to
 // the XCDs in turn.) 8 groups read 90 MB where it was 575, 2 groups 162 where it was 330, which takes them from 91 to
-// 88 us; 8 groups as long as before.
+// 88 us; 8 groups as long as before. Runs are counted in whole `side`s, which costs 2 or 3 groups of a short request
+// most. One request, in us behind each other and side by side: 2 groups x 640 keys 18.9 and 20.7, x 4000 26.6 and 27.3;
+// 8 x 1000 25.5 and 26.2, x 4000 37.2 and 36.8; 29 x 96 23.6 and 17.6, x 4000 65.6 and 62.8; 60 x 256 38.9 and 30.2, x 4000
+// 95.6 and 94.5; 128 x 96 28.2 and 21.6, x 4000 152 and 150. 16 requests of 5 groups x 1000 56.4 and 52.4, of 28 164 and 159.
 struct SharedRun {
     int run, own;                            // the run, the row group (of those side by side); run -1: none
 };
@@ -1006,7 +1009,7 @@ static DecodeArgs decode_args(const skinny_latent_decode_args &p, int cus) {
     const int mb = block_rows(a.rows);
     a.all_groups = (a.rows + mb - 1) / mb;
     a.c = p.scale * kLog2e;
-    // side by side where that leaves few CUs idle: at most an eighth
+    // side by side where that leaves few CUs idle: at most an eighth (29 groups 24 of 256; see shared_run)
     const int most = takers(a, cus);
     const bool shared = a.all_groups <= most && most % a.all_groups * 8 <= most;
     a.side = shared ? a.all_groups : 1;

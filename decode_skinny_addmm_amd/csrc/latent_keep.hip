@@ -383,7 +383,7 @@ __global__ __launch_bounds__(THREADS) void latent_keep_kernel(KeepArgs a) {
         for (int u = 0; u < KEEP_TURNS; ++u) {
             const int j = u * (THREADS / LANES) + tid / LANES;
             x[u] = u32x4_t{0, 0, 0, 0};
-            if (j0 + j < k.count && to[j] >= 0) 
+            if (j0 + j < k.count && to[j] >= 0)
                 x[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(piece + from[j]));
         }
         in_vgpr(x);                                      // all are there
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(THREADS) void latent_keep_kernel(KeepArgs a) {
 #pragma unroll
         for (int u = 0; u < KEEP_TURNS; ++u) {
             const int j = u * (THREADS / LANES) + tid / LANES;
-            if (j0 + j < k.count && to[j] >= 0) 
+            if (j0 + j < k.count && to[j] >= 0)
                 __builtin_nontemporal_store(x[u], reinterpret_cast<u32x4_t *>(piece + to[j]));
         }
         __syncthreads();                                 // from and to are read

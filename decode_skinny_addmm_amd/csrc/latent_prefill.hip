@@ -626,7 +626,7 @@ __global__ __launch_bounds__(WIDE_THREADS) void latent_prefill_wide_kernel(A a) 
         for (int x = 0; x < NP / 8; ++x) {
             u32x4_t see;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) 
+            for (int j = 0; j < 8; j += 2)
                 see[j / 2] = seen_pair(left.sees<WINDOW>(place0(8 * x + j)), left.sees<WINDOW>(place0(8 * x + j + 1)));
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
@@ -743,9 +743,10 @@ struct Plan {
     int splits;
 };
 // With a window a wide workgroup takes 128 more keys that only half of its rows see, and the narrow form leaves
-// out a wave's tiles that none of its rows sees, so that longer windows are needed (16384 tokens x 16 heads, wide
-// and narrow in us: windows of 1024 265 and 228, of 2048 424 and 432, of 4096 738 and 801; 2 x 6000 tokens x 5
-// heads, window 2500 115 and 117). keys: those that a workgroup takes, on average.
+// out a wave's tiles that none of its rows sees, so that longer windows are needed. Wide and narrow in us, for windows of
+// 1024, 2048, 2560 and 4096: 16384 tokens x 16 heads 256 and 236, 366 and 378, 430 and 438, 606 and 618; 4 x 3900 x 8 116 and
+// 109, 162 and 149, 184 and 185, 201 and 200; 4 chunks of 300 after 6000 keys x 32 61 and 56, 88 and 87, 100 and 103, 149 and
+// 156; 2 x 6000 x 5 heads 64 and 65, 86 and 94, 99 and 107, 135 and 152. keys: those that a workgroup takes, on average.
 Plan plan(int64_t nq, int64_t keys, int64_t batch, int64_t heads, bool window, int cus) {
     Plan p;
     p.wide = nq / batch >= 192 && keys >= (window ? 2560 : 1024);
