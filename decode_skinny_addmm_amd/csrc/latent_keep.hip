@@ -302,10 +302,11 @@ __global__ __launch_bounds__(SELECT_THREADS) void latent_select_kernel(SelectArg
 // all rows before it writes one. Places rise and no row lies before its place, so what a chunk writes no
 // later one reads. Pieces of 384 bytes, and 512 rows a chunk (196 KB on its way a workgroup), where there are
 // requests enough to fill the chip with them; otherwise 128 bytes and 2048 rows, 262 KB, half of a CU's registers
-// (64 requests, of 4096 kept rows each 123 and 127 us, of 500 12.2 and 14.9; 16 requests 63 and 31, 6.8 and 5.5;
-// with 1024 rows a chunk 4 requests of 2048 10.8 us where it is 9.0). Many requests the bytes bound, which are not
-// read again soon (past the caches: 94 us where it was 100; 64 requests of which most drop some 110 of 4200 rows 86
-// us, 390 MB read and written, 4.5 TB/s), few of them the chain of a chunk's loads: list, page ids, rows, stores.
+// (one call after another: 64 requests, of 4096 of 4200 rows each 118 and 122 us, of 500 of 1000 12.7 and 15.7; 16 requests 63
+// and 31, 7.5 and 5.7; with 1024 rows a chunk 4 requests of 2048 of 32768 11.2 us where it is 10.6). Many requests the bytes
+// bound, which are not read again soon (past the caches: 94 us where it was 100; 64 requests of which most drop some 110 of 4200
+// rows 86 us, 390 MB read and written, 4.5 TB/s), few of them the chain of a chunk's loads: list, page ids, rows, stores
+// (13 us where the rows come from memory).
 constexpr int DIM = 576;
 constexpr int KEEP_TURNS = 16;               // rows that a lane has on their way
 constexpr int KEEP_WEIGHTS = 2048;           // weights a workgroup
@@ -450,7 +451,7 @@ hipError_t launch_latent_keep(const skinny_latent_keep_args &p, hipStream_t stre
     a.columns = (int)p.columns;
     reciprocal(a.page, a.page_mul, a.page_shift);
     const int64_t wblocks = a.new_weights ? (p.columns + KEEP_WEIGHTS - 1) / KEEP_WEIGHTS : 0;
-    // few rows a request, as of a tree's path: few workgroups (64 requests of 5 rows 5.1 and 3.9 us)
+    // few rows a request, as of a tree's path: few workgroups (64 requests of 5 rows 3.9 us, 8.0 otherwise)
     if (p.batch >= 64 || p.most <= 64)
         hipLaunchKernelGGL((latent_keep_kernel<24, 768>), dim3((unsigned)(DIM / 8 / 24 + wblocks), (unsigned)p.batch),
                            dim3(768), 0, stream, a);
