@@ -21,7 +21,7 @@
 // Measured: one request of 131071 keys x 32 heads 34 us (151 MB, 4.4 TB/s; its inner loop 6 TB/s) and 7
 // for the join; 96 requests of about 4000 keys x 128 heads 119 us (484 MB read, 89 MB of partials
 // written) and 22 for the join; 64 requests of 3000 keys x 64 heads 55 us (240 MB read) and 7.6 for the
-// join; windows of 4096 of 64 requests x 16 heads 61 us (311 MB read, 5.1 TB/s) and 4.8; trees of 24 tokens x 8
+// join; windows of 4096 of 64 requests x 16 heads 59 us (311 MB read, 5.3 TB/s) and 4.8; trees of 24 tokens x 8
 // heads over 32 requests of 4096 keys 84 and 14, of 64 x 16 over 8 of 8000 138 and 16; a tree of 7 x 8 over 500
 // keys 10 and 4. With 128 rows the matrix instructions take 40% of a wave's time (36% of the kernel's, with its
 // start and end), and neither they nor memory bound it alone: in this layout of one wave a
@@ -232,8 +232,8 @@ __device__ __forceinline__ void pieces_at(int at, int of, const Source &p) {
 // BLOCKS: pages are whole groups of 8 rows, so that the 8 keys that a wave stages of a tile lie in one page, whose
 // id and address are worked out once a wave, by the scalar unit. A step's cursor and addresses take the wave
 // some 970 cycles otherwise, and 775 so, of a tile of 128 rows' 4300 (8 requests of 8000 keys x 1024 rows: 157 and 148
-// us). Not with 16 rows: their short tiles gain nothing, and where the caches hold the rows they lose, as reads of LDS then
-// wait for the page id's scalar load (64 requests of 2100 keys x 16 heads: 32 us by lanes, 34 by blocks; of 3000 40.5 and
+// us). Not with 16 rows: their short tiles gain nothing, and where the caches hold the rows they lose (reads of LDS wait
+// for the page id's scalar load with them, which may be why; 64 requests of 2100 keys x 16 heads: 32 us by lanes, 34 by blocks; of 3000 40.5 and
 // 43.5; 32 heads the same either way).
 template <typename T, int WR, int WD, bool MASKED, bool BLOCKS>
 __global__ __launch_bounds__(THREADS) void latent_decode_kernel(std::conditional_t<MASKED, MaskedArgs, DecodeArgs> a) {
